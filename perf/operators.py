@@ -6,7 +6,7 @@ Three operators, on matrices held as e4m3 codes with one power-of-two scale
   encode  W [M, N] -> codes [M, N] (e4m3) and scales: one for each block of
           128 x 128 (weights) or of 1 x 128 (activations, row by row)
   matmul  Y = X8 . W8^T, W8 an encoded weight, X8 the rows of X encoded by
-          blocks of 1 x 128 on the way in; Y float32
+          blocks of 1 x 128 on the way in; Y float32, bfloat16 or binary16
   moe     a mixture-of-experts layer for a few tokens: router, softmax, the
           top k of E experts, SwiGLU experts on encoded weights, their
           weighted sum; Y float32, the chosen experts and their weights
@@ -35,22 +35,22 @@ def _ceil(a, b):
 
 def listed():
     return [
-        # a small projection, encoded once while a model is loaded
-        {"name": "encode_w_attn", "op": "encode", "M": 4096, "N": 4096, "rows": 128, "dt": "bf16"},
-        # the largest linear of the benchmark, beyond the last-level cache
+        # the largest linear of the benchmark, encoded once while a model is loaded, beyond the last-level cache
         {"name": "encode_w_mlp_70b", "op": "encode", "M": 28672, "N": 8192, "rows": 128, "dt": "bf16"},
         # activations of a prompt, row by row, an odd number of tokens and of columns
         {"name": "encode_rows_odd", "op": "encode", "M": 517, "N": 4001, "rows": 1, "dt": "f32"},
         # a small linear at one token: latency alone
-        {"name": "mm_256x512_b1", "op": "matmul", "M": 256, "N": 512, "b": 1, "dt": "f32"},
+        {"name": "mm_256x512_b1", "op": "matmul", "M": 256, "N": 512, "b": 1, "dt": "f32", "y": "f32"},
         # one decode step of an attention projection
-        {"name": "mm_attn_b1", "op": "matmul", "M": 4096, "N": 4096, "b": 1, "dt": "bf16"},
+        {"name": "mm_attn_b1", "op": "matmul", "M": 4096, "N": 4096, "b": 1, "dt": "bf16", "y": "bf16"},
         # a batch of decode tokens through the up projection of an MLP
-        {"name": "mm_up_b16", "op": "matmul", "M": 11008, "N": 4096, "b": 16, "dt": "bf16"},
+        {"name": "mm_up_b16", "op": "matmul", "M": 11008, "N": 4096, "b": 16, "dt": "bf16", "y": "bf16"},
         # a short prompt, nothing a multiple of anything
-        {"name": "mm_odd_b77", "op": "matmul", "M": 4099, "N": 5003, "b": 77, "dt": "f16"},
+        {"name": "mm_odd_b77", "op": "matmul", "M": 4099, "N": 5003, "b": 77, "dt": "f16", "y": "f16"},
+        # a prompt through the up projection, summed and returned in float32
+        {"name": "mm_up_b512_f32", "op": "matmul", "M": 11008, "N": 4096, "b": 512, "dt": "bf16", "y": "f32"},
         # the benchmark's prefill product
-        {"name": "mm_mlp_70b_prefill", "op": "matmul", "M": 28672, "N": 8192, "b": 2048, "dt": "bf16"},
+        {"name": "mm_mlp_70b_prefill", "op": "matmul", "M": 28672, "N": 8192, "b": 2048, "dt": "bf16", "y": "bf16"},
         # a toy layer at one token: latency alone
         {"name": "moe_small_t1", "op": "moe", "H": 512, "I": 256, "E": 8, "k": 2, "T": 1, "norm": True, "dt": "f32"},
         # one decode token through a layer of large experts
@@ -74,7 +74,8 @@ def draw(rng):
     if op == "encode":
         return {"op": op, "M": _log(rng, 1, 28672), "N": _log(rng, 64, 8192), "rows": rng.choice([1, 128]), "dt": dt}
     if op == "matmul":
-        return {"op": op, "M": _log(rng, 64, 28672), "N": _log(rng, 64, 8192), "b": _log(rng, 1, 2048), "dt": dt}
+        return {"op": op, "M": _log(rng, 64, 28672), "N": _log(rng, 64, 8192), "b": _log(rng, 1, 2048), "dt": dt,
+                "y": rng.choice(["f32", dt])}
     E = rng.choice([4, 8, 8, 16, 32, 64, 128])
     H = _log(rng, 256, 4096)
     I = min(_log(rng, 128, 11008), 8 * 4096 * 11008 // (E * H))
@@ -197,13 +198,13 @@ def run(st):
             t = sk.fp8_encode(st["x"], block_rows=st["rows"], check=False)
             return t.codes(), t.scales()
         if op == "matmul":
-            return sk.fp8_matmul(st["w"], st["x"])
+            return sk.fp8_matmul(st["w"], st["x"], dtype=DT[st["y"]])
         return sk.moe(st["layer"], st["x"], return_routing=True)
     if op == "encode":
         return _encode(st["x"], st["rows"])
     if op == "matmul":
         x = _decode(*_encode(st["x"], 1), 1)
-        return x @ _decode(*st["w"], 128).t()
+        return (x @ _decode(*st["w"], 128).t()).to(DT[st["y"]])
     return _moe(st)
 
 
@@ -215,7 +216,7 @@ def work(case):
     if case["op"] == "matmul":
         M, N, b = case["M"], case["N"], case["b"]
         w = M * N + _ceil(M, B) * _ceil(N, B)
-        return {"bytes": w + b * N * ES[case["dt"]] + 4 * b * M, "flops": 2 * b * M * N}
+        return {"bytes": w + b * N * ES[case["dt"]] + b * M * ES[case["y"]], "flops": 2 * b * M * N}
     H, I, E, k, T = (case[n] for n in ("H", "I", "E", "k", "T"))
     active = E * (1.0 - (1.0 - k / E) ** T)            # experts some token takes, routed evenly
     expert = 3 * H * I + 2 * _ceil(I, B) * _ceil(H, B) + _ceil(H, B) * _ceil(I, B)
