@@ -1,0 +1,69 @@
+// fp8.h -- internal definitions of the e4m3 linears (fp8.hip) and of the
+// mixture-of-experts layer that reads them (moe.hip).
+#pragma once
+
+#include "../../include/sketch_fp8.h"
+#include "common.h"
+
+namespace sketch {
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kFp8Block = 128;   // columns of a block
+
+// Checks the parameters and fills the layout (the rules of sketch_fp8_layout).
+sketch_status fp8_shape(const sketch_fp8_params* p, sketch_fp8_shape* s);
+
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// Compute units of the current device (256 when none answers).
+inline int compute_units() {
+    int dev = 0, ncu = 0;
+    if (hipGetDevice(&dev) != hipSuccess ||
+        hipDeviceGetAttribute(&ncu, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || ncu <= 0)
+        ncu = 256;
+    return ncu;
+}
+
+// Scale byte of a block from the bits of its largest magnitude.  With
+// amax = m 2^p, 1 <= m < 2, the smallest e with amax <= 448 2^e = 1.75 2^(e+8)
+// is p - 8, or p - 7 when m > 1.75.  NaN and infinities give 255.
+__device__ inline uint32_t fp8_scale_byte(uint32_t amax_bits) {
+    const uint32_t ex = amax_bits >> 23;
+    if (ex == 255u) return 255u;
+    const int b = int(ex) - 8 + ((amax_bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+    return b < 0 ? 0u : uint32_t(b);
+}
+
+// 2^(127 - byte), the factor that takes an element to its code's range
+// (byte <= 247; the exponent field is 254 - byte >= 7).
+__device__ inline float fp8_inv_scale(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
+
+// Four floats -> four e4m3 codes, ties to even.
+__device__ inline uint32_t fp8_pack4(float a, float b, float c, float d) {
+    int v = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+    v = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, v, true);
+    return uint32_t(v);
+}
+
+// 2^(byte - 127); 255, the NaN scale, gives infinity, and its codes are NaN.
+__device__ inline float fp8_scale(uint32_t byte) { return __uint_as_float(byte << 23); }
+
+// 8 codes (two dwords) -> 8 bfloat16 values times a power of two (exact).
+__device__ inline bf16x8 fp8_widen(uint32_t lo, uint32_t hi, float scale) {
+    const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, false);
+    const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, true);
+    const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, false);
+    const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, true);
+    return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+sketch_status launch_fp8_encode(const sketch_fp8_params* p, const sketch_fp8_shape& s, const void* W,
+                                sketch_dtype dt, void* buf, int32_t* status, hipStream_t st);
+
+}  // namespace sketch

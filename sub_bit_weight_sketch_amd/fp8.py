@@ -1,0 +1,302 @@
+"""Binding of the 8-bit floating-point linears and of the mixture-of-experts
+layer (``include/sketch_fp8.h``).
+
+Argument marshalling only, as in the rest of the package: ``sketch_fp8_layout``,
+``sketch_fp8_encode``, ``sketch_fp8_workspace_bytes``, ``sketch_fp8_matmul``,
+``sketch_moe_workspace_bytes`` and ``sketch_moe`` have the names of the C ABI;
+the rest is a convenience layer over them.
+"""
+import contextlib
+import ctypes
+
+import torch
+
+from . import OK, SketchError, _check, _ptr, _stream_handle, dtype_code, lib, sketch_encode_status
+
+FP8_ROWS = 3                # x_dtype of rows that sketch_fp8_encode wrote
+MOE_MAX_EXPERTS, MOE_MAX_TOPK, MOE_MAX_TOKENS = 512, 16, 64
+FP8_EXPORTS = ("sketch_fp8_layout", "sketch_fp8_encode", "sketch_fp8_workspace_bytes", "sketch_fp8_matmul",
+               "sketch_moe_workspace_bytes", "sketch_moe")
+
+
+class Fp8Params(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("N", ctypes.c_int64), ("block_rows", ctypes.c_int32),
+                ("count", ctypes.c_int32)]
+
+
+class Fp8Shape(ctypes.Structure):
+    _fields_ = [("ld", ctypes.c_int64), ("row_blocks", ctypes.c_int64), ("col_blocks", ctypes.c_int64),
+                ("lds", ctypes.c_int64), ("scales_offset", ctypes.c_size_t), ("bytes", ctypes.c_size_t)]
+
+
+class MoEParams(ctypes.Structure):
+    _fields_ = [("H", ctypes.c_int64), ("I", ctypes.c_int64), ("E", ctypes.c_int32), ("topk", ctypes.c_int32),
+                ("renorm", ctypes.c_int32), ("x_dtype", ctypes.c_int)]
+
+
+_declared = None
+
+
+def _fp8_lib():
+    global _declared
+    if _declared is None:
+        L = lib()
+        P, Q = ctypes.POINTER(Fp8Params), ctypes.POINTER(MoEParams)
+        vp, i64, sz, it = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int
+        L.sketch_fp8_layout.argtypes = [P, ctypes.POINTER(Fp8Shape)]
+        L.sketch_fp8_encode.argtypes = [P, vp, it, vp, vp, vp]
+        L.sketch_fp8_workspace_bytes.argtypes = [P, i64, it, ctypes.POINTER(sz)]
+        L.sketch_fp8_matmul.argtypes = [P, vp, vp, it, i64, vp, it, vp, sz, vp]
+        L.sketch_moe_workspace_bytes.argtypes = [Q, i64, ctypes.POINTER(sz)]
+        L.sketch_moe.argtypes = [Q, vp, vp, vp, vp, vp, i64, vp, vp, vp, vp, sz, vp]
+        for name in FP8_EXPORTS:
+            getattr(L, name).restype = it
+        _declared = L
+    return _declared
+
+
+# ---------------------------------------------------------------------------
+# thin wrappers of the C ABI (same names)
+# ---------------------------------------------------------------------------
+
+def sketch_fp8_layout(p):
+    s = Fp8Shape()
+    _check(_fp8_lib().sketch_fp8_layout(ctypes.byref(p), ctypes.byref(s)), "sketch_fp8_layout")
+    return s
+
+
+def sketch_fp8_encode(p, W, buf, status=None, stream=None):
+    """status: an int32 device tensor the kernel ORs flags into, or None."""
+    stream = stream if stream is not None else _stream_handle(W.device)
+    _check(_fp8_lib().sketch_fp8_encode(ctypes.byref(p), _ptr(W), dtype_code(W), _ptr(buf), _ptr(status), stream),
+           "sketch_fp8_encode")
+
+
+def sketch_fp8_workspace_bytes(p, batch, x_dtype):
+    n = ctypes.c_size_t()
+    _check(_fp8_lib().sketch_fp8_workspace_bytes(ctypes.byref(p), int(batch), int(x_dtype), ctypes.byref(n)),
+           "sketch_fp8_workspace_bytes")
+    return n.value
+
+
+def sketch_fp8_matmul(p, buf, X, x_dtype, batch, Y, workspace, stream=None):
+    stream = stream if stream is not None else _stream_handle(Y.device)
+    wsb = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _check(_fp8_lib().sketch_fp8_matmul(ctypes.byref(p), _ptr(buf), _ptr(X), int(x_dtype), int(batch), _ptr(Y),
+                                        dtype_code(Y), _ptr(workspace), wsb, stream), "sketch_fp8_matmul")
+
+
+def sketch_moe_workspace_bytes(p, tokens):
+    n = ctypes.c_size_t()
+    _check(_fp8_lib().sketch_moe_workspace_bytes(ctypes.byref(p), int(tokens), ctypes.byref(n)),
+           "sketch_moe_workspace_bytes")
+    return n.value
+
+
+def sketch_moe(p, router, gate, up, down, X, Y, ids, weights, workspace, stream=None):
+    stream = stream if stream is not None else _stream_handle(X.device)
+    wsb = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _check(_fp8_lib().sketch_moe(ctypes.byref(p), _ptr(router), _ptr(gate), _ptr(up), _ptr(down), _ptr(X), X.shape[0],
+                                 _ptr(Y), _ptr(ids), _ptr(weights), _ptr(workspace), wsb, stream), "sketch_moe")
+
+
+# ---------------------------------------------------------------------------
+# high-level API
+# ---------------------------------------------------------------------------
+
+def _on(device):
+    """The device made current for the call (launches go to the current device)."""
+    if torch.cuda.current_device() == device.index:
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def _need(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def _aligned(t):
+    """t itself when dense and 16-byte aligned, else a copy that is."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
+class Fp8Tables:
+    """A matrix [M, N] (or a stack [count, M, N]) as e4m3 codes and block
+    scales, in the buffer layout of the C ABI (a uint8 device tensor)."""
+
+    def __init__(self, M, N, block_rows=128, count=None, device="cuda", buf=None):
+        _need(count is None or count > 0, "an empty stack of matrices")
+        self.M, self.N, self.block_rows, self.count = int(M), int(N), int(block_rows), count
+        self.params = Fp8Params(self.M, self.N, self.block_rows, 1 if count is None else int(count))
+        self.layout = sketch_fp8_layout(self.params)
+        n = (1 if count is None else int(count)) * self.layout.bytes
+        if buf is None:
+            buf = torch.empty(n, dtype=torch.uint8, device=device)
+        _need(buf.dtype == torch.uint8 and buf.is_contiguous() and buf.numel() >= n and buf.data_ptr() % 16 == 0,
+              "the buffer must be %d dense, 16-byte aligned bytes" % n)
+        self.buf = buf
+        self._ws = {}
+
+    @property
+    def shape(self):
+        return ((self.M, self.N) if self.count is None else (self.count, self.M, self.N))
+
+    @property
+    def device(self):
+        return self.buf.device
+
+    def _view(self, rows, cols, ld, at):
+        if self.count is None:
+            return self.buf.as_strided((rows, cols), (ld, 1), self.buf.storage_offset() + at)
+        return self.buf.as_strided((self.count, rows, cols), (self.layout.bytes, ld, 1), self.buf.storage_offset() + at)
+
+    def codes(self):
+        """The codes as a float8_e4m3fn view (rows are padded: not contiguous unless N % 128 == 0)."""
+        return self._view(self.M, self.N, self.layout.ld, 0).view(torch.float8_e4m3fn)
+
+    def scales(self):
+        """The biased scale exponents, uint8 [row blocks, column blocks] (a view): scale = 2^(byte - 127)."""
+        s = self.layout
+        return self._view(s.row_blocks, s.col_blocks, s.lds, s.scales_offset)
+
+
+def fp8_encode(W, block_rows=128, check=True, status=None):
+    """Encode W [M, N], or a stack [count, M, N] of matrices, float32,
+    bfloat16 or float16 on a GPU, in blocks of 128 x 128 (weights) or, with
+    block_rows=1, of 1 x 128 (activations).
+
+    With check=True the call waits for the device and raises SketchError when
+    an element is NaN or infinite; with check=False it stays asynchronous (such
+    a block encodes to NaN) and ORs flags into `status`, an int32 device tensor
+    of one element, when given."""
+    if W.dim() not in (2, 3) or not W.is_cuda:
+        raise ValueError("W must be a 2-D GPU tensor, or a 3-D one for a stack of matrices")
+    dtype_code(W)
+    W = _aligned(W)
+    t = Fp8Tables(W.shape[-2], W.shape[-1], block_rows, W.shape[0] if W.dim() == 3 else None, W.device)
+    with _on(W.device):
+        if check and status is None:
+            status = torch.zeros(1, dtype=torch.int32, device=W.device)
+        sketch_fp8_encode(t.params, W, t.buf, status)
+        if check:
+            flags = int(status.item())
+            rc = sketch_encode_status(flags)
+            if rc != OK:
+                raise SketchError(rc, "sketch_fp8_encode (device flags 0x%x)" % flags)
+    return t
+
+
+def fp8_tables(codes, scales, block_rows=128):
+    """Fp8Tables from codes [M, N] (float8_e4m3fn, or their uint8 bits) and
+    biased scale exponents [row blocks, column blocks] (float8_e8m0fnu, or
+    uint8), or stacks of both: a copy into the library's layout."""
+    codes, scales = codes.view(torch.uint8), scales.view(torch.uint8)
+    _need(codes.dim() in (2, 3) and codes.is_cuda and scales.device == codes.device,
+          "codes and scales must be 2-D (or 3-D) tensors on one GPU")
+    count = codes.shape[0] if codes.dim() == 3 else None
+    t = Fp8Tables(codes.shape[-2], codes.shape[-1], block_rows, count, codes.device)
+    want = (t.layout.row_blocks, t.layout.col_blocks)
+    _need(tuple(scales.shape) == (want if count is None else (count,) + want), "scales must have shape %s" % (want,))
+    t.buf.zero_()
+    t._view(t.M, t.N, t.layout.ld, 0).copy_(codes)
+    t.scales().copy_(scales)
+    return t
+
+
+def fp8_workspace_for(t, batch, x_dtype, device):
+    """Workspace for products of `batch` rows (None if not needed).  Reuse it
+    across calls on one stream, never for two calls in flight at once."""
+    key = (batch, x_dtype)
+    n = t._ws.get(key)
+    if n is None:
+        n = t._ws[key] = sketch_fp8_workspace_bytes(t.params, batch, x_dtype)
+    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+
+
+def _out(out, shape, dtype, device):
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _need(tuple(out.shape) == tuple(shape) and out.dtype == dtype and out.is_contiguous() and out.device == device,
+          "out must be a dense %s tensor %s on the same device" % (dtype, tuple(shape)))
+    return out
+
+
+def fp8_matmul(t, X, out=None, workspace=None, dtype=None):
+    """Y = X8 . W8^T [batch, M] for an encoded weight t and X [batch, N] (or
+    [N]), encoded row by row on the way in; X may also be an Fp8Tables with
+    block_rows=1, for rows that several linears share.  dtype: of Y, float32
+    (the default, or that of `out`), bfloat16 or float16; see
+    include/sketch_fp8.h for how the sums of large batches differ."""
+    dtype = dtype or (out.dtype if out is not None else torch.float32)
+    _need(t.block_rows == 128 and t.count is None, "t must be one weight, encoded with block_rows=128")
+    rows = isinstance(X, Fp8Tables)
+    if rows:
+        _need(X.block_rows == 1 and X.count is None, "encoded rows must have block_rows=1")
+    squeeze = not rows and X.dim() == 1
+    if squeeze:
+        X = X[None, :]
+    _need(X.device == t.device, "X and the weight are on different devices")
+    if len(X.shape) != 2 or X.shape[1] != t.N:
+        raise ValueError("X must have %d columns, got shape %s" % (t.N, tuple(X.shape)))
+    batch = X.shape[0]
+    xdt = FP8_ROWS if rows else dtype_code(X)
+    x = X.buf if rows else _aligned(X)
+    with _on(t.device):
+        Y = _out(out[None, :] if squeeze and out is not None and out.dim() == 1 else out, (batch, t.M), dtype, t.device)
+        if workspace is None:
+            workspace = fp8_workspace_for(t, batch, xdt, t.device)
+        sketch_fp8_matmul(t.params, t.buf, x, xdt, batch, Y, workspace)
+    return Y[0] if squeeze else Y
+
+
+class MoE:
+    """A mixture-of-experts layer: router [E, H] (float32, bfloat16 or
+    float16, the dtype its tokens have) and the experts' weights, stacks of E
+    encoded matrices: gate and up [E, I, H], down [E, H, I].  renorm: whether
+    the weights of the chosen experts are scaled to sum to one."""
+
+    def __init__(self, router, gate, up, down, topk, renorm=True):
+        _need(router.dim() == 2 and router.is_cuda, "router must be a 2-D GPU tensor")
+        E, H = router.shape
+        for name, t in (("gate", gate), ("up", up), ("down", down)):
+            _need(isinstance(t, Fp8Tables) and t.block_rows == 128 and t.count == E and t.device == router.device,
+                  "%s must be a stack of %d weights, encoded with block_rows=128, on the router's device" % (name, E))
+        I = gate.M
+        _need(gate.shape == up.shape == (E, I, H) and down.shape == (E, H, I),
+              "gate and up must be [E, I, H], down [E, H, I], the router [E, H]")
+        self.router, self.gate, self.up, self.down = _aligned(router), gate, up, down
+        self.topk, self.renorm = int(topk), bool(renorm)
+        self.params = MoEParams(H, I, E, self.topk, int(self.renorm), dtype_code(router))
+        sketch_moe_workspace_bytes(self.params, 0)   # checks the sizes
+        self._ws = {}
+
+    def workspace_for(self, tokens):
+        """Workspace for `tokens` tokens.  Reuse it across calls on one
+        stream, never for two calls in flight at once."""
+        n = self._ws.get(tokens)
+        if n is None:
+            n = self._ws[tokens] = sketch_moe_workspace_bytes(self.params, tokens)
+        return torch.empty(max(n, 16), dtype=torch.uint8, device=self.router.device)
+
+
+def moe(layer, X, out=None, workspace=None, return_routing=False):
+    """Y float32 [tokens, H] of a MoE layer for X [tokens, H] (up to
+    MOE_MAX_TOKENS tokens, of the router's dtype); with return_routing also
+    the chosen experts int32 [tokens, topk], by descending logit, and their
+    weights float32 [tokens, topk]."""
+    p = layer.params
+    _need(X.dim() == 2 and X.shape[1] == p.H, "X must be [tokens, %d]" % p.H)
+    _need(X.dtype == layer.router.dtype and X.device == layer.router.device,
+          "X must have the router's dtype and device")
+    X = _aligned(X)
+    T, dev = X.shape[0], X.device
+    with _on(dev):
+        Y = _out(out, (T, p.H), torch.float32, dev)
+        ids = torch.empty((T, p.topk), dtype=torch.int32, device=dev)
+        weights = torch.empty((T, p.topk), dtype=torch.float32, device=dev)
+        if workspace is None:
+            workspace = layer.workspace_for(T)
+        sketch_moe(p, layer.router, layer.gate.buf, layer.up.buf, layer.down.buf, X, Y, ids, weights, workspace)
+    return (Y, ids, weights) if return_routing else Y

@@ -1,0 +1,217 @@
+"""The mixture-of-experts layer on the GPU against the plain 64-bit form."""
+import numpy as np
+import pytest
+import torch
+
+import fp8_util as u
+from gpu_util import dev
+
+sk = pytest.importorskip("sub_bit_weight_sketch_amd")
+
+pytestmark = pytest.mark.gpu
+
+DT = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+
+
+def make(H, I, E, k, dt, seed, renorm=True):
+    g = torch.Generator().manual_seed(seed)
+    rn = lambda *s: torch.randn(*s, generator=g)
+    router = (rn(E, H) * 1.5 / H ** 0.5).to(DT[dt])
+    gate, up = (sk.fp8_encode((rn(E, I, H) / H ** 0.5).to(dev())) for _ in range(2))
+    down = sk.fp8_encode((rn(E, H, I) / I ** 0.5).to(dev()))
+    return sk.MoE(router.to(dev()), gate, up, down, k, renorm)
+
+
+def plain(layer, X):
+    p = layer.params
+    return u.moe(u.to64(X), u.to64(layer.router), u.table_values(layer.gate), u.table_values(layer.up),
+                 u.table_values(layer.down), p.topk, bool(p.renorm))
+
+
+def check(layer, X, what=""):
+    """Experts equal; weights within a few roundings (one to float32, the sums
+    in float64); y within six times sqrt(n) * 2^-24 of its row's size, n = H + I
+    the terms of the two sums an output goes through (each a float32 random
+    walk), plus 16 roundings for silu, the split and the weighted sum."""
+    Y, ids, w = sk.moe(layer, X, return_routing=True)
+    y, i, wr = plain(layer, X)
+    assert np.array_equal(ids.cpu().numpy(), i), what
+    assert np.abs(u.to64(w) / wr - 1).max() <= 2 * u.EPS32, what
+    size = np.sqrt((y ** 2).mean(axis=1, keepdims=True))
+    err = (np.abs(u.to64(Y) - y) / size).max()
+    n = layer.params.H + layer.params.I
+    assert err <= (6 * np.sqrt(n) + 16) * u.EPS32, (what, err)
+    return Y
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("H,I,E,k,T,renorm", [(1, 1, 1, 1, 1, True), (64, 32, 4, 2, 3, True), (128, 128, 8, 8, 2, False),
+                                              (257, 129, 8, 2, 16, True), (512, 256, 64, 6, 7, False),
+                                              (130, 700, 16, 4, 33, True), (1000, 333, 5, 3, 64, False),
+                                              (256, 128, 512, 16, 5, True), (300, 64, 3, 1, 64, True)])
+def test_layer(H, I, E, k, T, renorm, dt):
+    layer = make(H, I, E, k, dt, H + I + E, renorm)
+    X = torch.randn(T, H, generator=torch.Generator().manual_seed(T)).to(DT[dt]).to(dev())
+    check(layer, X)
+
+
+@pytest.mark.parametrize("T", [1, 2, 16, 17, 40, 64])
+def test_all_tokens_at_one_expert(T):
+    """More tokens at one expert than a matrix-core tile has columns."""
+    layer = make(256, 192, 4, 1, "bf16", 3)
+    layer.router[2] = 1.0
+    X = (torch.rand(T, 256, generator=torch.Generator().manual_seed(1)) + 0.5).to(torch.bfloat16).to(dev())
+    assert (sk.moe(layer, X, return_routing=True)[1] == 2).all()
+    check(layer, X)
+
+
+def test_each_index_path():
+    """Gate, up and down pick single entries, so that every output is one known
+    term: y[t][i] = sum_e w_e silu(x[a]) x[b], with a, b known from (e, i).
+    Wrong rows, columns, experts or scales would each show up whole."""
+    H, I, E, k, T = 384, 300, 6, 3, 20
+    g = np.random.default_rng(0)
+    pa, pb, pd = (g.integers(0, n, (E, m)) for n, m in ((H, I), (H, I), (I, H)))
+    gate, up, down = np.zeros((E, I, H), np.float32), np.zeros((E, I, H), np.float32), np.zeros((E, H, I), np.float32)
+    for e in range(E):
+        gate[e, np.arange(I), pa[e]] = 2.0 ** (np.arange(I) // 128)
+        up[e, np.arange(I), pb[e]] = 2.0 ** e
+        down[e, np.arange(H), pd[e]] = 2.0 ** (-(np.arange(H) // 128) - e)
+    enc = lambda a: sk.fp8_encode(torch.from_numpy(a).to(dev()))
+    router = torch.from_numpy(g.standard_normal((E, H)).astype(np.float32)).to(dev())
+    layer = sk.MoE(router, enc(gate), enc(up), enc(down), k)
+    x = g.standard_normal((T, H)).astype(np.float32) * 0.5
+    Y, ids, w = (u.to64(v) for v in sk.moe(layer, torch.from_numpy(x).to(dev()), return_routing=True))
+    x = x.astype(np.float64)
+    y, size = np.zeros((T, H)), np.zeros((T, H))
+    for t in range(T):
+        for s in range(k):
+            e = int(ids[t, s])
+            gv = x[t, pa[e]] * 2.0 ** (np.arange(I) // 128)
+            h = gv / (1 + np.exp(-gv)) * x[t, pb[e]] * 2.0 ** e
+            term = w[t, s] * h[pd[e]] * 2.0 ** (-(np.arange(H) // 128) - e)
+            y[t] += term
+            size[t] += np.abs(term)
+    # roundings: exp (2 steps), 1 + exp, the division, h, w, w * h and k sums: 8 + k steps of 2^-23
+    assert (np.abs(Y - y) <= (8 + k) * 2 * u.EPS32 * size).all()
+
+
+def test_ties_take_the_lower_expert():
+    layer = make(128, 64, 16, 5, "bf16", 4)
+    layer.router[:] = layer.router[:1].clone()          # all logits equal
+    X = torch.randn(3, 128, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16).to(dev())
+    _, ids, w = sk.moe(layer, X, return_routing=True)
+    assert (ids.cpu() == torch.arange(5, dtype=torch.int32)).all()
+    assert np.abs(u.to64(w) - 0.2).max() <= 0.2 * 2 * u.EPS32
+    layer.router[:] = 0                                  # +0 and -0 are equal
+    layer.router[::2] = -0.0
+    assert (sk.moe(layer, X, return_routing=True)[1].cpu() == torch.arange(5, dtype=torch.int32)).all()
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_non_finite_tokens_stay_in_their_row(bad, dt):
+    layer = make(256, 128, 8, 2, dt, 6)
+    X = torch.randn(5, 256, generator=torch.Generator().manual_seed(3)).to(DT[dt]).to(dev())
+    Y = sk.moe(layer, X)
+    Z = X.clone()
+    Z[2, 17] = bad
+    Yz, ids, _ = sk.moe(layer, Z, return_routing=True)
+    keep = torch.tensor([0, 1, 3, 4], device=dev())
+    assert not torch.isfinite(Yz[2]).any()
+    assert torch.isfinite(Yz[keep]).all() and (Yz[keep] - Y[keep]).abs().max() <= 1e-5 * Y.abs().max()
+    assert ((ids >= 0) & (ids < 8)).all() and int(ids[2, 0]) != int(ids[2, 1])
+
+
+def test_repeats_are_identical_and_streams_do_not_mix():
+    layer = make(512, 384, 8, 2, "bf16", 7)
+    g = torch.Generator().manual_seed(4)
+    Xs = [torch.randn(11, 512, generator=g).to(torch.bfloat16).to(dev()) for _ in range(4)]
+    ref = [sk.moe(layer, X) for X in Xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in Xs]
+    for _ in range(3):
+        outs = []
+        for X, s in zip(Xs, streams):
+            with torch.cuda.stream(s):
+                outs.append(sk.moe(layer, X))
+        torch.cuda.synchronize()
+        for a, b in zip(outs, ref):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("T", [1, 9, 40])
+def test_captured_and_replayed(T):
+    """One workspace, two graphs and eager calls in turn."""
+    layer = make(300, 200, 8, 2, "f16", 8)
+    g = torch.Generator().manual_seed(5)
+    Xs = [torch.randn(T, 300, generator=g).to(torch.float16).to(dev()) for _ in range(3)]
+    ref = [sk.moe(layer, X) for X in Xs]
+    ws = layer.workspace_for(T)
+    graphs = []
+    for _ in range(2):
+        x, Y = Xs[0].clone(), torch.empty(T, 300, device=dev())
+        sk.moe(layer, x, out=Y, workspace=ws)
+        torch.cuda.synchronize()
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            sk.moe(layer, x, out=Y, workspace=ws)
+        graphs.append((gr, x, Y))
+    for i in (0, 1, 2, 1):
+        for gr, x, Y in graphs:
+            x.copy_(Xs[i])
+            Y.fill_(float("nan"))
+            gr.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(Y, ref[i])
+            assert torch.equal(sk.moe(layer, Xs[i]), ref[i])
+
+
+def test_refusals():
+    layer = make(128, 64, 8, 2, "bf16", 9)
+    X = torch.zeros(4, 128, dtype=torch.bfloat16, device=dev())
+    for bad in (X[:, :100], X.float(), X.cpu(), X[0]):
+        with pytest.raises(ValueError):
+            sk.moe(layer, bad)
+    with pytest.raises(sk.SketchError):
+        sk.moe(layer, torch.zeros(65, 128, dtype=torch.bfloat16, device=dev()))
+    assert sk.moe(layer, X[:0]).shape == (0, 128)
+    with pytest.raises(ValueError):
+        sk.MoE(layer.router, layer.gate, layer.up, layer.gate, 2)
+    with pytest.raises(sk.SketchError):
+        sk.MoE(layer.router, layer.gate, layer.up, layer.down, 9)
+    with pytest.raises(sk.SketchError):
+        sk.moe(layer, X, workspace=torch.empty(256, dtype=torch.uint8, device=dev()))
+
+
+def test_a_block_of_a_model():
+    """The operators as a model runs them: a sketched projection, an 8-bit one
+    and the layer of experts, on the same tokens, in one captured step."""
+    H, T = 256, 6
+    g = torch.Generator().manual_seed(10)
+    W = torch.randn(H, H, generator=g) * 0.06
+    sketched = sk.encode(W.to(torch.bfloat16).to(dev()), bpw=4.0)
+    fp8 = sk.fp8_encode(W.to(dev()))
+    layer = make(H, 384, 8, 2, "f32", 11)
+    x = torch.randn(T, H, generator=g).to(dev())
+    sk.matmul(sketched, x), sk.fp8_matmul(fp8, x), sk.moe(layer, x)
+
+    def step():
+        a = sk.matmul(sketched, x)
+        b = sk.fp8_matmul(fp8, a)
+        return a, b, sk.moe(layer, b)
+
+    torch.cuda.synchronize()
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        a, b, y = step()
+    for seed in (1, 2, 3):
+        x.copy_(torch.randn(T, H, generator=torch.Generator().manual_seed(seed)))
+        gr.replay()
+        torch.cuda.synchronize()
+        for got, want in zip((a, b, y), step()):
+            assert torch.equal(got, want)
+        bv = u.encoded(u.to64(a), 1) @ u.table_values(fp8).T
+        assert np.abs(u.to64(b) - bv).max() <= 6 * np.sqrt(H) * u.EPS32 * np.abs(bv).max()
+        yv, _, _ = plain(layer, b)
+        assert np.abs(u.to64(y) - yv).max() <= (6 * np.sqrt(H + 384) + 16) * u.EPS32 * np.abs(yv).max()
