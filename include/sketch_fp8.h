@@ -80,10 +80,12 @@ sketch_status sketch_fp8_encode(const sketch_fp8_params* p, const void* W, sketc
 
 /*
  * sketch_fp8_workspace_bytes -- device scratch sketch_fp8_matmul needs for
- * `batch` rows of X (host only).  Its contents need no initialisation; calls
+ * `batch` rows of X on the current device (host only): the encoded rows, and
+ * the float32 parts where K is split over workgroups.  Its contents need no initialisation; calls
  * that overlap in time need separate workspaces.
  */
-sketch_status sketch_fp8_workspace_bytes(const sketch_fp8_params* p, int64_t batch, int x_dtype, size_t* bytes);
+sketch_status sketch_fp8_workspace_bytes(const sketch_fp8_params* p, int64_t batch, int x_dtype, sketch_dtype y_dtype,
+                                         size_t* bytes);
 
 /*
  * sketch_fp8_matmul -- Y = X8 * W8^T.

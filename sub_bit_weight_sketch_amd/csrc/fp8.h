@@ -63,6 +63,20 @@ __device__ inline bf16x8 fp8_widen(uint32_t lo, uint32_t hi, float scale) {
     return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
+// Operands of one product: codes and scales of the weight [M] and of the
+// encoded rows [T], both with row strides ld and lds.
+struct Fp8Product {
+    const uint8_t *w, *ws, *x, *xs;
+    void* Y;
+    int64_t M, T, ld, lds;
+    uint32_t kb;   // blocks of 128 columns
+    int ydt;
+};
+
+// Products of many rows (fp8_gemm.hip): scratch (parts of a split of K), launch.
+size_t fp8_gemm_workspace(int64_t M, int64_t T, uint32_t kb, int ydt);
+sketch_status launch_fp8_gemm(const Fp8Product& p, void* ws, hipStream_t st);
+
 sketch_status launch_fp8_encode(const sketch_fp8_params* p, const sketch_fp8_shape& s, const void* W,
                                 sketch_dtype dt, void* buf, int32_t* status, hipStream_t st);
 

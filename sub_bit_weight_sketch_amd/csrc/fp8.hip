@@ -114,13 +114,6 @@ __global__ __launch_bounds__(256) void fp8_encode_kernel(EncodeArgs a) {
 // 64+16c..64+16c+15, c = l / 16, in both, so that each load covers 64
 // contiguous bytes of a row.  D: token l % 16, outputs 4c..4c+3.
 // ---------------------------------------------------------------------------
-struct MatmulArgs {
-    const uint8_t *w, *ws, *x, *xs;   // codes and scales of the weight and of the rows
-    void* Y;
-    int64_t M, T, ld, lds;
-    uint32_t kb;                      // blocks of 128 columns
-};
-
 __device__ inline i32x8 load_frag(const uint8_t* row, int c) {
     const i32x4 lo = *reinterpret_cast<const i32x4*>(row + 16 * c);
     const i32x4 hi = *reinterpret_cast<const i32x4*>(row + 64 + 16 * c);
@@ -128,7 +121,7 @@ __device__ inline i32x8 load_frag(const uint8_t* row, int c) {
 }
 
 template <int YD>
-__global__ __launch_bounds__(64) void fp8_simple_kernel(MatmulArgs a) {
+__global__ __launch_bounds__(64) void fp8_simple_kernel(Fp8Product a) {
     const int lane = threadIdx.x, r = lane & 15, c = lane >> 4;
     const int64_t m0 = int64_t(blockIdx.x) * 16, t0 = int64_t(blockIdx.y) * 16;
     const int64_t m = min(m0 + r, a.M - 1), t = min(t0 + r, a.T - 1);
@@ -205,16 +198,21 @@ sketch_status sketch_fp8_encode(const sketch_fp8_params* p, const void* W, sketc
     return launch_fp8_encode(p, s, W, w_dtype, buf, status_dev, static_cast<hipStream_t>(stream));
 }
 
-sketch_status sketch_fp8_workspace_bytes(const sketch_fp8_params* p, int64_t batch, int x_dtype, size_t* bytes) {
+sketch_status sketch_fp8_workspace_bytes(const sketch_fp8_params* p, int64_t batch, int x_dtype, sketch_dtype y_dtype,
+                                         size_t* bytes) {
     sketch_fp8_shape s, xs;
     sketch_status rc = fp8_shape(p, &s);
     if (rc != SKETCH_OK) return rc;
-    if (!bytes || batch < 0 || p->block_rows != 128 || p->count > 1 || (!valid_dtype(x_dtype) && x_dtype != SKETCH_FP8_ROWS))
+    if (!bytes || batch < 0 || p->block_rows != 128 || p->count > 1 || (!valid_dtype(x_dtype) && x_dtype != SKETCH_FP8_ROWS) ||
+        !valid_dtype(y_dtype))
         return SKETCH_EINVAL;
     const sketch_fp8_params xp{batch, p->N, 1, 1};
     rc = fp8_shape(&xp, &xs);
     if (rc != SKETCH_OK) return rc;
-    *bytes = batch == 0 || p->M == 0 || x_dtype == SKETCH_FP8_ROWS ? 0 : xs.bytes;
+    *bytes = 0;
+    if (batch == 0 || p->M == 0) return SKETCH_OK;
+    if (x_dtype != SKETCH_FP8_ROWS) *bytes += xs.bytes;
+    if (batch > SKETCH_FP8_EXACT_BATCH) *bytes += fp8_gemm_workspace(p->M, batch, uint32_t(s.col_blocks), y_dtype);
     return SKETCH_OK;
 }
 
@@ -222,32 +220,33 @@ sketch_status sketch_fp8_matmul(const sketch_fp8_params* p, const void* buf, con
                                 int64_t batch, void* Y, sketch_dtype y_dtype, void* workspace,
                                 size_t workspace_bytes, void* stream) {
     size_t need = 0;
-    sketch_status rc = sketch_fp8_workspace_bytes(p, batch, x_dtype, &need);
+    sketch_status rc = sketch_fp8_workspace_bytes(p, batch, x_dtype, y_dtype, &need);
     if (rc != SKETCH_OK) return rc;
-    if (!valid_dtype(y_dtype)) return SKETCH_EINVAL;
     if (batch == 0 || p->M == 0) return SKETCH_OK;
     if (!buf || !X || !Y || !aligned16(buf) || !aligned16(X) || !aligned16(Y)) return SKETCH_EINVAL;
     if (need > 0) {
         if (!workspace || !aligned16(workspace)) return SKETCH_EINVAL;
         if (workspace_bytes < need) return SKETCH_ESMALL;
     }
-    const int64_t tiles_t = (batch + 15) / 16;
-    if (tiles_t > 65535) return SKETCH_EINVAL;
     const hipStream_t st = static_cast<hipStream_t>(stream);
     sketch_fp8_shape s, xs;
     const sketch_fp8_params xp{batch, p->N, 1, 1};
     (void)fp8_shape(p, &s);
     (void)fp8_shape(&xp, &xs);
-    const uint8_t* x8 = static_cast<const uint8_t*>(X);
+    const uint8_t *w8 = static_cast<const uint8_t*>(buf), *x8 = static_cast<const uint8_t*>(X);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
     if (x_dtype != SKETCH_FP8_ROWS) {
-        rc = launch_fp8_encode(&xp, xs, X, sketch_dtype(x_dtype), workspace, nullptr, st);
+        rc = launch_fp8_encode(&xp, xs, X, sketch_dtype(x_dtype), ws, nullptr, st);
         if (rc != SKETCH_OK) return rc;
-        x8 = static_cast<const uint8_t*>(workspace);
+        x8 = ws;
+        ws += xs.bytes;
     }
-    const uint8_t* w8 = static_cast<const uint8_t*>(buf);
-    MatmulArgs a{w8, w8 + s.scales_offset, x8, x8 + xs.scales_offset, Y, p->M, batch, s.ld, s.lds, uint32_t(s.col_blocks)};
+    const Fp8Product a{w8, w8 + s.scales_offset, x8, x8 + xs.scales_offset, Y, p->M, batch, s.ld, s.lds,
+                       uint32_t(s.col_blocks), int(y_dtype)};
+    if (batch > SKETCH_FP8_EXACT_BATCH) return launch_fp8_gemm(a, ws, st);
+    const dim3 grid(unsigned((p->M + 15) / 16), unsigned((batch + 15) / 16));
     auto go = [&](auto kernel) {
-        kernel<<<dim3(unsigned((p->M + 15) / 16), unsigned(tiles_t)), 64, 0, st>>>(a);
+        kernel<<<grid, 64, 0, st>>>(a);
         return launch_status();
     };
     return y_dtype == SKETCH_F32    ? go(fp8_simple_kernel<SKETCH_F32>)

@@ -1,0 +1,408 @@
+// fp8_gemm.hip -- the e4m3 product Y = X8 * W8^T for many rows.
+//
+// Both operands are staged in LDS one block of 128 columns at a time, straight
+// from memory (no registers in between), 128 bytes to a row, the row's eight
+// 16-byte pieces in the order piece ^ (row % 8), which lets the 16 rows of a
+// fragment be read without bank conflicts.  A fragment is 16 rows x 128
+// columns: lane l holds row l % 16 and the columns 16c..16c+15 and
+// 64+16c..64+16c+15, c = l / 16, the same ones in both operands.
+#include "fp8.h"
+
+namespace sketch {
+namespace {
+
+struct GemmArgs {
+    Fp8Product p;
+    uint32_t tiles_o, tiles_t;
+    uint32_t splits;   // of K, over blockIdx.y (fp8_gemm_kernel)
+    float* parts;      // [splits][T][M] when splits > 1
+};
+
+// 16 (or 4) bytes per lane from base + off to LDS bytes lds + 16 i (4 i) of
+// lane i.  Inline asm, because with the builtin the compiler waits for every
+// outstanding load before each LDS read; here the waits that matter are
+// written out.  There is no register result; M0 needs a wait state after its
+// write.
+__device__ inline void dma16(const uint8_t* base, uint32_t off, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(lds)
+                 : "memory", "m0");
+}
+__device__ inline void dma4(const uint8_t* base, uint32_t off, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1" ::"v"(off), "s"(base), "s"(lds)
+                 : "memory", "m0");
+}
+__device__ inline void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+__device__ inline void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+__device__ inline void barrier() {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_barrier" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+__device__ inline uint32_t lds_address(const void* p) {
+    return __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)));
+}
+
+// Tile of a workgroup.  Workgroups go round the 8 XCDs, so each XCD gets a
+// contiguous run of tiles; a run goes through groups of 8 token tiles, so that
+// the tiles in flight on an XCD share both operands in its L2.
+__device__ inline void tile_of(const GemmArgs& a, uint32_t& to, uint32_t& tt) {
+    const uint32_t n = gridDim.x, q = n / 8, rem = n % 8, xcd = blockIdx.x % 8;
+    const uint32_t id = xcd * q + (xcd < rem ? xcd : rem) + blockIdx.x / 8;
+    constexpr uint32_t G = 8;
+    const uint32_t g = id / (G * a.tiles_o), gt = min(G, a.tiles_t - g * G), in = id - g * G * a.tiles_o;
+    to = in / gt;
+    tt = g * G + in % gt;
+}
+
+template <int YD>
+__device__ inline void store4(void* Y, int64_t e, f32x4 v, int64_t m, int64_t M, bool vec) {
+    if (vec && m + 4 <= M) {
+        if constexpr (YD == SKETCH_F32) {
+            *reinterpret_cast<f32x4*>(static_cast<float*>(Y) + e) = v;
+        } else {
+            uint32_t h[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) h[i] = YD == SKETCH_BF16 ? f32_to_bf16_bits(v[i]) : f32_to_f16_bits(v[i]);
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(Y) + e) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (m + i < M) store1_val<YD>(Y, e + i, v[i]);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// 256 outputs x 256 tokens on the e4m3 matrix cores (16-bit Y).  8 waves, two
+// to a SIMD, each 128 x 64: 32 accumulators of 16x16.  The waves work in two
+// groups, one on each SIMD, half a step apart: while one group runs the 32
+// MFMAs of its step from registers, the other reads its 12 fragments from LDS,
+// so the matrix cores always have one wave's work and LDS the other's.  The
+// 64 KiB of a step are loaded while the step before is worked on.
+// ---------------------------------------------------------------------------
+constexpr int kBigRows = 512;                       // 256 of W, 256 of X
+constexpr uint32_t kBigStage = kBigRows * 128;
+constexpr uint32_t kBigScales = (256 + 16) * 4;     // dwords of 4 steps: one per token, one per 16 outputs
+constexpr uint32_t kBigLds = 2 * kBigStage + 2 * kBigScales;
+
+template <int YD>
+__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void fp8_gemm_big_kernel(GemmArgs a) {
+    extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
+    const Fp8Product& p = a.p;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int r = lane & 15, c = lane >> 4, group = wave >> 2, wm = group * 128, wt = (wave & 3) * 64;
+    uint32_t to, tt;
+    tile_of(a, to, tt);
+    const int64_t o0 = int64_t(to) * 256, t0 = int64_t(tt) * 256;
+
+    // loads of this wave: 4 x 8 rows of W and 4 x 8 rows of X per step
+    const uint8_t *wbase = p.w + o0 * p.ld, *xbase = p.x + t0 * p.ld;
+    const uint32_t wlast = uint32_t(min(int64_t(255), p.M - 1 - o0)), xlast = uint32_t(min(int64_t(255), p.T - 1 - t0));
+    const uint32_t piece = uint32_t((lane & 7) ^ (lane >> 3)) * 16, ld = uint32_t(p.ld);
+    uint32_t woff[4], xoff[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t row = uint32_t(wave * 32 + i * 8 + (lane >> 3));
+        woff[i] = min(row, wlast) * ld + piece;
+        xoff[i] = min(row, xlast) * ld + piece;
+    }
+    // scales: waves 0..3 the tokens', wave 4 the outputs' (a row of 16 outputs lies in one block of 128)
+    const uint8_t* sbase = wave < 4 ? p.xs + t0 * p.lds : p.ws;
+    const uint32_t srow = wave < 4 ? min(uint32_t(wave * 64 + lane), xlast)
+                                   : uint32_t(min(o0 + (lane & 15) * 16, p.M - 1) / 128);
+    const uint32_t soff = srow * uint32_t(p.lds);
+    const uint32_t lds0 = lds_address(lds), lw = lds0 + wave * 4096, lx = lw + 32768;
+    const uint32_t lsc = lds0 + 2 * kBigStage + (wave < 4 ? wave * 256 : 1024);
+
+    auto load_step = [&](uint32_t k) {
+        const uint32_t st = (k & 1) * kBigStage;
+        const uint8_t *wk = wbase + size_t(k) * 128, *xk = xbase + size_t(k) * 128;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) dma16(wk, woff[i], lw + st + i * 1024);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) dma16(xk, xoff[i], lx + st + i * 1024);
+        if ((k & 3) == 0) {
+            if (wave < 4 || (wave == 4 && lane < 16)) dma4(sbase + k, soff, lsc + ((k >> 2) & 1) * kBigScales);
+        }
+    };
+
+    f32x4 acc[8][4];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+    i32x8 af[8], bf[4];
+    int as[8], bs[4];
+    const unsigned char* frag = lds + r * 128 + ((c ^ (r & 7)) << 4);
+    const unsigned char* frag2 = lds + r * 128 + (((c + 4) ^ (r & 7)) << 4);
+
+    auto read_step = [&](uint32_t k) {
+        const uint32_t st = (k & 1) * kBigStage;
+        const unsigned char *f1 = frag + st + wm * 128, *f2 = frag2 + st + wm * 128;
+        const unsigned char *g1 = frag + st + 32768 + wt * 128, *g2 = frag2 + st + 32768 + wt * 128;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            bf[j] = __builtin_shufflevector(*reinterpret_cast<const i32x4*>(g1 + j * 2048),
+                                            *reinterpret_cast<const i32x4*>(g2 + j * 2048), 0, 1, 2, 3, 4, 5, 6, 7);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            af[i] = __builtin_shufflevector(*reinterpret_cast<const i32x4*>(f1 + i * 2048),
+                                            *reinterpret_cast<const i32x4*>(f2 + i * 2048), 0, 1, 2, 3, 4, 5, 6, 7);
+        if ((k & 3) == 0) {
+            const int* sc = reinterpret_cast<const int*>(lds + 2 * kBigStage + ((k >> 2) & 1) * kBigScales);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) bs[j] = sc[wt + j * 16 + r];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) as[i] = sc[256 + wm / 16 + i];
+        } else {   // the next byte to the low end
+#pragma unroll
+            for (int j = 0; j < 4; ++j) bs[j] = int(uint32_t(bs[j]) >> 8);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) as[i] = int(uint32_t(as[i]) >> 8);
+        }
+    };
+    auto compute = [&]() {
+        __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(af[i], bf[j], acc[i][j], 0, 0, 0, as[i],
+                                                                              0, bs[j]);
+        __builtin_amdgcn_s_setprio(0);
+    };
+
+    // Step k is read by group 0 in phase 2k and by group 1 in phase 2k + 1;
+    // its buffer is loaded again, with step k + 2, in phase 2k + 2, and that
+    // is waited for at the end of phase 2k + 3.
+    load_step(0);
+    wait_loads();
+    barrier();
+    if (group == 0) {
+        for (uint32_t k = 0; k < p.kb; ++k) {
+            if (k + 1 < p.kb) load_step(k + 1);
+            read_step(k);
+            wait_lds();
+            barrier();
+            compute();
+            wait_loads();
+            barrier();
+        }
+        barrier();
+    } else {
+        if (p.kb > 1) load_step(1);
+        barrier();
+        for (uint32_t k = 0; k < p.kb; ++k) {
+            read_step(k);
+            wait_lds();
+            wait_loads();
+            barrier();
+            if (k + 2 < p.kb) load_step(k + 2);
+            compute();
+            barrier();
+        }
+    }
+
+    const bool vec = p.M % 4 == 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int64_t t = t0 + wt + j * 16 + r;
+        if (t >= p.T) continue;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int64_t m = o0 + wm + i * 16 + 4 * c;
+            store4<YD>(p.Y, t * p.M + m, acc[i][j], m, p.M, vec);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// 128 outputs x 128 tokens, 4 waves of 64 x 64, two workgroups to a CU: for
+// fewer tiles than the big kernel needs, and (EXACT) for float32 Y, whose
+// fragments are widened to bfloat16 with their scales applied, so that every
+// product is exact and the sums are float32.  K is split over blockIdx.y when
+// the tiles alone leave compute units idle; the parts are float32 and
+// fp8_add_kernel adds them in their order.
+// ---------------------------------------------------------------------------
+constexpr uint32_t kMidStage = 256 * 128;
+constexpr uint32_t kMidScales = (128 + 64) * 4;
+constexpr uint32_t kMidLds = 2 * kMidStage + 2 * kMidScales;
+
+template <int YD, bool EXACT>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void fp8_gemm_kernel(GemmArgs a) {
+    extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
+    const Fp8Product& p = a.p;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int r = lane & 15, c = lane >> 4, wm = (wave >> 1) * 64, wt = (wave & 1) * 64;
+    uint32_t to, tt;
+    tile_of(a, to, tt);
+    const int64_t o0 = int64_t(to) * 128, t0 = int64_t(tt) * 128;
+    const uint32_t kend = uint32_t(uint64_t(p.kb) * (blockIdx.y + 1) / a.splits);
+    const uint32_t kbeg = uint32_t(uint64_t(p.kb) * blockIdx.y / a.splits);
+
+    // loads of this wave: 32 rows of W and 32 of X per step; waves 0 and 1 the
+    // tokens' scales, wave 2 the outputs' (one block of 128)
+    const uint8_t *wbase = p.w + o0 * p.ld, *xbase = p.x + t0 * p.ld;
+    const uint32_t wlast = uint32_t(min(int64_t(127), p.M - 1 - o0)), xlast = uint32_t(min(int64_t(127), p.T - 1 - t0));
+    const uint32_t piece = uint32_t((lane & 7) ^ (lane >> 3)) * 16, ld = uint32_t(p.ld);
+    uint32_t woff[4], xoff[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t row = uint32_t(wave * 32 + i * 8 + (lane >> 3));
+        woff[i] = min(row, wlast) * ld + piece;
+        xoff[i] = min(row, xlast) * ld + piece;
+    }
+    const uint8_t* sbase = wave < 2 ? p.xs + t0 * p.lds : p.ws + o0 / 128 * p.lds;
+    const uint32_t soff = wave < 2 ? min(uint32_t(wave * 64 + lane), xlast) * uint32_t(p.lds) : 0;
+    const uint32_t lds0 = lds_address(lds), lw = lds0 + wave * 4096, lx = lw + 16384;
+    const uint32_t lsc = lds0 + 2 * kMidStage + wave * 256;
+    auto load_step = [&](uint32_t k) {
+        const uint32_t st = ((k - kbeg) & 1) * kMidStage;
+        const uint8_t *wk = wbase + size_t(k) * 128, *xk = xbase + size_t(k) * 128;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) dma16(wk, woff[i], lw + st + i * 1024);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) dma16(xk, xoff[i], lx + st + i * 1024);
+        if (((k & 3) == 0 || k == kbeg) && wave < 3) dma4(sbase + (k & ~3u), soff, lsc + ((k >> 2) & 1) * kMidScales);
+    };
+
+    f32x4 acc[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+    const unsigned char* frag = lds + r * 128 + ((c ^ (r & 7)) << 4);
+    const unsigned char* frag2 = lds + r * 128 + (((c + 4) ^ (r & 7)) << 4);
+
+    if (kbeg < kend) load_step(kbeg);
+    for (uint32_t k = kbeg; k < kend; ++k) {
+        wait_loads();
+        barrier();   // step k is here, and every wave is done with step k - 1
+        if (k + 1 < kend) load_step(k + 1);
+        const uint32_t st = ((k - kbeg) & 1) * kMidStage;
+        const unsigned char *f1 = frag + st + wm * 128, *f2 = frag2 + st + wm * 128;
+        const unsigned char *g1 = frag + st + 16384 + wt * 128, *g2 = frag2 + st + 16384 + wt * 128;
+        const int* sc = reinterpret_cast<const int*>(lds + 2 * kMidStage + ((k >> 2) & 1) * kMidScales);
+        const uint32_t as = uint32_t(sc[128]) >> (8 * (k & 3)) & 255u;
+        i32x8 af[4], bf[4];
+        uint32_t bs[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            bf[j] = __builtin_shufflevector(*reinterpret_cast<const i32x4*>(g1 + j * 2048),
+                                            *reinterpret_cast<const i32x4*>(g2 + j * 2048), 0, 1, 2, 3, 4, 5, 6, 7);
+            bs[j] = uint32_t(sc[wt + j * 16 + r]) >> (8 * (k & 3)) & 255u;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            af[i] = __builtin_shufflevector(*reinterpret_cast<const i32x4*>(f1 + i * 2048),
+                                            *reinterpret_cast<const i32x4*>(f2 + i * 2048), 0, 1, 2, 3, 4, 5, 6, 7);
+        if constexpr (EXACT) {
+            bf16x8 bw[4][4];
+            const float asf = fp8_scale(as);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) bw[j][q] = fp8_widen(bf[j][2 * q], bf[j][2 * q + 1], fp8_scale(bs[j]));
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const bf16x8 aw = fp8_widen(af[i][2 * q], af[i][2 * q + 1], asf);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(aw, bw[j][q], acc[i][j], 0, 0, 0);
+                }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(af[i], bf[j], acc[i][j], 0, 0, 0,
+                                                                                  int(as), 0, int(bs[j]));
+        }
+    }
+
+    const bool vec = p.M % 4 == 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int64_t t = t0 + wt + j * 16 + r;
+        if (t >= p.T) continue;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t m = o0 + wm + i * 16 + 4 * c;
+            if (a.splits > 1)
+                store4<SKETCH_F32>(a.parts + (blockIdx.y * p.T) * p.M, t * p.M + m, acc[i][j], m, p.M, vec);
+            else
+                store4<YD>(p.Y, t * p.M + m, acc[i][j], m, p.M, vec);
+        }
+    }
+}
+
+template <int YD>
+__global__ __launch_bounds__(256) void fp8_add_kernel(GemmArgs a) {
+    const int64_t n = a.p.T * a.p.M, step = int64_t(gridDim.x) * 1024;
+    for (int64_t e = (int64_t(blockIdx.x) * 256 + threadIdx.x) * 4; e < n; e += step) {
+        if (n % 4 == 0) {   // planes keep their 16-byte alignment
+            f32x4 sum = *reinterpret_cast<const f32x4*>(a.parts + e);
+            for (uint32_t s = 1; s < a.splits; ++s) sum += *reinterpret_cast<const f32x4*>(a.parts + s * n + e);
+            store4<YD>(a.p.Y, e, sum, 0, 4, true);
+        } else {
+            for (int64_t i = e; i < n && i < e + 4; ++i) {
+                float sum = a.parts[i];
+                for (uint32_t s = 1; s < a.splits; ++s) sum += a.parts[s * n + i];
+                store1_val<YD>(a.p.Y, i, sum);
+            }
+        }
+    }
+}
+
+// Which kernel a product takes, and over how many workgroups K is split.
+struct GemmPlan {
+    bool big;
+    uint32_t splits;
+};
+
+GemmPlan gemm_plan(int64_t M, int64_t T, uint32_t kb, int ydt) {
+    const int64_t ncu = compute_units();
+    const int64_t big = (M + 255) / 256 * ((T + 255) / 256), mid = (M + 127) / 128 * ((T + 127) / 128);
+    if (ydt != SKETCH_F32 && big >= ncu * 3 / 4) return {true, 1};
+    int64_t splits = mid >= ncu ? 1 : 2 * ncu / mid;
+    if (splits > kb / 4) splits = kb / 4 > 1 ? kb / 4 : 1;
+    return {false, uint32_t(splits)};
+}
+
+}  // namespace
+
+size_t fp8_gemm_workspace(int64_t M, int64_t T, uint32_t kb, int ydt) {
+    const GemmPlan g = gemm_plan(M, T, kb, ydt);
+    return g.splits > 1 ? align256(size_t(g.splits) * size_t(M) * size_t(T) * 4) : 0;
+}
+
+sketch_status launch_fp8_gemm(const Fp8Product& p, void* ws, hipStream_t st) {
+    const GemmPlan g = gemm_plan(p.M, p.T, p.kb, p.ydt);
+    const int64_t edge = g.big ? 256 : 128;
+    GemmArgs a{p, uint32_t((p.M + edge - 1) / edge), uint32_t((p.T + edge - 1) / edge), g.splits, static_cast<float*>(ws)};
+    const int64_t tiles = int64_t(a.tiles_o) * a.tiles_t;
+    if (tiles > 0x7FFFFFFF) return SKETCH_EINVAL;
+    if (g.big) {
+        if (p.ydt == SKETCH_BF16)
+            fp8_gemm_big_kernel<SKETCH_BF16><<<unsigned(tiles), 512, kBigLds, st>>>(a);
+        else
+            fp8_gemm_big_kernel<SKETCH_F16><<<unsigned(tiles), 512, kBigLds, st>>>(a);
+        return launch_status();
+    }
+    auto go = [&](auto product, auto add) {
+        product<<<dim3(unsigned(tiles), g.splits), 256, kMidLds, st>>>(a);
+        if (g.splits == 1) return launch_status();
+        if (hipGetLastError() != hipSuccess) return SKETCH_EDEVICE;
+        const int64_t blocks = (p.T * p.M + 1023) / 1024;
+        add<<<unsigned(blocks < 2048 ? blocks : 2048), 256, 0, st>>>(a);
+        return launch_status();
+    };
+    return p.ydt == SKETCH_F32    ? go(fp8_gemm_kernel<SKETCH_F32, true>, fp8_add_kernel<SKETCH_F32>)
+           : p.ydt == SKETCH_BF16 ? go(fp8_gemm_kernel<SKETCH_BF16, false>, fp8_add_kernel<SKETCH_BF16>)
+                                  : go(fp8_gemm_kernel<SKETCH_F16, false>, fp8_add_kernel<SKETCH_F16>);
+}
+
+}  // namespace sketch

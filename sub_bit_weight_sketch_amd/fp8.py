@@ -45,7 +45,7 @@ def _fp8_lib():
         vp, i64, sz, it = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int
         L.sketch_fp8_layout.argtypes = [P, ctypes.POINTER(Fp8Shape)]
         L.sketch_fp8_encode.argtypes = [P, vp, it, vp, vp, vp]
-        L.sketch_fp8_workspace_bytes.argtypes = [P, i64, it, ctypes.POINTER(sz)]
+        L.sketch_fp8_workspace_bytes.argtypes = [P, i64, it, it, ctypes.POINTER(sz)]
         L.sketch_fp8_matmul.argtypes = [P, vp, vp, it, i64, vp, it, vp, sz, vp]
         L.sketch_moe_workspace_bytes.argtypes = [Q, i64, ctypes.POINTER(sz)]
         L.sketch_moe.argtypes = [Q, vp, vp, vp, vp, vp, i64, vp, vp, vp, vp, sz, vp]
@@ -72,10 +72,10 @@ def sketch_fp8_encode(p, W, buf, status=None, stream=None):
            "sketch_fp8_encode")
 
 
-def sketch_fp8_workspace_bytes(p, batch, x_dtype):
+def sketch_fp8_workspace_bytes(p, batch, x_dtype, y_dtype):
     n = ctypes.c_size_t()
-    _check(_fp8_lib().sketch_fp8_workspace_bytes(ctypes.byref(p), int(batch), int(x_dtype), ctypes.byref(n)),
-           "sketch_fp8_workspace_bytes")
+    _check(_fp8_lib().sketch_fp8_workspace_bytes(ctypes.byref(p), int(batch), int(x_dtype), int(y_dtype),
+                                                 ctypes.byref(n)), "sketch_fp8_workspace_bytes")
     return n.value
 
 
@@ -205,13 +205,13 @@ def fp8_tables(codes, scales, block_rows=128):
     return t
 
 
-def fp8_workspace_for(t, batch, x_dtype, device):
+def fp8_workspace_for(t, batch, x_dtype, y_dtype, device):
     """Workspace for products of `batch` rows (None if not needed).  Reuse it
     across calls on one stream, never for two calls in flight at once."""
-    key = (batch, x_dtype)
+    key = (batch, x_dtype, y_dtype)
     n = t._ws.get(key)
     if n is None:
-        n = t._ws[key] = sketch_fp8_workspace_bytes(t.params, batch, x_dtype)
+        n = t._ws[key] = sketch_fp8_workspace_bytes(t.params, batch, x_dtype, y_dtype)
     return torch.empty(n, dtype=torch.uint8, device=device) if n else None
 
 
@@ -246,7 +246,7 @@ def fp8_matmul(t, X, out=None, workspace=None, dtype=None):
     with _on(t.device):
         Y = _out(out[None, :] if squeeze and out is not None and out.dim() == 1 else out, (batch, t.M), dtype, t.device)
         if workspace is None:
-            workspace = fp8_workspace_for(t, batch, xdt, t.device)
+            workspace = fp8_workspace_for(t, batch, xdt, dtype_code(Y), t.device)
         sketch_fp8_matmul(t.params, t.buf, x, xdt, batch, Y, workspace)
     return Y[0] if squeeze else Y
 

@@ -80,13 +80,14 @@ def test_encode_and_matmul_validate_before_launching():
     assert L.sketch_fp8_encode(ref(p), vp(256), sk.BF16, vp(256), vp(2), None) == sk.EINVAL
     assert L.sketch_fp8_encode(ref(sk.Fp8Params(0, 100, 128, 1)), None, sk.F32, None, None, None) == sk.OK
     n = ctypes.c_size_t()
-    assert L.sketch_fp8_workspace_bytes(ref(p), -1, sk.BF16, ref(n)) == sk.EINVAL
-    assert L.sketch_fp8_workspace_bytes(ref(p), 4, 4, ref(n)) == sk.EINVAL
-    assert L.sketch_fp8_workspace_bytes(ref(p), 4, sk.BF16, None) == sk.EINVAL
-    assert L.sketch_fp8_workspace_bytes(ref(sk.Fp8Params(64, 100, 1, 1)), 4, sk.BF16, ref(n)) == sk.EINVAL
-    assert L.sketch_fp8_workspace_bytes(ref(sk.Fp8Params(64, 100, 128, 2)), 4, sk.BF16, ref(n)) == sk.EINVAL
-    assert L.sketch_fp8_workspace_bytes(ref(p), 0, sk.BF16, ref(n)) == sk.OK and n.value == 0
-    big = sk.sketch_fp8_workspace_bytes(p, 4096, sk.BF16)
+    assert L.sketch_fp8_workspace_bytes(ref(p), -1, sk.BF16, sk.F32, ref(n)) == sk.EINVAL
+    assert L.sketch_fp8_workspace_bytes(ref(p), 4, 4, sk.F32, ref(n)) == sk.EINVAL
+    assert L.sketch_fp8_workspace_bytes(ref(p), 4, sk.BF16, sk.F32, None) == sk.EINVAL
+    assert L.sketch_fp8_workspace_bytes(ref(sk.Fp8Params(64, 100, 1, 1)), 4, sk.BF16, sk.F32, ref(n)) == sk.EINVAL
+    assert L.sketch_fp8_workspace_bytes(ref(sk.Fp8Params(64, 100, 128, 2)), 4, sk.BF16, sk.F32, ref(n)) == sk.EINVAL
+    assert L.sketch_fp8_workspace_bytes(ref(p), 0, sk.BF16, sk.F32, ref(n)) == sk.OK and n.value == 0
+    big = sk.sketch_fp8_workspace_bytes(p, 4096, sk.BF16, sk.BF16)
+    assert L.sketch_fp8_workspace_bytes(ref(p), 4, sk.BF16, 3, ref(n)) == sk.EINVAL
     assert big >= 4096 * 128       # room for the encoded rows at least
     mm = L.sketch_fp8_matmul
     assert mm(ref(p), vp(256), vp(256), sk.BF16, 0, vp(256), sk.F32, None, 0, None) == sk.OK

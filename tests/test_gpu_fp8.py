@@ -122,7 +122,7 @@ def exact_case(M, N, b, dt, seed=0):
     w = w * f.repeat_interleave(128)[:M, None]
     fx = torch.from_numpy(np.exp2(g.integers(-3, 4, (b,))).astype(np.float32))
     x = x * fx[:, None].to(x.dtype)
-    # the scale of column block j: 2^(j % 3) on the one side, in the weight
+    # column block j is 2^(j % 3) as large in the weight
     fk = torch.exp2((torch.arange(u.blocks(N, 128)) % 3).float()).repeat_interleave(128)[:N]
     w = w * fk
     assert N * 12 * 4 < 2 ** 24
@@ -146,14 +146,15 @@ def test_product_exact(M, N, b):
 
 @pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("M,N,b", [(300, 4001, 1), (300, 4001, 9), (2050, 640, 40), (700, 900, 300), (4096, 11008, 3),
-                                   (384, 300, 2000)])
+                                   (384, 300, 2000), (130, 11008, 140), (2100, 2500, 1300)])
 def test_product_exact_larger(M, N, b, dt):
     w, x = exact_case(M, N, b, dt, 5)
     t = sk.fp8_encode(w.to(dev()))
     assert np.array_equal(u.to64(sk.fp8_matmul(t, x.to(dev()))), u.to64(x) @ u.to64(w).T)
 
 
-@pytest.mark.parametrize("M,N,b", [(16, 128, 70), (700, 900, 1), (513, 1300, 65), (1000, 1111, 300), (2050, 640, 128)])
+@pytest.mark.parametrize("M,N,b", [(16, 128, 70), (700, 900, 1), (513, 1300, 65), (1000, 1111, 300), (2050, 640, 128),
+                                   (4300, 300, 3000), (4097, 1, 3001), (5000, 1155, 2570), (130, 11008, 140)])
 @pytest.mark.parametrize("y", ["bf16", "f16"])
 def test_product_in_16_bits(M, N, b, y):
     """Small integers: groups of 8 products, and all sums, are exact on either
@@ -269,7 +270,7 @@ def test_captured_and_replayed(b):
     t = sk.fp8_encode(w.to(dev()))
     xs = [exact_case(M, N, b, "bf16", 50 + i)[1].to(dev()) for i in range(3)]
     x, Y = xs[0].clone(), torch.empty(b, M, device=dev())
-    ws = sk.fp8_workspace_for(t, b, sk.BF16, dev())
+    ws = sk.fp8_workspace_for(t, b, sk.BF16, sk.F32, dev())
     sk.fp8_matmul(t, x, out=Y, workspace=ws)
     torch.cuda.synchronize()
     g = torch.cuda.CUDAGraph()
