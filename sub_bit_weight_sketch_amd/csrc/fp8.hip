@@ -12,134 +12,405 @@
 namespace sketch {
 namespace {
 
+// 8 elements of a row from column c0 on, zeros past its end.  Rows of any
+// length: the wide loads need only the alignment of an element (7.6 us
+// element by element -> 4.1 us for 517 x 4001 float32).
+template <int DT>
+__device__ inline void load_row8(const void* W, int64_t row, int64_t N, int64_t c0, float (&v)[8]) {
+    if (c0 + 8 <= N) {
+        typedef uint32_t loose __attribute__((ext_vector_type(4), aligned(2)));
+        constexpr int es = DT == SKETCH_F32 ? 4 : 2;
+        const loose* at = reinterpret_cast<const loose*>(static_cast<const char*>(W) + (row * N + c0) * es);
+        const loose a = at[0], b = DT == SKETCH_F32 ? at[1] : a;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const uint32_t h = (a[e >> 1] >> ((e & 1) * 16)) & 0xFFFFu;
+            v[e] = DT == SKETCH_F32    ? __uint_as_float(e < 4 ? a[e & 3] : b[e & 3])
+                   : DT == SKETCH_BF16 ? bf16_bits_to_f32(h)
+                                       : f16_bits_to_f32(h);
+        }
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = c0 + e < N ? load_elem<DT>(W, row * N + c0 + e) : 0.0f;
+}
+
+// Largest magnitude's bits; magnitudes compare as their bits, NaN above infinity.
+__device__ inline uint32_t max_bits(const float (&v)[8]) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(v[e]) & 0x7FFFFFFFu);
+    return m;
+}
+
+// The codes of 8 elements in a block of scale byte b (255: NaN).
+__device__ inline uint2 codes8(const float (&v)[8], uint32_t b) {
+    if (b == 255u) return make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
+    const float inv = fp8_inv_scale(b);
+    return make_uint2(fp8_pack4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
+                      fp8_pack4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv));
+}
+
+// The same at column c0 of a row of N: past the end the codes are zero.
+__device__ inline uint2 codes8(const float (&v)[8], uint32_t b, int64_t c0, int64_t N) {
+    uint2 q = codes8(v, b);
+    if (b == 255u && c0 + 8 > N) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (c0 + e >= N) (e < 4 ? q.x : q.y) &= ~(0xFFu << (8 * (e & 3)));
+    }
+    return q;
+}
+
+// Maximum over the 16 lanes of a row of a block.
+__device__ inline uint32_t max16(uint32_t m) {
+#pragma unroll
+    for (int d = 1; d < 16; d <<= 1) m = max(m, uint32_t(__shfl_xor(int(m), d)));
+    return m;
+}
+
 // ---------------------------------------------------------------------------
-// Encoder.  One workgroup per 128 x 128 tile, 16 lanes to a row: a thread
-// holds 8 columns of 8 rows, so the elements stay in registers between the
-// maximum and the rounding and W is read once.  HBM-bound.
+// Encoder of 128 x 128 blocks.  One workgroup per block, 16 lanes to a row: a
+// thread holds 8 columns of 8 rows, so the elements stay in registers between
+// the maximum and the rounding and W is read once.  HBM-bound.
 // ---------------------------------------------------------------------------
 struct EncodeArgs {
     const void* W;
     uint8_t* buf;
     int32_t* status;
-    int64_t M, N, ld, lds, tiles_m, col_blocks;
+    int64_t M, N, ld, lds, row_blocks, col_blocks, count;
     size_t scales_offset, bytes;
 };
 
-template <int DT, bool ROWS>
+template <int DT>
 __global__ __launch_bounds__(256) void fp8_encode_kernel(EncodeArgs a) {
     __shared__ uint32_t red[4];
     const int tid = threadIdx.x;
-    const int64_t cb = blockIdx.x % a.lds, tm = (blockIdx.x / a.lds) % a.tiles_m,
-                  mat = blockIdx.x / a.lds / a.tiles_m;
+    const int64_t cb = blockIdx.x % a.lds, rb = (blockIdx.x / a.lds) % a.row_blocks,
+                  mat = blockIdx.x / a.lds / a.row_blocks;
     uint8_t* codes = a.buf + mat * a.bytes;
-    uint8_t* scales = codes + a.scales_offset;
+    uint8_t* scale = codes + a.scales_offset + rb * a.lds + cb;
     if (cb >= a.col_blocks) {   // scale bytes that round a row of scales up to a dword
-        if (ROWS) {
-            const int64_t row = tm * 128 + tid;
-            if (tid < 128 && row < a.M) scales[row * a.lds + cb] = 0;
-        } else if (tid == 0) {
-            scales[tm * a.lds + cb] = 0;
-        }
+        if (tid == 0) *scale = 0;
         return;
     }
     constexpr int64_t es = DT == SKETCH_F32 ? 4 : 2;
     const unsigned char* W = static_cast<const unsigned char*>(a.W) + mat * a.M * a.N * es;
-    const int64_t c0 = cb * 128 + (tid & 15) * 8;
-    const bool whole = a.N % 8 == 0 && c0 + 8 <= a.N;   // rows keep 16-byte alignment
+    const int64_t c0 = cb * 128 + (tid & 15) * 8, row0 = rb * 128 + (tid >> 4);
     float v[8][8];
-    uint32_t mx[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const int64_t row = tm * 128 + i * 16 + (tid >> 4);
-        if (row < a.M && whole) {
-            load8_f32<DT>(W, row * a.N + c0, v[i]);
+        if (row0 + i * 16 < a.M) {
+            load_row8<DT>(W, row0 + i * 16, a.N, c0, v[i]);
         } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                v[i][e] = row < a.M && c0 + e < a.N ? load_elem<DT>(W, row * a.N + c0 + e) : 0.0f;
+            for (int e = 0; e < 8; ++e) v[i][e] = 0.0f;
         }
     }
+    uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        mx[i] = 0;   // magnitudes compare as their bits; NaN is above infinity
+    for (int i = 0; i < 8; ++i) m = max(m, max_bits(v[i]));
 #pragma unroll
-        for (int e = 0; e < 8; ++e) mx[i] = max(mx[i], __float_as_uint(v[i][e]) & 0x7FFFFFFFu);
+    for (int d = 1; d < 64; d <<= 1) m = max(m, uint32_t(__shfl_xor(int(m), d)));
+    if ((tid & 63) == 0) red[tid >> 6] = m;
+    __syncthreads();
+    const uint32_t b = fp8_scale_byte(max(max(red[0], red[1]), max(red[2], red[3])));
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (row0 + i * 16 < a.M)
+            *reinterpret_cast<uint2*>(codes + (row0 + i * 16) * a.ld + c0) = codes8(v[i], b, c0, a.N);
+    if (tid == 0) {
+        *scale = uint8_t(b);
+        if (a.status && b == 255u) atomicOr(a.status, SKETCH_FLAG_WEIGHT_RANGE);
     }
-    if constexpr (ROWS) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-            for (int d = 1; d < 16; d <<= 1) mx[i] = max(mx[i], uint32_t(__shfl_xor(int(mx[i]), d)));
-    } else {
-        uint32_t m = mx[0];
-#pragma unroll
-        for (int i = 1; i < 8; ++i) m = max(m, mx[i]);
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) m = max(m, uint32_t(__shfl_xor(int(m), d)));
-        if ((tid & 63) == 0) red[tid >> 6] = m;
-        __syncthreads();
-        m = max(max(red[0], red[1]), max(red[2], red[3]));
-#pragma unroll
-        for (int i = 0; i < 8; ++i) mx[i] = m;
+}
+
+// Encoder of 1 x 128 blocks: 16 lanes per block, one block each.
+template <int DT>
+__global__ __launch_bounds__(256) void fp8_encode_rows_kernel(EncodeArgs a) {
+    const uint64_t id = uint64_t(blockIdx.x) * 16 + (threadIdx.x >> 4);   // (matrix, row, column block)
+    const uint32_t lds = uint32_t(a.lds);
+    const uint64_t grow = id / lds;
+    const int64_t cb = int64_t(id - grow * lds), mat = int64_t(grow / uint64_t(a.M)), row = int64_t(grow) - mat * a.M;
+    if (mat >= a.count) return;
+    uint8_t* codes = a.buf + mat * a.bytes;
+    uint8_t* scale = codes + a.scales_offset + row * a.lds + cb;
+    const int64_t c0 = cb * 128 + (threadIdx.x & 15) * 8;
+    constexpr int64_t es = DT == SKETCH_F32 ? 4 : 2;
+    const unsigned char* W = static_cast<const unsigned char*>(a.W) + mat * a.M * a.N * es;
+    float v[8];
+    load_row8<DT>(W, row, a.N, c0, v);
+    const uint32_t b = fp8_scale_byte(max16(max_bits(v)));
+    if (cb < a.col_blocks) *reinterpret_cast<uint2*>(codes + row * a.ld + c0) = codes8(v, b, c0, a.N);
+    if ((threadIdx.x & 15) == 0) {
+        *scale = cb < a.col_blocks ? uint8_t(b) : uint8_t(0);
+        if (a.status && b == 255u) atomicOr(a.status, SKETCH_FLAG_WEIGHT_RANGE);
     }
-    bool bad = false;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int64_t row = tm * 128 + i * 16 + (tid >> 4);
-        if (row >= a.M) continue;
-        const uint32_t b = fp8_scale_byte(mx[i]);
-        const bool nan = b == 255u;
-        bad |= nan;
-        const float inv = fp8_inv_scale(nan ? 127u : b);
-        uint2 q;
-        q.x = nan ? 0x7F7F7F7Fu : fp8_pack4(v[i][0] * inv, v[i][1] * inv, v[i][2] * inv, v[i][3] * inv);
-        q.y = nan ? 0x7F7F7F7Fu : fp8_pack4(v[i][4] * inv, v[i][5] * inv, v[i][6] * inv, v[i][7] * inv);
-        if (nan && c0 + 8 > a.N) {   // the padding stays zero
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (c0 + e >= a.N) (e < 4 ? q.x : q.y) &= ~(0xFFu << (8 * (e & 3)));
-        }
-        *reinterpret_cast<uint2*>(codes + row * a.ld + c0) = q;
-        if (ROWS && (tid & 15) == 0) scales[row * a.lds + cb] = uint8_t(b);
-        if (!ROWS && tid == 0 && i == 0) scales[tm * a.lds + cb] = uint8_t(b);
-    }
-    if (a.status && __ballot(bad) != 0 && (tid & 63) == 0) atomicOr(a.status, SKETCH_FLAG_WEIGHT_RANGE);
 }
 
 // ---------------------------------------------------------------------------
-// Product.  One wave per 16 outputs x 16 tokens, operands straight from
-// memory, widened to bfloat16 with their scales applied (exact) and summed by
-// 16x16x32 MFMAs.  A (weights): lane l holds output l % 16; B (tokens): token
-// l % 16; the lane's 32 columns of a block are bytes 16c..16c+15 and
-// 64+16c..64+16c+15, c = l / 16, in both, so that each load covers 64
-// contiguous bytes of a row.  D: token l % 16, outputs 4c..4c+3.
+// Products of few rows.  Bound by the codes of W coming from memory, so every
+// code is read once, 16 or 32 outputs to a workgroup, and its 8 waves share
+// out the columns in runs of U blocks of 128, the next run's codes loaded
+// while this one's are multiplied.  Operands are widened to bfloat16 with
+// their scales applied (exact) and summed by 16x16x32 MFMAs.  A (weights):
+// lane l holds output l % 16; B (tokens): token l % 16; the lane's 32 columns
+// of a block are bytes 16c..16c+15 and 64+16c..64+16c+15, c = l / 16, in both,
+// so that each load covers 64 contiguous bytes of a row.  D: token l % 16,
+// outputs 4c..4c+3.  The waves' sums meet in LDS and are added in their order.
 // ---------------------------------------------------------------------------
-__device__ inline i32x8 load_frag(const uint8_t* row, int c) {
-    const i32x4 lo = *reinterpret_cast<const i32x4*>(row + 16 * c);
-    const i32x4 hi = *reinterpret_cast<const i32x4*>(row + 64 + 16 * c);
-    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+constexpr int kWaves = 8;
+constexpr int kTokens = 4;   // rows that fp8_tokens_kernel takes
+
+__device__ inline i32x8 load_frag(const uint8_t* lo, const uint8_t* hi) {
+    return __builtin_shufflevector(*reinterpret_cast<const i32x4*>(lo), *reinterpret_cast<const i32x4*>(hi), 0, 1, 2,
+                                   3, 4, 5, 6, 7);
 }
 
-template <int YD>
-__global__ __launch_bounds__(64) void fp8_simple_kernel(Fp8Product a) {
-    const int lane = threadIdx.x, r = lane & 15, c = lane >> 4;
-    const int64_t m0 = int64_t(blockIdx.x) * 16, t0 = int64_t(blockIdx.y) * 16;
-    const int64_t m = min(m0 + r, a.M - 1), t = min(t0 + r, a.T - 1);
-    const uint8_t *w = a.w + m * a.ld, *x = a.x + t * a.ld;
-    const uint8_t *ws = a.ws + (m0 / 128) * a.lds, *xs = a.xs + t * a.lds;
-    f32x4 acc = {0, 0, 0, 0};
-    for (uint32_t k = 0; k < a.kb; ++k) {
-        const i32x8 wf = load_frag(w + k * 128, c), xf = load_frag(x + k * 128, c);
-        const float wsc = fp8_scale(ws[k]), xsc = fp8_scale(xs[k]);
+__device__ inline void widen_frag(const i32x8& f, float scale, bf16x8 (&w)[4]) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fp8_widen(wf[2 * j], wf[2 * j + 1], wsc),
-                                                          fp8_widen(xf[2 * j], xf[2 * j + 1], xsc), acc, 0, 0, 0);
+    for (int q = 0; q < 4; ++q) w[q] = fp8_widen(f[2 * q], f[2 * q + 1], scale);
+}
+
+__device__ inline void store_y(const Fp8Product& p, int64_t t, int64_t m, float v) {
+    const int64_t e = t * p.M + m;
+    if (p.ydt == SKETCH_F32)
+        store1_val<SKETCH_F32>(p.Y, e, v);
+    else if (p.ydt == SKETCH_BF16)
+        store1_val<SKETCH_BF16>(p.Y, e, v);
+    else
+        store1_val<SKETCH_F16>(p.Y, e, v);
+}
+
+// The codes of a run of U blocks and RT x 16 outputs, and their scales.
+template <int RT, int U>
+struct WeightRun {
+    i32x8 f[RT][U];
+    uint32_t scales;   // one byte per block
+
+    __device__ inline void load(const Fp8Product& p, const uint8_t* const (&row)[RT], const uint8_t* srow, int c,
+                                uint32_t k0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const size_t at = size_t(min(k0 + u, p.kb - 1)) * 128;
+#pragma unroll
+            for (int i = 0; i < RT; ++i) f[i][u] = load_frag(row[i] + at + 16 * c, row[i] + at + 64 + 16 * c);
+        }
+        scales = U == 4 ? *reinterpret_cast<const uint32_t*>(srow + k0) : *reinterpret_cast<const uint16_t*>(srow + k0);
     }
-    if (t0 + r < a.T)
+};
+
+template <int RT, int NT>
+__device__ inline void add_and_store(const Fp8Product& p, float (*part)[NT * 16][RT * 16 + 1],
+                                     const f32x4 (&acc)[RT][NT], int64_t m0) {
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 15, c = lane >> 4;
 #pragma unroll
-        for (int v = 0; v < 4; ++v)
-            if (m0 + 4 * c + v < a.M) store1_val<YD>(a.Y, (t0 + r) * a.M + m0 + 4 * c + v, acc[v]);
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) part[wave][j * 16 + r][i * 16 + 4 * c + v] = acc[i][j][v];
+    __syncthreads();
+    for (int u = tid; u < RT * 16 * NT * 16; u += kWaves * 64) {
+        const int m = u % (RT * 16), t = u / (RT * 16);
+        if (t >= p.T || m0 + m >= p.M) continue;
+        float sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) sum += part[w][t][m];
+        store_y(p, t, m0 + m, sum);
+    }
+}
+
+// Up to kTokens rows of X (p.x) of dtype XD, encoded by every workgroup for
+// itself, which saves the launch that would encode them first: a wave encodes
+// the blocks of its own run, 16 lanes to a (block, row), into its own part of
+// LDS.  Repeated by all workgroups, this costs more than the launch from about
+// 5 rows on (16 rows of 4096, 688 workgroups: 41 us against 18.5 us in two).
+template <int XD, int RT>
+__global__ __launch_bounds__(kWaves * 64) void fp8_tokens_kernel(Fp8Product p, int64_t N) {
+    constexpr int U = 4, NP = U * kTokens / 4;
+    __shared__ __attribute__((aligned(16))) uint8_t codes[kWaves][4 * NP][128];
+    __shared__ float scales[kWaves][4 * NP];
+    __shared__ float part[kWaves][16][RT * 16 + 1];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int r = lane & 15, c = lane >> 4, T = int(p.T);
+    const int64_t m0 = int64_t(blockIdx.x) * (RT * 16);
+    const uint8_t* row[RT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i) row[i] = p.w + min(m0 + i * 16 + r, p.M - 1) * p.ld;
+    const uint8_t* srow = p.ws + m0 / 128 * p.lds;   // RT * 16 outputs lie in one block of 128
+
+    // (block, row) of X that this lane helps encode in each of the NP turns
+    int xu[NP], xt[NP];
+#pragma unroll
+    for (int n = 0; n < NP; ++n) {
+        const int i = n * 4 + c;
+        xu[n] = i < U * T ? i / T : -1;
+        xt[n] = i < U * T ? i % T : 0;
+    }
+    float xv[NP][8] = {};
+    auto load_x = [&](uint32_t k0) {
+#pragma unroll
+        for (int n = 0; n < NP; ++n)
+            if (xu[n] >= 0) load_row8<XD>(p.x, xt[n], N, int64_t(k0 + xu[n]) * 128 + r * 8, xv[n]);
+    };
+    auto encode_x = [&]() {
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+        for (int n = 0; n < NP; ++n) {
+            const uint32_t b = fp8_scale_byte(max16(max_bits(xv[n])));
+            const int at = n * 4 + c;
+            *reinterpret_cast<uint2*>(&codes[wave][at][(((r >> 1) ^ (at & 7)) << 4) + (r & 1) * 8]) = codes8(xv[n], b);
+            if (r == 0) scales[wave][at] = fp8_scale(b);
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+    };
+    f32x4 acc[RT][1];
+#pragma unroll
+    for (int i = 0; i < RT; ++i) acc[i][0] = f32x4{0, 0, 0, 0};
+    auto multiply = [&](const WeightRun<RT, U>& w, uint32_t k0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (k0 + u >= p.kb) break;
+            const int at = u * T + min(r, T - 1);   // tokens past the last are not stored
+            bf16x8 xw[4], ww[4];
+            widen_frag(load_frag(&codes[wave][at][(c ^ (at & 7)) << 4], &codes[wave][at][((c + 4) ^ (at & 7)) << 4]),
+                       scales[wave][at], xw);
+            const float ws = fp8_scale(w.scales >> (8 * u) & 255u);
+#pragma unroll
+            for (int i = 0; i < RT; ++i) {
+                widen_frag(w.f[i][u], ws, ww);
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    acc[i][0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ww[q], xw[q], acc[i][0], 0, 0, 0);
+            }
+        }
+    };
+    WeightRun<RT, U> w0, w1;
+    uint32_t k = wave * U;
+    if (k < p.kb) {
+        load_x(k);
+        w0.load(p, row, srow, c, k);
+    }
+    while (k < p.kb) {
+        encode_x();
+        uint32_t next = k + kWaves * U;
+        if (next < p.kb) {
+            load_x(next);
+            w1.load(p, row, srow, c, next);
+        }
+        multiply(w0, k);
+        k = next;
+        if (k >= p.kb) break;
+        encode_x();
+        next = k + kWaves * U;
+        if (next < p.kb) {
+            load_x(next);
+            w0.load(p, row, srow, c, next);
+        }
+        multiply(w1, k);
+        k = next;
+    }
+    add_and_store<RT, 1>(p, part, acc, m0);
+}
+
+// Up to 16 NT encoded rows, read from memory (they stay in the caches).  U as
+// in fp8_tokens_kernel for the same number of rows, so that the sums run in
+// the same order.
+template <int RT, int NT, int U>
+__global__ __launch_bounds__(kWaves * 64) void fp8_rows_kernel(Fp8Product p) {
+    __shared__ float part[kWaves][NT * 16][RT * 16 + 1];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int r = lane & 15, c = lane >> 4;
+    const int64_t m0 = int64_t(blockIdx.x) * (RT * 16);
+    const uint8_t* row[RT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i) row[i] = p.w + min(m0 + i * 16 + r, p.M - 1) * p.ld;
+    const uint8_t* srow = p.ws + m0 / 128 * p.lds;
+    const uint8_t *x[NT], *xs[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+        const int64_t t = min(int64_t(j * 16 + r), p.T - 1);
+        x[j] = p.x + t * p.ld;
+        xs[j] = p.xs + t * p.lds;
+    }
+    i32x8 xf[NT][U];
+    uint32_t xsc[NT];
+    auto load_x = [&](uint32_t k0) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const uint8_t* at = x[j] + size_t(min(k0 + u, p.kb - 1)) * 128;
+                xf[j][u] = load_frag(at + 16 * c, at + 64 + 16 * c);
+            }
+            xsc[j] = U == 4 ? *reinterpret_cast<const uint32_t*>(xs[j] + k0)
+                            : *reinterpret_cast<const uint16_t*>(xs[j] + k0);
+        }
+    };
+    f32x4 acc[RT][NT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+    auto multiply = [&](const WeightRun<RT, U>& w, uint32_t k0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (k0 + u >= p.kb) break;
+            bf16x8 ww[RT][4], xw[4];
+#pragma unroll
+            for (int i = 0; i < RT; ++i) widen_frag(w.f[i][u], fp8_scale(w.scales >> (8 * u) & 255u), ww[i]);
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                widen_frag(xf[j][u], fp8_scale(xsc[j] >> (8 * u) & 255u), xw);
+#pragma unroll
+                for (int i = 0; i < RT; ++i)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ww[i][q], xw[q], acc[i][j], 0, 0, 0);
+            }
+        }
+    };
+    WeightRun<RT, U> w0, w1;
+    uint32_t k = wave * U;
+    if (k < p.kb) w0.load(p, row, srow, c, k);
+    while (k < p.kb) {
+        load_x(k);
+        uint32_t next = k + kWaves * U;
+        if (next < p.kb) w1.load(p, row, srow, c, next);
+        multiply(w0, k);
+        k = next;
+        if (k >= p.kb) break;
+        load_x(k);
+        next = k + kWaves * U;
+        if (next < p.kb) w0.load(p, row, srow, c, next);
+        multiply(w1, k);
+        k = next;
+    }
+    add_and_store<RT, NT>(p, part, acc, m0);
+}
+
+template <int RT>
+sketch_status launch_few(const Fp8Product& p, int x_dtype, int64_t N, hipStream_t st) {
+    const unsigned grid = unsigned((p.M + RT * 16 - 1) / (RT * 16));
+    auto tokens = [&](auto kernel) {
+        kernel<<<grid, kWaves * 64, 0, st>>>(p, N);
+        return launch_status();
+    };
+    auto rows = [&](auto kernel) {
+        kernel<<<grid, kWaves * 64, 0, st>>>(p);
+        return launch_status();
+    };
+    switch (x_dtype) {
+        case SKETCH_F32: return tokens(fp8_tokens_kernel<SKETCH_F32, RT>);
+        case SKETCH_BF16: return tokens(fp8_tokens_kernel<SKETCH_BF16, RT>);
+        case SKETCH_F16: return tokens(fp8_tokens_kernel<SKETCH_F16, RT>);
+    }
+    if (p.T <= kTokens) return rows(fp8_rows_kernel<RT, 1, 4>);
+    return p.T <= 16   ? rows(fp8_rows_kernel<RT, 1, 2>)
+           : p.T <= 32 ? rows(fp8_rows_kernel<RT, 2, 2>)
+                       : rows(fp8_rows_kernel<RT, 4, 2>);
 }
 
 bool valid_dtype(int d) { return d == SKETCH_F32 || d == SKETCH_BF16 || d == SKETCH_F16; }
@@ -161,20 +432,18 @@ sketch_status fp8_shape(const sketch_fp8_params* p, sketch_fp8_shape* s) {
 
 sketch_status launch_fp8_encode(const sketch_fp8_params* p, const sketch_fp8_shape& s, const void* W,
                                 sketch_dtype dt, void* buf, int32_t* status, hipStream_t st) {
-    EncodeArgs a{W, static_cast<uint8_t*>(buf), status, p->M, p->N, s.ld, s.lds, (p->M + 127) / 128, s.col_blocks,
-                 s.scales_offset, s.bytes};
-    const int64_t grid = a.lds * a.tiles_m * (p->count > 1 ? p->count : 1);
-    if (grid > 0x7FFFFFFF) return SKETCH_EINVAL;
+    EncodeArgs a{W, static_cast<uint8_t*>(buf), status, p->M, p->N, s.ld, s.lds, s.row_blocks, s.col_blocks,
+                 p->count > 1 ? p->count : 1, s.scales_offset, s.bytes};
     const bool rows = p->block_rows == 1;
+    const int64_t blocks = a.lds * a.row_blocks * a.count, grid = rows ? (blocks + 15) / 16 : blocks;
+    if (grid > 0x7FFFFFFF) return SKETCH_EINVAL;
     auto go = [&](auto kernel) {
         kernel<<<unsigned(grid), 256, 0, st>>>(a);
         return launch_status();
     };
-    if (dt == SKETCH_F32)
-        return rows ? go(fp8_encode_kernel<SKETCH_F32, true>) : go(fp8_encode_kernel<SKETCH_F32, false>);
-    if (dt == SKETCH_BF16)
-        return rows ? go(fp8_encode_kernel<SKETCH_BF16, true>) : go(fp8_encode_kernel<SKETCH_BF16, false>);
-    return rows ? go(fp8_encode_kernel<SKETCH_F16, true>) : go(fp8_encode_kernel<SKETCH_F16, false>);
+    if (dt == SKETCH_F32) return rows ? go(fp8_encode_rows_kernel<SKETCH_F32>) : go(fp8_encode_kernel<SKETCH_F32>);
+    if (dt == SKETCH_BF16) return rows ? go(fp8_encode_rows_kernel<SKETCH_BF16>) : go(fp8_encode_kernel<SKETCH_BF16>);
+    return rows ? go(fp8_encode_rows_kernel<SKETCH_F16>) : go(fp8_encode_kernel<SKETCH_F16>);
 }
 
 }  // namespace sketch
@@ -211,7 +480,7 @@ sketch_status sketch_fp8_workspace_bytes(const sketch_fp8_params* p, int64_t bat
     if (rc != SKETCH_OK) return rc;
     *bytes = 0;
     if (batch == 0 || p->M == 0) return SKETCH_OK;
-    if (x_dtype != SKETCH_FP8_ROWS) *bytes += xs.bytes;
+    if (x_dtype != SKETCH_FP8_ROWS && batch > kTokens) *bytes += xs.bytes;
     if (batch > SKETCH_FP8_EXACT_BATCH) *bytes += fp8_gemm_workspace(p->M, batch, uint32_t(s.col_blocks), y_dtype);
     return SKETCH_OK;
 }
@@ -235,7 +504,8 @@ sketch_status sketch_fp8_matmul(const sketch_fp8_params* p, const void* buf, con
     (void)fp8_shape(&xp, &xs);
     const uint8_t *w8 = static_cast<const uint8_t*>(buf), *x8 = static_cast<const uint8_t*>(X);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    if (x_dtype != SKETCH_FP8_ROWS) {
+    const bool encode = x_dtype != SKETCH_FP8_ROWS && batch > kTokens;
+    if (encode) {
         rc = launch_fp8_encode(&xp, xs, X, sketch_dtype(x_dtype), ws, nullptr, st);
         if (rc != SKETCH_OK) return rc;
         x8 = ws;
@@ -244,14 +514,8 @@ sketch_status sketch_fp8_matmul(const sketch_fp8_params* p, const void* buf, con
     const Fp8Product a{w8, w8 + s.scales_offset, x8, x8 + xs.scales_offset, Y, p->M, batch, s.ld, s.lds,
                        uint32_t(s.col_blocks), int(y_dtype)};
     if (batch > SKETCH_FP8_EXACT_BATCH) return launch_fp8_gemm(a, ws, st);
-    const dim3 grid(unsigned((p->M + 15) / 16), unsigned((batch + 15) / 16));
-    auto go = [&](auto kernel) {
-        kernel<<<grid, 64, 0, st>>>(a);
-        return launch_status();
-    };
-    return y_dtype == SKETCH_F32    ? go(fp8_simple_kernel<SKETCH_F32>)
-           : y_dtype == SKETCH_BF16 ? go(fp8_simple_kernel<SKETCH_BF16>)
-                                    : go(fp8_simple_kernel<SKETCH_F16>);
+    const int few = encode ? int(SKETCH_FP8_ROWS) : x_dtype;
+    return p->M >= 64 * int64_t(compute_units()) ? launch_few<2>(a, few, p->N, st) : launch_few<1>(a, few, p->N, st);
 }
 
 }  // extern "C"
