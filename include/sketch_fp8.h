@@ -96,14 +96,13 @@ sketch_status sketch_fp8_workspace_bytes(const sketch_fp8_params* p, int64_t bat
  *            several linears share.  Both give the same bits.
  *   Y        [batch][M] of y_dtype, overwritten (rounded once from float32).
  * Products of e4m3 codes are exact.  With y_dtype SKETCH_F32 they are summed
- * in float32.  With a 16-bit y_dtype and more than SKETCH_FP8_EXACT_BATCH rows
- * the sums run on the e4m3 matrix cores, which add 8 neighbouring products at
- * a time with 13 bits below the largest of them and those sums in float32:
- * within sum over the groups of 8 of 7 * 2^-13 * max |product|, far below the
- * rounding of Y.  A row of X that holds NaN or an infinity gives a row of NaN
- * in Y; other rows are unaffected.  batch == 0 or M == 0 is a no-op.
+ * in float32, on the bfloat16 matrix cores.  With a 16-bit y_dtype the sums run
+ * on the e4m3 matrix cores, twice as fast, which add 8 neighbouring products
+ * at a time with 13 bits below the largest of them, and those sums in float32:
+ * within the sum, over the groups of 8, of 7 * 2^-13 * max |product|, far below
+ * the rounding of Y.  A row of X that holds NaN or an infinity gives a row of
+ * NaN in Y; other rows are unaffected.  batch == 0 or M == 0 is a no-op.
  */
-#define SKETCH_FP8_EXACT_BATCH 64
 sketch_status sketch_fp8_matmul(const sketch_fp8_params* p, const void* buf, const void* X, int x_dtype,
                                 int64_t batch, void* Y, sketch_dtype y_dtype, void* workspace,
                                 size_t workspace_bytes, void* stream);

@@ -150,16 +150,22 @@ __global__ __launch_bounds__(256) void fp8_encode_rows_kernel(EncodeArgs a) {
 
 // ---------------------------------------------------------------------------
 // Products of few rows.  Bound by the codes of W coming from memory, so every
-// code is read once, 16 or 32 outputs to a workgroup, and its 8 waves share
-// out the columns in runs of U blocks of 128, the next run's codes loaded
-// while this one's are multiplied.  Operands are widened to bfloat16 with
-// their scales applied (exact) and summed by 16x16x32 MFMAs.  A (weights):
-// lane l holds output l % 16; B (tokens): token l % 16; the lane's 32 columns
-// of a block are bytes 16c..16c+15 and 64+16c..64+16c+15, c = l / 16, in both,
-// so that each load covers 64 contiguous bytes of a row.  D: token l % 16,
-// outputs 4c..4c+3.  The waves' sums meet in LDS and are added in their order.
+// code is read once: a workgroup has 16 or 32 outputs, and its 8 waves share
+// out the columns in runs of 4 blocks of 128.  A fragment is 16 rows x 128
+// columns, one row to a lane: lane l holds row l % 16 and the columns
+// 16c..16c+15 and 64+16c..64+16c+15, c = l / 16, the same ones of outputs (A)
+// and tokens (B), so that each load covers 64 contiguous bytes of a row.
+// D: token l % 16, outputs 4c..4c+3.  The waves' sums meet in LDS and are
+// added in their order.
+//
+// EXACT (float32 Y): both fragments are widened to bfloat16 with their scales
+// applied, four 16x16x32 MFMAs, exact products, float32 sums.  Otherwise one
+// 16x16x128 MFMA on the codes, which applies the scales itself: its sums of 8
+// neighbouring products keep 13 bits below the largest, which a 16-bit Y does
+// not show, and nothing is spent on widening.
 // ---------------------------------------------------------------------------
 constexpr int kWaves = 8;
+constexpr int kRun = 4;      // blocks of 128 columns in a wave's run
 constexpr int kTokens = 4;   // rows that fp8_tokens_kernel takes
 
 __device__ inline i32x8 load_frag(const uint8_t* lo, const uint8_t* hi) {
@@ -167,9 +173,18 @@ __device__ inline i32x8 load_frag(const uint8_t* lo, const uint8_t* hi) {
                                    3, 4, 5, 6, 7);
 }
 
-__device__ inline void widen_frag(const i32x8& f, float scale, bf16x8 (&w)[4]) {
+// acc += A B for a block: the fragments and their scale bytes.
+template <bool EXACT>
+__device__ inline f32x4 multiply(const i32x8& a, uint32_t as, const i32x8& b, uint32_t bs, f32x4 acc) {
+    if constexpr (EXACT) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) w[q] = fp8_widen(f[2 * q], f[2 * q + 1], scale);
+        for (int q = 0; q < 4; ++q)
+            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fp8_widen(a[2 * q], a[2 * q + 1], fp8_scale(as)),
+                                                          fp8_widen(b[2 * q], b[2 * q + 1], fp8_scale(bs)), acc, 0, 0, 0);
+        return acc;
+    } else {
+        return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, acc, 0, 0, 0, int(as), 0, int(bs));
+    }
 }
 
 __device__ inline void store_y(const Fp8Product& p, int64_t t, int64_t m, float v) {
@@ -182,38 +197,42 @@ __device__ inline void store_y(const Fp8Product& p, int64_t t, int64_t m, float 
         store1_val<SKETCH_F16>(p.Y, e, v);
 }
 
-// The codes of a run of U blocks and RT x 16 outputs, and their scales.
-template <int RT, int U>
-struct WeightRun {
-    i32x8 f[RT][U];
-    uint32_t scales;   // one byte per block
+// The codes of a run for RT x 16 outputs, and its scale bytes.  Blocks past
+// the last are read as the last and not used.
+template <int RT>
+struct Run {
+    i32x8 f[RT][kRun];
+    uint32_t scales;
 
-    __device__ inline void load(const Fp8Product& p, const uint8_t* const (&row)[RT], const uint8_t* srow, int c,
-                                uint32_t k0) {
+    __device__ inline void load(const uint8_t* const (&row)[RT], const uint8_t* srow, int c, uint32_t k0, uint32_t kb) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const size_t at = size_t(min(k0 + u, p.kb - 1)) * 128;
+        for (int u = 0; u < kRun; ++u) {
+            const size_t at = size_t(min(k0 + u, kb - 1)) * 128;
 #pragma unroll
             for (int i = 0; i < RT; ++i) f[i][u] = load_frag(row[i] + at + 16 * c, row[i] + at + 64 + 16 * c);
         }
-        scales = U == 4 ? *reinterpret_cast<const uint32_t*>(srow + k0) : *reinterpret_cast<const uint16_t*>(srow + k0);
+        scales = *reinterpret_cast<const uint32_t*>(srow + k0);
     }
 };
 
-template <int RT, int NT>
-__device__ inline void add_and_store(const Fp8Product& p, float (*part)[NT * 16][RT * 16 + 1],
-                                     const f32x4 (&acc)[RT][NT], int64_t m0) {
+template <int RT>
+__device__ inline void weight_rows(const Fp8Product& p, int64_t m0, int r, const uint8_t* (&row)[RT]) {
+#pragma unroll
+    for (int i = 0; i < RT; ++i) row[i] = p.w + min(m0 + i * 16 + r, p.M - 1) * p.ld;
+}
+
+template <int RT>
+__device__ inline void add_and_store(const Fp8Product& p, float (*part)[16][RT * 16 + 1], const f32x4 (&acc)[RT],
+                                     int64_t m0) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 15, c = lane >> 4;
 #pragma unroll
     for (int i = 0; i < RT; ++i)
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int v = 0; v < 4; ++v) part[wave][j * 16 + r][i * 16 + 4 * c + v] = acc[i][j][v];
+        for (int v = 0; v < 4; ++v) part[wave][r][i * 16 + 4 * c + v] = acc[i][v];
     __syncthreads();
-    for (int u = tid; u < RT * 16 * NT * 16; u += kWaves * 64) {
-        const int m = u % (RT * 16), t = u / (RT * 16);
-        if (t >= p.T || m0 + m >= p.M) continue;
+    if (tid < RT * 256) {
+        const int m = tid % (RT * 16), t = tid / (RT * 16);
+        if (t >= p.T || m0 + m >= p.M) return;
         float sum = 0.0f;
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) sum += part[w][t][m];
@@ -221,196 +240,107 @@ __device__ inline void add_and_store(const Fp8Product& p, float (*part)[NT * 16]
     }
 }
 
-// Up to kTokens rows of X (p.x) of dtype XD, encoded by every workgroup for
-// itself, which saves the launch that would encode them first: a wave encodes
-// the blocks of its own run, 16 lanes to a (block, row), into its own part of
-// LDS.  Repeated by all workgroups, this costs more than the launch from about
-// 5 rows on (16 rows of 4096, 688 workgroups: 41 us against 18.5 us in two).
-template <int XD, int RT>
+// Up to NP rows of X (p.x, of dtype XD), encoded by every workgroup for itself,
+// which saves the launch that would encode them first: a wave encodes the
+// blocks of its own run, 16 lanes to a (block, row), into its own part of LDS.
+// Repeated by all workgroups, this costs more than the launch beyond a few
+// rows (28672 x 8192, 16 rows: 114 us against 66 us in two launches).
+template <int XD, bool EXACT, int NP>
 __global__ __launch_bounds__(kWaves * 64) void fp8_tokens_kernel(Fp8Product p, int64_t N) {
-    constexpr int U = 4, NP = U * kTokens / 4;
     __shared__ __attribute__((aligned(16))) uint8_t codes[kWaves][4 * NP][128];
-    __shared__ float scales[kWaves][4 * NP];
-    __shared__ float part[kWaves][16][RT * 16 + 1];
+    __shared__ uint32_t scales[kWaves][4 * NP];
+    __shared__ float part[kWaves][16][17];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r = lane & 15, c = lane >> 4, T = int(p.T);
-    const int64_t m0 = int64_t(blockIdx.x) * (RT * 16);
-    const uint8_t* row[RT];
+    const int64_t m0 = int64_t(blockIdx.x) * 16;
+    const uint8_t* row[1];
+    weight_rows<1>(p, m0, r, row);
+    const uint8_t* srow = p.ws + m0 / 128 * p.lds;
+    f32x4 acc[1] = {f32x4{0, 0, 0, 0}};
+    for (uint32_t k = wave * kRun; k < p.kb; k += kWaves * kRun) {
+        float x[NP][8] = {};
 #pragma unroll
-    for (int i = 0; i < RT; ++i) row[i] = p.w + min(m0 + i * 16 + r, p.M - 1) * p.ld;
-    const uint8_t* srow = p.ws + m0 / 128 * p.lds;   // RT * 16 outputs lie in one block of 128
-
-    // (block, row) of X that this lane helps encode in each of the NP turns
-    int xu[NP], xt[NP];
-#pragma unroll
-    for (int n = 0; n < NP; ++n) {
-        const int i = n * 4 + c;
-        xu[n] = i < U * T ? i / T : -1;
-        xt[n] = i < U * T ? i % T : 0;
-    }
-    float xv[NP][8] = {};
-    auto load_x = [&](uint32_t k0) {
-#pragma unroll
-        for (int n = 0; n < NP; ++n)
-            if (xu[n] >= 0) load_row8<XD>(p.x, xt[n], N, int64_t(k0 + xu[n]) * 128 + r * 8, xv[n]);
-    };
-    auto encode_x = [&]() {
+        for (int n = 0; n < NP; ++n) {   // (block, row) number 4 n + c of the run
+            const int i = n * 4 + c;
+            if (i < kRun * T) load_row8<XD>(p.x, i % T, N, int64_t(k + i / T) * 128 + r * 8, x[n]);
+        }
+        Run<1> w;
+        w.load(row, srow, c, k, p.kb);
+        asm volatile("" ::: "memory");   // all loads of the run before its first use
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
         for (int n = 0; n < NP; ++n) {
-            const uint32_t b = fp8_scale_byte(max16(max_bits(xv[n])));
+            const uint32_t b = fp8_scale_byte(max16(max_bits(x[n])));
             const int at = n * 4 + c;
-            *reinterpret_cast<uint2*>(&codes[wave][at][(((r >> 1) ^ (at & 7)) << 4) + (r & 1) * 8]) = codes8(xv[n], b);
-            if (r == 0) scales[wave][at] = fp8_scale(b);
+            *reinterpret_cast<uint2*>(&codes[wave][at][(((r >> 1) ^ (at & 7)) << 4) + (r & 1) * 8]) = codes8(x[n], b);
+            if (r == 0) scales[wave][at] = b;
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
-    };
-    f32x4 acc[RT][1];
 #pragma unroll
-    for (int i = 0; i < RT; ++i) acc[i][0] = f32x4{0, 0, 0, 0};
-    auto multiply = [&](const WeightRun<RT, U>& w, uint32_t k0) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (k0 + u >= p.kb) break;
+        for (int u = 0; u < kRun; ++u) {
+            if (k + u >= p.kb) break;
             const int at = u * T + min(r, T - 1);   // tokens past the last are not stored
-            bf16x8 xw[4], ww[4];
-            widen_frag(load_frag(&codes[wave][at][(c ^ (at & 7)) << 4], &codes[wave][at][((c + 4) ^ (at & 7)) << 4]),
-                       scales[wave][at], xw);
-            const float ws = fp8_scale(w.scales >> (8 * u) & 255u);
-#pragma unroll
-            for (int i = 0; i < RT; ++i) {
-                widen_frag(w.f[i][u], ws, ww);
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    acc[i][0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ww[q], xw[q], acc[i][0], 0, 0, 0);
-            }
+            const i32x8 xf = load_frag(&codes[wave][at][(c ^ (at & 7)) << 4], &codes[wave][at][((c + 4) ^ (at & 7)) << 4]);
+            acc[0] = multiply<EXACT>(w.f[0][u], w.scales >> (8 * u) & 255u, xf, scales[wave][at], acc[0]);
         }
-    };
-    WeightRun<RT, U> w0, w1;
-    uint32_t k = wave * U;
-    if (k < p.kb) {
-        load_x(k);
-        w0.load(p, row, srow, c, k);
     }
-    while (k < p.kb) {
-        encode_x();
-        uint32_t next = k + kWaves * U;
-        if (next < p.kb) {
-            load_x(next);
-            w1.load(p, row, srow, c, next);
-        }
-        multiply(w0, k);
-        k = next;
-        if (k >= p.kb) break;
-        encode_x();
-        next = k + kWaves * U;
-        if (next < p.kb) {
-            load_x(next);
-            w0.load(p, row, srow, c, next);
-        }
-        multiply(w1, k);
-        k = next;
-    }
-    add_and_store<RT, 1>(p, part, acc, m0);
+    add_and_store<1>(p, part, acc, m0);
 }
 
-// Up to 16 NT encoded rows, read from memory (they stay in the caches).  U as
-// in fp8_tokens_kernel for the same number of rows, so that the sums run in
-// the same order.
-template <int RT, int NT, int U>
+// Up to 16 encoded rows, read from memory (they stay in the caches).  The
+// sums run in the same order as in fp8_tokens_kernel.
+template <int RT, bool EXACT>
 __global__ __launch_bounds__(kWaves * 64) void fp8_rows_kernel(Fp8Product p) {
-    __shared__ float part[kWaves][NT * 16][RT * 16 + 1];
+    __shared__ float part[kWaves][16][RT * 16 + 1];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r = lane & 15, c = lane >> 4;
     const int64_t m0 = int64_t(blockIdx.x) * (RT * 16);
     const uint8_t* row[RT];
+    weight_rows<RT>(p, m0, r, row);
+    const uint8_t* srow = p.ws + m0 / 128 * p.lds;   // RT * 16 outputs lie in one block of 128
+    const int64_t t = min(int64_t(r), p.T - 1);
+    const uint8_t* x[1] = {p.x + t * p.ld};
+    const uint8_t* xs = p.xs + t * p.lds;
+    f32x4 acc[RT];
 #pragma unroll
-    for (int i = 0; i < RT; ++i) row[i] = p.w + min(m0 + i * 16 + r, p.M - 1) * p.ld;
-    const uint8_t* srow = p.ws + m0 / 128 * p.lds;
-    const uint8_t *x[NT], *xs[NT];
+    for (int i = 0; i < RT; ++i) acc[i] = f32x4{0, 0, 0, 0};
+    for (uint32_t k = wave * kRun; k < p.kb; k += kWaves * kRun) {
+        Run<RT> w;
+        Run<1> xr;
+        w.load(row, srow, c, k, p.kb);
+        xr.load(x, xs, c, k, p.kb);
+        asm volatile("" ::: "memory");   // all loads of the run before its first use
 #pragma unroll
-    for (int j = 0; j < NT; ++j) {
-        const int64_t t = min(int64_t(j * 16 + r), p.T - 1);
-        x[j] = p.x + t * p.ld;
-        xs[j] = p.xs + t * p.lds;
-    }
-    i32x8 xf[NT][U];
-    uint32_t xsc[NT];
-    auto load_x = [&](uint32_t k0) {
+        for (int u = 0; u < kRun; ++u) {
+            if (k + u >= p.kb) break;
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const uint8_t* at = x[j] + size_t(min(k0 + u, p.kb - 1)) * 128;
-                xf[j][u] = load_frag(at + 16 * c, at + 64 + 16 * c);
-            }
-            xsc[j] = U == 4 ? *reinterpret_cast<const uint32_t*>(xs[j] + k0)
-                            : *reinterpret_cast<const uint16_t*>(xs[j] + k0);
+            for (int i = 0; i < RT; ++i)
+                acc[i] = multiply<EXACT>(w.f[i][u], w.scales >> (8 * u) & 255u, xr.f[0][u], xr.scales >> (8 * u) & 255u,
+                                         acc[i]);
         }
-    };
-    f32x4 acc[RT][NT];
-#pragma unroll
-    for (int i = 0; i < RT; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
-    auto multiply = [&](const WeightRun<RT, U>& w, uint32_t k0) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (k0 + u >= p.kb) break;
-            bf16x8 ww[RT][4], xw[4];
-#pragma unroll
-            for (int i = 0; i < RT; ++i) widen_frag(w.f[i][u], fp8_scale(w.scales >> (8 * u) & 255u), ww[i]);
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                widen_frag(xf[j][u], fp8_scale(xsc[j] >> (8 * u) & 255u), xw);
-#pragma unroll
-                for (int i = 0; i < RT; ++i)
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ww[i][q], xw[q], acc[i][j], 0, 0, 0);
-            }
-        }
-    };
-    WeightRun<RT, U> w0, w1;
-    uint32_t k = wave * U;
-    if (k < p.kb) w0.load(p, row, srow, c, k);
-    while (k < p.kb) {
-        load_x(k);
-        uint32_t next = k + kWaves * U;
-        if (next < p.kb) w1.load(p, row, srow, c, next);
-        multiply(w0, k);
-        k = next;
-        if (k >= p.kb) break;
-        load_x(k);
-        next = k + kWaves * U;
-        if (next < p.kb) w0.load(p, row, srow, c, next);
-        multiply(w1, k);
-        k = next;
     }
-    add_and_store<RT, NT>(p, part, acc, m0);
+    add_and_store<RT>(p, part, acc, m0);
 }
 
-template <int RT>
+template <bool EXACT>
 sketch_status launch_few(const Fp8Product& p, int x_dtype, int64_t N, hipStream_t st) {
-    const unsigned grid = unsigned((p.M + RT * 16 - 1) / (RT * 16));
     auto tokens = [&](auto kernel) {
-        kernel<<<grid, kWaves * 64, 0, st>>>(p, N);
+        kernel<<<unsigned((p.M + 15) / 16), kWaves * 64, 0, st>>>(p, N);
         return launch_status();
     };
-    auto rows = [&](auto kernel) {
-        kernel<<<grid, kWaves * 64, 0, st>>>(p);
+    auto rows = [&](auto kernel, int64_t outputs) {
+        kernel<<<unsigned((p.M + outputs - 1) / outputs), kWaves * 64, 0, st>>>(p);
         return launch_status();
     };
-    switch (x_dtype) {
-        case SKETCH_F32: return tokens(fp8_tokens_kernel<SKETCH_F32, RT>);
-        case SKETCH_BF16: return tokens(fp8_tokens_kernel<SKETCH_BF16, RT>);
-        case SKETCH_F16: return tokens(fp8_tokens_kernel<SKETCH_F16, RT>);
-    }
-    if (p.T <= kTokens) return rows(fp8_rows_kernel<RT, 1, 4>);
-    return p.T <= 16   ? rows(fp8_rows_kernel<RT, 1, 2>)
-           : p.T <= 32 ? rows(fp8_rows_kernel<RT, 2, 2>)
-                       : rows(fp8_rows_kernel<RT, 4, 2>);
+    if (x_dtype == SKETCH_F32)
+        return p.T == 1 ? tokens(fp8_tokens_kernel<SKETCH_F32, EXACT, 1>) : tokens(fp8_tokens_kernel<SKETCH_F32, EXACT, 4>);
+    if (x_dtype == SKETCH_BF16)
+        return p.T == 1 ? tokens(fp8_tokens_kernel<SKETCH_BF16, EXACT, 1>) : tokens(fp8_tokens_kernel<SKETCH_BF16, EXACT, 4>);
+    if (x_dtype == SKETCH_F16)
+        return p.T == 1 ? tokens(fp8_tokens_kernel<SKETCH_F16, EXACT, 1>) : tokens(fp8_tokens_kernel<SKETCH_F16, EXACT, 4>);
+    // 32 outputs to a workgroup halve the reads of X; with few workgroups 16 fill the chip better
+    return p.M >= 64 * int64_t(compute_units()) ? rows(fp8_rows_kernel<2, EXACT>, 32) : rows(fp8_rows_kernel<1, EXACT>, 16);
 }
 
 bool valid_dtype(int d) { return d == SKETCH_F32 || d == SKETCH_BF16 || d == SKETCH_F16; }
@@ -481,7 +411,7 @@ sketch_status sketch_fp8_workspace_bytes(const sketch_fp8_params* p, int64_t bat
     *bytes = 0;
     if (batch == 0 || p->M == 0) return SKETCH_OK;
     if (x_dtype != SKETCH_FP8_ROWS && batch > kTokens) *bytes += xs.bytes;
-    if (batch > SKETCH_FP8_EXACT_BATCH) *bytes += fp8_gemm_workspace(p->M, batch, uint32_t(s.col_blocks), y_dtype);
+    if (batch > 16) *bytes += fp8_gemm_workspace(p->M, batch, uint32_t(s.col_blocks), y_dtype);
     return SKETCH_OK;
 }
 
@@ -513,9 +443,9 @@ sketch_status sketch_fp8_matmul(const sketch_fp8_params* p, const void* buf, con
     }
     const Fp8Product a{w8, w8 + s.scales_offset, x8, x8 + xs.scales_offset, Y, p->M, batch, s.ld, s.lds,
                        uint32_t(s.col_blocks), int(y_dtype)};
-    if (batch > SKETCH_FP8_EXACT_BATCH) return launch_fp8_gemm(a, ws, st);
+    if (batch > 16) return launch_fp8_gemm(a, ws, st);
     const int few = encode ? int(SKETCH_FP8_ROWS) : x_dtype;
-    return p->M >= 64 * int64_t(compute_units()) ? launch_few<2>(a, few, p->N, st) : launch_few<1>(a, few, p->N, st);
+    return y_dtype == SKETCH_F32 ? launch_few<true>(a, few, p->N, st) : launch_few<false>(a, few, p->N, st);
 }
 
 }  // extern "C"
