@@ -12,29 +12,6 @@
 namespace sketch {
 namespace {
 
-// 8 elements of a row from column c0 on, zeros past its end.  Rows of any
-// length: the wide loads need only the alignment of an element (7.6 us
-// element by element -> 4.1 us for 517 x 4001 float32).
-template <int DT>
-__device__ inline void load_row8(const void* W, int64_t row, int64_t N, int64_t c0, float (&v)[8]) {
-    if (c0 + 8 <= N) {
-        typedef uint32_t loose __attribute__((ext_vector_type(4), aligned(2)));
-        constexpr int es = DT == SKETCH_F32 ? 4 : 2;
-        const loose* at = reinterpret_cast<const loose*>(static_cast<const char*>(W) + (row * N + c0) * es);
-        const loose a = at[0], b = DT == SKETCH_F32 ? at[1] : a;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const uint32_t h = (a[e >> 1] >> ((e & 1) * 16)) & 0xFFFFu;
-            v[e] = DT == SKETCH_F32    ? __uint_as_float(e < 4 ? a[e & 3] : b[e & 3])
-                   : DT == SKETCH_BF16 ? bf16_bits_to_f32(h)
-                                       : f16_bits_to_f32(h);
-        }
-        return;
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = c0 + e < N ? load_elem<DT>(W, row * N + c0 + e) : 0.0f;
-}
-
 // Largest magnitude's bits; magnitudes compare as their bits, NaN above infinity.
 __device__ inline uint32_t max_bits(const float (&v)[8]) {
     uint32_t m = 0;

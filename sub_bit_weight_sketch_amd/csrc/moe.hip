@@ -11,8 +11,8 @@
 // over.  The split is exact, and so is e4m3 in bfloat16, so the products are
 // exact and are summed in float32.
 //
-// Three launches: the logits (one workgroup per expert) and the split of x;
-// gate and up; down and the weighted sum.
+// Three launches: the logits and the split of x; gate and up; down and the
+// weighted sum; and a fourth that adds the parts where down is split.
 #include "fp8.h"
 
 namespace sketch {
@@ -41,10 +41,12 @@ struct MoeArgs {
     uint16_t* xs;        // [terms][T][ldh] bfloat16
     uint16_t* hs;        // [3][T * topk][ldi] bfloat16
     Route* route;
+    float* parts;        // [splits][T][H], the down kernel's sums
     int64_t H, I, ldh, ldi;
     size_t gu_bytes, gu_scales, d_bytes, d_scales;   // one matrix, and its scales' offset
     int32_t gu_lds, d_lds;
     int32_t T, E, topk, renorm;
+    int32_t splits, groups;   // of the down kernel
 };
 
 template <int DT> constexpr int x_terms() { return DT == SKETCH_BF16 ? 1 : DT == SKETCH_F16 ? 2 : 3; }
@@ -56,28 +58,47 @@ __device__ inline uint16_t take_bf16(float& v) {
     return uint16_t(u >> 16);
 }
 
-template <int DT>
+// Logits of expert blockIdx.x for NT tokens; the sums are float64,
+// so that no two logits change places by rounding.  All workgroups also share
+// out the split of x.
+template <int DT, int NT>
 __global__ __launch_bounds__(256) void moe_logits_kernel(MoeArgs a) {
-    __shared__ double part[4][SKETCH_MOE_MAX_TOKENS];
-    const int tid = threadIdx.x, wave = tid >> 6, e = blockIdx.x;
-    const int64_t total = int64_t(a.T) * a.ldh;
-    for (int64_t u = int64_t(e) * 256 + tid; u < total; u += int64_t(a.E) * 256) {
-        const int64_t t = u / a.ldh, j = u % a.ldh;
-        float v = j < a.H ? load_elem<DT>(a.X, t * a.H + j) : 0.0f;
+    __shared__ double part[4][NT];
+    const int tid = threadIdx.x, e = blockIdx.x, t0 = blockIdx.y * NT;
+    double sum[NT] = {};
+    for (int64_t j = tid * 8; j < a.H; j += 2048) {
+        float w[8], x[NT][8];
+        load_row8<DT>(a.router, e, a.H, j, w);
 #pragma unroll
-        for (int s = 0; s < x_terms<DT>(); ++s)
-            a.xs[s * total + u] = DT == SKETCH_BF16 && j < a.H ? static_cast<const uint16_t*>(a.X)[t * a.H + j] : take_bf16(v);
+        for (int i = 0; i < NT; ++i) load_row8<DT>(a.X, min(t0 + i, a.T - 1), a.H, j, x[i]);
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+#pragma unroll
+            for (int i = 0; i < NT; ++i) sum[i] += double(x[i][q]) * double(w[q]);
     }
-    for (int t = 0; t < a.T; ++t) {
-        double sum = 0.0;
-        for (int64_t j = tid; j < a.H; j += 256)
-            sum += double(load_elem<DT>(a.X, t * a.H + j)) * double(load_elem<DT>(a.router, e * a.H + j));
 #pragma unroll
-        for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
-        if ((tid & 63) == 0) part[wave][t] = sum;
+    for (int i = 0; i < NT; ++i) {
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) sum[i] += __shfl_xor(sum[i], d);
+        if ((tid & 63) == 0) part[tid >> 6][i] = sum[i];
+    }
+    const int64_t total = int64_t(a.T) * a.ldh, step = int64_t(gridDim.x) * gridDim.y * 2048;
+    for (int64_t u = (int64_t(blockIdx.y) * gridDim.x + e) * 2048 + tid * 8; u < total; u += step) {
+        const int64_t t = u / a.ldh, j = u % a.ldh;   // ldh is a multiple of 8
+        float v[8];
+        load_row8<DT>(a.X, t, a.H, j, v);
+#pragma unroll
+        for (int s = 0; s < x_terms<DT>(); ++s) {
+            uint32_t h[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) h[q] = take_bf16(v[q]);
+            *reinterpret_cast<u32x4*>(a.xs + s * total + u) =
+                u32x4{h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16)};
+        }
     }
     __syncthreads();
-    if (tid < a.T) a.logits[int64_t(tid) * a.E + e] = (part[0][tid] + part[1][tid]) + (part[2][tid] + part[3][tid]);
+    if (tid < NT && t0 + tid < a.T)
+        a.logits[int64_t(t0 + tid) * a.E + e] = (part[0][tid] + part[1][tid]) + (part[2][tid] + part[3][tid]);
 }
 
 // Order of the logits as unsigned integers; NaN is the largest, 0 is free.
@@ -87,51 +108,46 @@ __device__ inline uint64_t order_key(double l) {
     return u >> 63 ? ~u : u | (1ull << 63);
 }
 
-// The top k of every token and the segments, by all 512 threads of a
-// workgroup.  Workgroup 0 also computes the weights and hands everything on.
-__device__ void build_route(const MoeArgs& a, Route& rt, int32_t* ids, bool publish) {
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    constexpr int kPer = SKETCH_MOE_MAX_EXPERTS / 64;
-    for (int t = wave; t < a.T; t += kWaves) {
-        const double* l = a.logits + int64_t(t) * a.E;
-        uint64_t key[kPer];
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) key[i] = lane + 64 * i < a.E ? order_key(l[lane + 64 * i]) : 0;
-        for (int s = 0; s < a.topk; ++s) {
-            uint64_t best = key[0];
-            int at = lane;
-#pragma unroll
-            for (int i = 1; i < kPer; ++i)
-                if (key[i] > best) best = key[i], at = lane + 64 * i;
-#pragma unroll
-            for (int d = 1; d < 64; d <<= 1) {
-                const uint64_t ob = __shfl_xor(best, d);
-                const int oa = __shfl_xor(at, d);
-                if (ob > best || (ob == best && oa < at)) best = ob, at = oa;
-            }
-            if (lane == 0) ids[t * a.topk + s] = at;
-#pragma unroll
-            for (int i = 0; i < kPer; ++i)
-                if (at == lane + 64 * i) key[i] = 0;
+// The top k of one token, by one wave.
+__device__ inline void top_k(const double* l, int E, int topk, int lane, int32_t* ids) {
+    if (E <= 64) {   // each lane counts the experts before its own
+        const uint64_t key = lane < E ? order_key(l[lane]) : 0;
+        int rank = 0;
+        for (int j = 0; j < E; ++j) {
+            const uint64_t other = uint64_t(uint32_t(__builtin_amdgcn_readlane(int(key >> 32), j))) << 32 |
+                                   uint32_t(__builtin_amdgcn_readlane(int(key), j));
+            rank += other > key || (other == key && j < lane);
         }
-        if (publish) {
-            const double top = l[ids[t * a.topk]];
-            double sum = 0.0;
-            if (!a.renorm)
-                for (int e = lane; e < a.E; e += 64) sum += exp(l[e] - top);
-            else if (lane < a.topk)
-                sum = exp(l[ids[t * a.topk + lane]] - top);
-#pragma unroll
-            for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
-            if (lane < a.topk) {
-                const int p = t * a.topk + lane;
-                const float w = float(exp(l[ids[p]] - top) / sum);
-                a.ids[p] = ids[p];
-                a.weights[p] = w;
-                a.route->weight[p] = w;
-            }
-        }
+        if (lane < E && rank < topk) ids[rank] = lane;
+        return;
     }
+    constexpr int kPer = SKETCH_MOE_MAX_EXPERTS / 64;
+    uint64_t key[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) key[i] = lane + 64 * i < E ? order_key(l[lane + 64 * i]) : 0;
+    for (int s = 0; s < topk; ++s) {
+        uint64_t best = key[0];
+        int at = lane;
+#pragma unroll
+        for (int i = 1; i < kPer; ++i)
+            if (key[i] > best) best = key[i], at = lane + 64 * i;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const uint64_t ob = __shfl_xor(best, d);
+            const int oa = __shfl_xor(at, d);
+            if (ob > best || (ob == best && oa < at)) best = ob, at = oa;
+        }
+        if (lane == 0) ids[s] = at;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+            if (at == lane + 64 * i) key[i] = 0;
+    }
+}
+
+// The top k of every token and the segments, by a whole workgroup.
+__device__ void build_route(const MoeArgs& a, Route& rt, int32_t* ids) {
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    for (int t = wave; t < a.T; t += kWaves) top_k(a.logits + int64_t(t) * a.E, a.E, a.topk, lane, ids + t * a.topk);
     __syncthreads();
     const int P = a.T * a.topk;
     for (int p = tid; p < P; p += kWaves * 64) {
@@ -161,14 +177,35 @@ __device__ void build_route(const MoeArgs& a, Route& rt, int32_t* ids, bool publ
         }
     }
     __syncthreads();
-    if (publish) {
-        for (int p = tid; p < P; p += kWaves * 64) a.route->pair[p] = rt.pair[p];
-        for (int i = tid; i <= rt.nact; i += kWaves * 64) {
-            if (i < rt.nact) a.route->expert[i] = rt.expert[i];
-            a.route->begin[i] = rt.begin[i];
+}
+
+// The route and the weights to memory, for the caller and the next launch.
+__device__ void publish_route(const MoeArgs& a, const Route& rt, const int32_t* ids) {
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, P = a.T * a.topk;
+    for (int t = wave; t < a.T; t += kWaves) {
+        const double* l = a.logits + int64_t(t) * a.E;
+        const double top = l[ids[t * a.topk]];
+        double sum = 0.0;
+        if (!a.renorm)
+            for (int e = lane; e < a.E; e += 64) sum += exp(l[e] - top);
+        else if (lane < a.topk)
+            sum = exp(l[ids[t * a.topk + lane]] - top);
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
+        if (lane < a.topk) {
+            const int p = t * a.topk + lane;
+            const float w = float(exp(l[ids[p]] - top) / sum);
+            a.ids[p] = ids[p];
+            a.weights[p] = w;
+            a.route->weight[p] = w;
         }
-        if (tid == 0) a.route->nact = rt.nact;
     }
+    for (int p = tid; p < P; p += kWaves * 64) a.route->pair[p] = rt.pair[p];
+    for (int i = tid; i <= rt.nact; i += kWaves * 64) {
+        if (i < rt.nact) a.route->expert[i] = rt.expert[i];
+        a.route->begin[i] = rt.begin[i];
+    }
+    if (tid == 0) a.route->nact = rt.nact;
 }
 
 __device__ inline void load_w(const uint8_t* row, int c, u32x4 (&w)[2]) {
@@ -176,53 +213,78 @@ __device__ inline void load_w(const uint8_t* row, int c, u32x4 (&w)[2]) {
     w[1] = *reinterpret_cast<const u32x4*>(row + 64 + 16 * c);
 }
 
-__device__ inline void load_x(const uint16_t* row, int c, bool valid, bf16x8 (&x)[4]) {
+// A fragment of bfloat16 values.  Tokens past an expert's last one read another
+// token's: no lane skips a load, and their products are not used.
+__device__ inline void load_x(const uint16_t* row, int c, bf16x8 (&x)[4]) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        x[j] = bf16x8{};
-        if (valid) x[j] = *reinterpret_cast<const bf16x8*>(row + 64 * (j >> 1) + 16 * c + 8 * (j & 1));
-    }
+    for (int j = 0; j < 4; ++j) x[j] = *reinterpret_cast<const bf16x8*>(row + 64 * (j >> 1) + 16 * c + 8 * (j & 1));
 }
 
+// Loads issued so far stay before what follows.
+__device__ inline void keep_order() { asm volatile("" ::: "memory"); }
 
 // Gate and up: a workgroup takes 16 rows of one active expert at a time, its
-// waves share out the blocks of 128 columns, and their sums meet in LDS.
+// waves share out the runs of kUpRun blocks of 128 columns, and their sums meet
+// in LDS.  The last workgroup only publishes the route.
+constexpr int kUpRun = 2;
+
 template <int NS>
 __global__ __launch_bounds__(kWaves * 64) void moe_up_kernel(MoeArgs a) {
     __shared__ Route rt;
     __shared__ int32_t ids[kMaxPairs];
     __shared__ float part[kWaves][2][16][17];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 15, c = lane >> 4;
-    build_route(a, rt, ids, blockIdx.x == 0);
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int r = lane & 15, c = lane >> 4;
+    build_route(a, rt, ids);
+    if (blockIdx.x == gridDim.x - 1) {
+        publish_route(a, rt, ids);
+        return;
+    }
     const int tiles = int(a.ldi / 16), items = rt.nact * tiles, kbs = int(a.ldh / 128);
     const int64_t plane = int64_t(a.T) * a.ldh, hplane = int64_t(a.T) * a.topk * a.ldi;
-    for (int it = blockIdx.x; it < items; it += gridDim.x) {
-        const int act = it / tiles, m0 = it % tiles * 16, e = rt.expert[act];
+    for (int it = blockIdx.x; it < items; it += gridDim.x - 1) {
+        const int act = it / tiles, m0 = it % tiles * 16, e = __builtin_amdgcn_readfirstlane(rt.expert[act]);
+        const int pend = __builtin_amdgcn_readfirstlane(rt.begin[act + 1]);
         const int64_t m = min(int64_t(m0 + r), a.I - 1);
         const uint8_t *G = a.gate + e * a.gu_bytes, *U = a.up + e * a.gu_bytes;
         const uint8_t *g = G + m * a.ldh, *u = U + m * a.ldh;
         const int64_t srow = min(int64_t(m0), a.I - 1) / 128 * a.gu_lds;
         const uint8_t *gs = G + a.gu_scales + srow, *us = U + a.gu_scales + srow;
-        for (int p0 = rt.begin[act]; p0 < rt.begin[act + 1]; p0 += 16) {
-            const bool valid = p0 + r < rt.begin[act + 1];
-            const uint16_t* x = a.xs + int64_t(valid ? rt.pair[p0 + r] / a.topk : 0) * a.ldh;
+        for (int p0 = __builtin_amdgcn_readfirstlane(rt.begin[act]); p0 < pend; p0 += 16) {
+            const uint16_t* x = a.xs + int64_t(rt.pair[min(p0 + r, pend - 1)] / a.topk) * a.ldh;
             f32x4 ga = {0, 0, 0, 0}, ua = {0, 0, 0, 0};
-            for (int kb = wave; kb < kbs; kb += kWaves) {
-                u32x4 gw[2], uw[2];
-                load_w(g + kb * 128, c, gw);
-                load_w(u + kb * 128, c, uw);
-                const float gsc = fp8_scale(gs[kb]), usc = fp8_scale(us[kb]);
-                bf16x8 xv[NS][4];
+            for (int k0 = wave * kUpRun; k0 < kbs; k0 += kWaves * kUpRun) {
+                u32x4 gw[kUpRun][2], uw[kUpRun][2];
+                bf16x8 x0[kUpRun][4];
 #pragma unroll
-                for (int s = 0; s < NS; ++s) load_x(x + s * plane + kb * 128, c, valid, xv[s]);
+                for (int v = 0; v < kUpRun; ++v) {
+                    const int kb = min(k0 + v, kbs - 1);
+                    load_w(g + kb * 128, c, gw[v]);
+                    load_w(u + kb * 128, c, uw[v]);
+                    load_x(x + kb * 128, c, x0[v]);
+                }
+                const uint32_t gsc = *reinterpret_cast<const uint16_t*>(gs + k0);
+                const uint32_t usc = *reinterpret_cast<const uint16_t*>(us + k0);
+                keep_order();
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const bf16x8 gb = fp8_widen(gw[j >> 1][2 * (j & 1)], gw[j >> 1][2 * (j & 1) + 1], gsc);
-                    const bf16x8 ub = fp8_widen(uw[j >> 1][2 * (j & 1)], uw[j >> 1][2 * (j & 1) + 1], usc);
+                for (int v = 0; v < kUpRun; ++v) {
+                    if (k0 + v >= kbs) break;
+                    bf16x8 xv[NS][4];
 #pragma unroll
-                    for (int s = 0; s < NS; ++s) {
-                        ga = __builtin_amdgcn_mfma_f32_16x16x32_bf16(gb, xv[s][j], ga, 0, 0, 0);
-                        ua = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ub, xv[s][j], ua, 0, 0, 0);
+                    for (int j = 0; j < 4; ++j) xv[0][j] = x0[v][j];
+#pragma unroll
+                    for (int s = 1; s < NS; ++s) load_x(x + s * plane + (k0 + v) * 128, c, xv[s]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const bf16x8 gb = fp8_widen(gw[v][j >> 1][2 * (j & 1)], gw[v][j >> 1][2 * (j & 1) + 1],
+                                                    fp8_scale(gsc >> (8 * v) & 255u));
+                        const bf16x8 ub = fp8_widen(uw[v][j >> 1][2 * (j & 1)], uw[v][j >> 1][2 * (j & 1) + 1],
+                                                    fp8_scale(usc >> (8 * v) & 255u));
+#pragma unroll
+                        for (int s = 0; s < NS; ++s) {
+                            ga = __builtin_amdgcn_mfma_f32_16x16x32_bf16(gb, xv[s][j], ga, 0, 0, 0);
+                            ua = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ub, xv[s][j], ua, 0, 0, 0);
+                        }
                     }
                 }
             }
@@ -241,7 +303,7 @@ __global__ __launch_bounds__(kWaves * 64) void moe_up_kernel(MoeArgs a) {
                     uv += part[w][1][tok][row];
                 }
                 float h = m0 + row < a.I ? gv / (1.0f + expf(-gv)) * uv : 0.0f;
-                if (p0 + tok < rt.begin[act + 1]) {
+                if (p0 + tok < pend) {
                     uint16_t* dst = a.hs + int64_t(rt.pair[p0 + tok]) * a.ldi + m0 + row;
 #pragma unroll
                     for (int s = 0; s < 3; ++s) dst[s * hplane] = take_bf16(h);
@@ -252,63 +314,122 @@ __global__ __launch_bounds__(kWaves * 64) void moe_up_kernel(MoeArgs a) {
     }
 }
 
-// Down and the weighted sum: a workgroup owns 16 outputs of every token; its
-// waves share out the (expert, block of 128 columns) units in order, each sums
-// into its own tile, and the tiles are added in the order of the waves.
+// Down and the weighted sum.  A workgroup owns kDownRows outputs and a run of
+// the active experts' blocks of 128 columns, which its waves take in turns;
+// each wave sums into a tile of its own, the tiles are added in the order of
+// the waves, and the runs in theirs by moe_add_kernel (the last workgroup of a
+// row group adding them up was measured: the fences that takes cost 75 us).
+// The three terms of h are 12 loads to a block, so they serve 32 outputs, and
+// come with the weights' 4 loads, not after them.
+constexpr int kDownTiles = 2, kDownRows = 16 * kDownTiles;
+constexpr int kDownRun = 2;   // blocks a wave has in flight
+
 __global__ __launch_bounds__(kWaves * 64) void moe_down_kernel(MoeArgs a) {
-    extern __shared__ float ytile[];   // [kWaves][T][16]
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 15, c = lane >> 4;
-    const Route& rt = *a.route;
-    float* y = ytile + wave * a.T * 16;
-    for (int u = lane; u < a.T * 16; u += 64) y[u] = 0.0f;
-    const int64_t m0 = int64_t(blockIdx.x) * 16, m = min(m0 + r, a.H - 1);
-    const int kbs = int(a.ldi / 128), units = rt.nact * kbs;
+    extern __shared__ __attribute__((aligned(16))) float ytile[];   // [kWaves][T][kDownRows]
+    __shared__ Route rt;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int r = lane & 15, c = lane >> 4;
+    {   // all of the route at once: at most a segment per pair
+        const int P = a.T * a.topk, A = min(P, a.E);
+        for (int i = tid; i < P; i += kWaves * 64) {
+            rt.pair[i] = a.route->pair[i];
+            rt.weight[i] = a.route->weight[i];
+        }
+        for (int i = tid; i <= A; i += kWaves * 64) {
+            if (i < A) rt.expert[i] = a.route->expert[i];
+            rt.begin[i] = a.route->begin[i];
+        }
+        if (tid == 0) rt.nact = a.route->nact;
+    }
+    for (int u = tid; u < kWaves * a.T * kDownRows; u += kWaves * 64) ytile[u] = 0.0f;
+    __syncthreads();
+    float* y = ytile + wave * a.T * kDownRows;
+    const int group = blockIdx.x % a.groups, split = blockIdx.x / a.groups;
+    const int64_t m0 = int64_t(group) * kDownRows;
+    const int kbs = int(a.ldi / 128), nact = __builtin_amdgcn_readfirstlane(rt.nact);
+    const int u0 = int(int64_t(nact) * kbs * split / a.splits), u1 = int(int64_t(nact) * kbs * (split + 1) / a.splits);
     const int64_t hplane = int64_t(a.T) * a.topk * a.ldi;
-    const int u0 = int(int64_t(units) * wave / kWaves), u1 = int(int64_t(units) * (wave + 1) / kWaves);
-    for (int u = u0; u < u1;) {
-        const int act = u / kbs, kb0 = u % kbs, kb1 = min(kbs, kb0 + u1 - u), e = rt.expert[act];
-        u += kb1 - kb0;
-        const uint8_t* D = a.down + e * a.d_bytes;
-        const uint8_t *d = D + m * a.ldi, *ds = D + a.d_scales + m0 / 128 * a.d_lds;
-        for (int p0 = rt.begin[act]; p0 < rt.begin[act + 1]; p0 += 16) {
-            const bool valid = p0 + r < rt.begin[act + 1];
-            const int pair = valid ? rt.pair[p0 + r] : 0;
+    int64_t roff[kDownTiles];
+#pragma unroll
+    for (int i = 0; i < kDownTiles; ++i) roff[i] = min(m0 + 16 * i + r, a.H - 1) * a.ldi + 16 * c;
+    for (int act = u0 / kbs; act * kbs < u1; ++act) {
+        const int e = __builtin_amdgcn_readfirstlane(rt.expert[act]), pend = __builtin_amdgcn_readfirstlane(rt.begin[act + 1]);
+        const int kend = min(u1 - act * kbs, kbs), kfirst = max(u0 - act * kbs, 0) + wave;
+        const uint8_t *D = a.down + e * a.d_bytes, *ds = D + a.d_scales + m0 / 128 * a.d_lds;
+        for (int p0 = __builtin_amdgcn_readfirstlane(rt.begin[act]); p0 < pend; p0 += 16) {
+            const int pair = rt.pair[min(p0 + r, pend - 1)];
             const uint16_t* h = a.hs + int64_t(pair) * a.ldi;
-            f32x4 acc = {0, 0, 0, 0};
-            for (int kb = kb0; kb < kb1; ++kb) {
-                u32x4 w[2];
-                load_w(d + kb * 128, c, w);
-                const float sc = fp8_scale(ds[kb]);
-                bf16x8 hv[3][4];
+            f32x4 acc[kDownTiles];
 #pragma unroll
-                for (int s = 0; s < 3; ++s) load_x(h + s * hplane + kb * 128, c, valid, hv[s]);
+            for (int i = 0; i < kDownTiles; ++i) acc[i] = f32x4{0, 0, 0, 0};
+            for (int k0 = kfirst; k0 < kend; k0 += kDownRun * kWaves) {
+                u32x4 w[kDownRun][kDownTiles][2];
+                bf16x8 hv[kDownRun][3][4];
+                float scale[kDownRun];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const bf16x8 wb = fp8_widen(w[j >> 1][2 * (j & 1)], w[j >> 1][2 * (j & 1) + 1], sc);
+                for (int v = 0; v < kDownRun; ++v) {
+                    const int kb = min(k0 + v * kWaves, kend - 1);
 #pragma unroll
-                    for (int s = 0; s < 3; ++s) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb, hv[s][j], acc, 0, 0, 0);
+                    for (int i = 0; i < kDownTiles; ++i) load_w(D + kb * 128 + roff[i], 0, w[v][i]);
+#pragma unroll
+                    for (int s = 0; s < 3; ++s) load_x(h + s * hplane + kb * 128, c, hv[v][s]);
+                    scale[v] = fp8_scale(ds[kb]);
+                }
+                keep_order();
+#pragma unroll
+                for (int v = 0; v < kDownRun; ++v) {
+                    if (k0 + v * kWaves >= kend) break;
+#pragma unroll
+                    for (int i = 0; i < kDownTiles; ++i)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const bf16x8 wb = fp8_widen(w[v][i][j >> 1][2 * (j & 1)], w[v][i][j >> 1][2 * (j & 1) + 1], scale[v]);
+#pragma unroll
+                            for (int s = 0; s < 3; ++s)
+                                acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb, hv[v][s][j], acc[i], 0, 0, 0);
+                        }
                 }
             }
-            if (valid) {
+            if (p0 + r < pend) {
                 const float w = rt.weight[pair];
-                float* dst = y + pair / a.topk * 16 + 4 * c;
+                f32x4* dst = reinterpret_cast<f32x4*>(y + pair / a.topk * kDownRows + 4 * c);
 #pragma unroll
-                for (int v = 0; v < 4; ++v) dst[v] += w * acc[v];
+                for (int i = 0; i < kDownTiles; ++i) dst[4 * i] += w * acc[i];
             }
         }
     }
     __syncthreads();
-    for (int u = tid; u < a.T * 16; u += kWaves * 64) {
+    float* out = a.splits > 1 ? a.parts + int64_t(split) * a.T * a.H : a.Y;
+    for (int u = tid; u < a.T * kDownRows; u += kWaves * 64) {
+        const int64_t m = m0 + u % kDownRows;
         float sum = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) sum += ytile[w * a.T * 16 + u];
-        if (m0 + u % 16 < a.H) a.Y[int64_t(u / 16) * a.H + m0 + u % 16] = sum;
+        for (int w = 0; w < kWaves; ++w) sum += ytile[w * a.T * kDownRows + u];
+        if (m < a.H) out[int64_t(u / kDownRows) * a.H + m] = sum;
     }
+}
+
+__global__ __launch_bounds__(256) void moe_add_kernel(MoeArgs a) {
+    const int64_t n = int64_t(a.T) * a.H, i = int64_t(blockIdx.x) * 256 + threadIdx.x;
+    if (i >= n) return;
+    float sum = 0.0f;
+    for (int s = 0; s < a.splits; ++s) sum += a.parts[s * n + i];
+    a.Y[i] = sum;
+}
+
+// Workgroups to a row group of the down kernel: about two per compute unit in
+// all, each with some blocks for every wave to go through (every token has topk experts).
+int down_splits(const sketch_moe_params* p, int64_t kbs) {
+    const int64_t groups = (p->H + kDownRows - 1) / kDownRows, steps = (p->topk * kbs + kWaves - 1) / kWaves;
+    int64_t s = (2 * compute_units() + groups - 1) / groups;
+    if (s > steps) s = steps;
+    return int(s < 1 ? 1 : s);
 }
 
 struct MoeLayout {
     sketch_fp8_shape gu, d;
-    size_t xs, hs, route, total;
+    size_t xs, hs, route, parts, total;
+    int splits, groups;
 };
 
 sketch_status moe_layout(const sketch_moe_params* p, int64_t tokens, MoeLayout* L) {
@@ -325,7 +446,10 @@ sketch_status moe_layout(const sketch_moe_params* p, int64_t tokens, MoeLayout* 
     L->xs = align256(size_t(tokens) * p->E * sizeof(double));
     L->hs = align256(L->xs + terms * size_t(tokens) * L->gu.ld * 2);
     L->route = align256(L->hs + 3 * size_t(tokens) * p->topk * L->d.ld * 2);
-    L->total = align256(L->route + sizeof(Route));
+    L->parts = align256(L->route + sizeof(Route));
+    L->splits = down_splits(p, L->d.col_blocks);
+    L->groups = int((p->H + kDownRows - 1) / kDownRows);
+    L->total = align256(L->parts + (L->splits > 1 ? size_t(L->splits) * size_t(tokens) * size_t(p->H) * 4 : 0));
     return SKETCH_OK;
 }
 
@@ -371,6 +495,9 @@ sketch_status sketch_moe(const sketch_moe_params* p, const void* router, const v
     a.xs = reinterpret_cast<uint16_t*>(ws + L.xs);
     a.hs = reinterpret_cast<uint16_t*>(ws + L.hs);
     a.route = reinterpret_cast<Route*>(ws + L.route);
+    a.parts = reinterpret_cast<float*>(ws + L.parts);
+    a.splits = L.splits;
+    a.groups = L.groups;
     a.H = p->H;
     a.I = p->I;
     a.ldh = L.gu.ld;
@@ -385,22 +512,26 @@ sketch_status sketch_moe(const sketch_moe_params* p, const void* router, const v
     a.E = p->E;
     a.topk = p->topk;
     a.renorm = p->renorm;
-    const unsigned E = unsigned(p->E);
+    const int64_t ncu = compute_units();
     const int64_t items = (tokens * p->topk < p->E ? tokens * p->topk : int64_t(p->E)) * (L.d.ld / 16);
-    const int64_t room = 2 * int64_t(compute_units());
-    const unsigned up_grid = unsigned(items < room ? items : room), down_grid = unsigned((p->H + 15) / 16);
-    const size_t lds = size_t(kWaves) * tokens * 16 * sizeof(float);
-    auto go = [&](auto logits, auto gate_up) {
-        logits<<<E, 256, 0, st>>>(a);
+    const unsigned up_grid = unsigned(items < 2 * ncu ? items : 2 * ncu) + 1;
+    const size_t lds = size_t(kWaves) * tokens * kDownRows * sizeof(float);
+    const int nt = tokens == 1 ? 1 : 4;   // tokens of a workgroup that sums logits
+    auto go = [&](auto one, auto four, auto gate_up) {
+        const auto logits = tokens == 1 ? one : four;
+        logits<<<dim3(unsigned(p->E), unsigned((tokens + nt - 1) / nt)), 256, 0, st>>>(a);
         if (hipGetLastError() != hipSuccess) return SKETCH_EDEVICE;
         gate_up<<<up_grid, kWaves * 64, 0, st>>>(a);
         if (hipGetLastError() != hipSuccess) return SKETCH_EDEVICE;
-        moe_down_kernel<<<down_grid, kWaves * 64, lds, st>>>(a);
+        moe_down_kernel<<<unsigned(L.groups * L.splits), kWaves * 64, lds, st>>>(a);
+        if (L.splits == 1) return launch_status();
+        if (hipGetLastError() != hipSuccess) return SKETCH_EDEVICE;
+        moe_add_kernel<<<unsigned((tokens * p->H + 255) / 256), 256, 0, st>>>(a);
         return launch_status();
     };
-    if (p->x_dtype == SKETCH_F32) return go(moe_logits_kernel<SKETCH_F32>, moe_up_kernel<3>);
-    if (p->x_dtype == SKETCH_BF16) return go(moe_logits_kernel<SKETCH_BF16>, moe_up_kernel<1>);
-    return go(moe_logits_kernel<SKETCH_F16>, moe_up_kernel<2>);
+    if (p->x_dtype == SKETCH_F32) return go(moe_logits_kernel<SKETCH_F32, 1>, moe_logits_kernel<SKETCH_F32, 4>, moe_up_kernel<3>);
+    if (p->x_dtype == SKETCH_BF16) return go(moe_logits_kernel<SKETCH_BF16, 1>, moe_logits_kernel<SKETCH_BF16, 4>, moe_up_kernel<1>);
+    return go(moe_logits_kernel<SKETCH_F16, 1>, moe_logits_kernel<SKETCH_F16, 4>, moe_up_kernel<2>);
 }
 
 }  // extern "C"
