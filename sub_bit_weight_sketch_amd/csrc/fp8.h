@@ -2,6 +2,8 @@
 // mixture-of-experts layer that reads them (moe.hip).
 #pragma once
 
+#include <atomic>
+
 #include "../../include/sketch_fp8.h"
 #include "common.h"
 
@@ -21,12 +23,16 @@ sketch_status fp8_shape(const sketch_fp8_params* p, sketch_fp8_shape* s);
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// Compute units of the current device (256 when none answers).
+// Compute units of the current device, asked for once per device (256 when
+// none answers).
 inline int compute_units() {
+    static std::atomic<int> known[64];
     int dev = 0, ncu = 0;
-    if (hipGetDevice(&dev) != hipSuccess ||
-        hipDeviceGetAttribute(&ncu, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || ncu <= 0)
-        ncu = 256;
+    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 256;
+    ncu = known[dev].load(std::memory_order_relaxed);
+    if (ncu > 0) return ncu;
+    if (hipDeviceGetAttribute(&ncu, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || ncu <= 0) return 256;
+    known[dev].store(ncu, std::memory_order_relaxed);
     return ncu;
 }
 

@@ -6,7 +6,6 @@ Argument marshalling only, as in the rest of the package: ``sketch_fp8_layout``,
 ``sketch_moe_workspace_bytes`` and ``sketch_moe`` have the names of the C ABI;
 the rest is a convenience layer over them.
 """
-import contextlib
 import ctypes
 
 import torch
@@ -104,11 +103,26 @@ def sketch_moe(p, router, gate, up, down, X, Y, ids, weights, workspace, stream=
 # high-level API
 # ---------------------------------------------------------------------------
 
-def _on(device):
-    """The device made current for the call (launches go to the current device)."""
-    if torch.cuda.current_device() == device.index:
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+class _On:
+    """The device made current for the call, if it is not (launches go to the
+    current device); `with` gives the current stream of the device."""
+
+    def __init__(self, device):
+        self.index, self.other = device.index, None
+
+    def __enter__(self):
+        if torch.cuda.current_device() != self.index:
+            self.other = torch.cuda.device(self.index)
+            self.other.__enter__()
+        return _raw_stream(self.index)
+
+    def __exit__(self, *exc):
+        if self.other is not None:
+            self.other.__exit__(*exc)
 
 
 def _need(ok, what):
@@ -118,7 +132,8 @@ def _need(ok, what):
 
 def _aligned(t):
     """t itself when dense and 16-byte aligned, else a copy that is."""
-    t = t.contiguous()
+    if not t.is_contiguous():
+        return t.contiguous()
     return t if t.data_ptr() % 16 == 0 else t.clone()
 
 
@@ -136,16 +151,13 @@ class Fp8Tables:
             buf = torch.empty(n, dtype=torch.uint8, device=device)
         _need(buf.dtype == torch.uint8 and buf.is_contiguous() and buf.numel() >= n and buf.data_ptr() % 16 == 0,
               "the buffer must be %d dense, 16-byte aligned bytes" % n)
-        self.buf = buf
+        self.buf, self.device = buf, buf.device
+        self._at, self._ref = buf.data_ptr(), ctypes.byref(self.params)
         self._ws = {}
 
     @property
     def shape(self):
         return ((self.M, self.N) if self.count is None else (self.count, self.M, self.N))
-
-    @property
-    def device(self):
-        return self.buf.device
 
     def _view(self, rows, cols, ld, at):
         if self.count is None:
@@ -176,10 +188,10 @@ def fp8_encode(W, block_rows=128, check=True, status=None):
     dtype_code(W)
     W = _aligned(W)
     t = Fp8Tables(W.shape[-2], W.shape[-1], block_rows, W.shape[0] if W.dim() == 3 else None, W.device)
-    with _on(W.device):
+    with _On(W.device) as stream:
         if check and status is None:
             status = torch.zeros(1, dtype=torch.int32, device=W.device)
-        sketch_fp8_encode(t.params, W, t.buf, status)
+        sketch_fp8_encode(t.params, W, t.buf, status, stream)
         if check:
             flags = int(status.item())
             rc = sketch_encode_status(flags)
@@ -205,13 +217,18 @@ def fp8_tables(codes, scales, block_rows=128):
     return t
 
 
-def fp8_workspace_for(t, batch, x_dtype, y_dtype, device):
-    """Workspace for products of `batch` rows (None if not needed).  Reuse it
-    across calls on one stream, never for two calls in flight at once."""
+def _workspace_bytes(t, batch, x_dtype, y_dtype):
     key = (batch, x_dtype, y_dtype)
     n = t._ws.get(key)
     if n is None:
         n = t._ws[key] = sketch_fp8_workspace_bytes(t.params, batch, x_dtype, y_dtype)
+    return n
+
+
+def fp8_workspace_for(t, batch, x_dtype, y_dtype, device):
+    """Workspace for products of `batch` rows (None if not needed).  Reuse it
+    across calls on one stream, never for two calls in flight at once."""
+    n = _workspace_bytes(t, batch, x_dtype, y_dtype)
     return torch.empty(n, dtype=torch.uint8, device=device) if n else None
 
 
@@ -229,26 +246,39 @@ def fp8_matmul(t, X, out=None, workspace=None, dtype=None):
     block_rows=1, for rows that several linears share.  dtype: of Y, float32
     (the default, or that of `out`), bfloat16 or float16; see
     include/sketch_fp8.h for how the sums of large batches differ."""
-    dtype = dtype or (out.dtype if out is not None else torch.float32)
-    _need(t.block_rows == 128 and t.count is None, "t must be one weight, encoded with block_rows=128")
+    if t.block_rows != 128 or t.count is not None:
+        raise ValueError("t must be one weight, encoded with block_rows=128")
     rows = isinstance(X, Fp8Tables)
     if rows:
         _need(X.block_rows == 1 and X.count is None, "encoded rows must have block_rows=1")
-    squeeze = not rows and X.dim() == 1
-    if squeeze:
-        X = X[None, :]
-    _need(X.device == t.device, "X and the weight are on different devices")
-    if len(X.shape) != 2 or X.shape[1] != t.N:
-        raise ValueError("X must have %d columns, got shape %s" % (t.N, tuple(X.shape)))
-    batch = X.shape[0]
-    xdt = FP8_ROWS if rows else dtype_code(X)
-    x = X.buf if rows else _aligned(X)
-    with _on(t.device):
-        Y = _out(out[None, :] if squeeze and out is not None and out.dim() == 1 else out, (batch, t.M), dtype, t.device)
+    shape, device = X.shape, t.device
+    if X.device != device:
+        raise ValueError("X and the weight are on different devices")
+    squeeze = len(shape) == 1
+    batch = 1 if squeeze else shape[0]
+    if len(shape) > 2 or shape[-1] != t.N:
+        raise ValueError("X must have %d columns, got shape %s" % (t.N, tuple(shape)))
+    if rows:
+        xdt, at = FP8_ROWS, X._at
+    else:
+        xdt, x = dtype_code(X), _aligned(X)
+        at = x.data_ptr()
+    shape = (t.M,) if squeeze else (batch, t.M)
+    if dtype is None:
+        dtype = torch.float32 if out is None else out.dtype
+    with _On(device) as stream:
+        Y = torch.empty(shape, dtype=dtype, device=device) if out is None else _out(out, shape, dtype, device)
+        ydt = dtype_code(Y)
         if workspace is None:
-            workspace = fp8_workspace_for(t, batch, xdt, dtype_code(Y), t.device)
-        sketch_fp8_matmul(t.params, t.buf, x, xdt, batch, Y, workspace)
-    return Y[0] if squeeze else Y
+            wsb = _workspace_bytes(t, batch, xdt, ydt)
+            workspace = torch.empty(wsb, dtype=torch.uint8, device=device) if wsb else None
+        else:
+            wsb = workspace.numel() * workspace.element_size()
+        rc = _fp8_lib().sketch_fp8_matmul(t._ref, t._at, at, xdt, batch, Y.data_ptr(), ydt,
+                                          workspace.data_ptr() if workspace is not None else None, wsb, stream)
+    if rc != OK:
+        raise SketchError(rc, "sketch_fp8_matmul")
+    return Y
 
 
 class MoE:
@@ -269,16 +299,21 @@ class MoE:
         self.router, self.gate, self.up, self.down = _aligned(router), gate, up, down
         self.topk, self.renorm = int(topk), bool(renorm)
         self.params = MoEParams(H, I, E, self.topk, int(self.renorm), dtype_code(router))
+        self._fixed = (ctypes.byref(self.params), self.router.data_ptr(), gate._at, up._at, down._at)
+        self._H, self._dtype, self._device = H, router.dtype, router.device
         sketch_moe_workspace_bytes(self.params, 0)   # checks the sizes
         self._ws = {}
+
+    def _workspace_bytes(self, tokens):
+        n = self._ws.get(tokens)
+        if n is None:
+            n = self._ws[tokens] = max(sketch_moe_workspace_bytes(self.params, tokens), 16)
+        return n
 
     def workspace_for(self, tokens):
         """Workspace for `tokens` tokens.  Reuse it across calls on one
         stream, never for two calls in flight at once."""
-        n = self._ws.get(tokens)
-        if n is None:
-            n = self._ws[tokens] = sketch_moe_workspace_bytes(self.params, tokens)
-        return torch.empty(max(n, 16), dtype=torch.uint8, device=self.router.device)
+        return torch.empty(self._workspace_bytes(tokens), dtype=torch.uint8, device=self._device)
 
 
 def moe(layer, X, out=None, workspace=None, return_routing=False):
@@ -286,17 +321,23 @@ def moe(layer, X, out=None, workspace=None, return_routing=False):
     MOE_MAX_TOKENS tokens, of the router's dtype); with return_routing also
     the chosen experts int32 [tokens, topk], by descending logit, and their
     weights float32 [tokens, topk]."""
-    p = layer.params
-    _need(X.dim() == 2 and X.shape[1] == p.H, "X must be [tokens, %d]" % p.H)
-    _need(X.dtype == layer.router.dtype and X.device == layer.router.device,
-          "X must have the router's dtype and device")
-    X = _aligned(X)
-    T, dev = X.shape[0], X.device
-    with _on(dev):
-        Y = _out(out, (T, p.H), torch.float32, dev)
-        ids = torch.empty((T, p.topk), dtype=torch.int32, device=dev)
-        weights = torch.empty((T, p.topk), dtype=torch.float32, device=dev)
+    shape, dev, k = X.shape, layer._device, layer.topk
+    if len(shape) != 2 or shape[1] != layer._H:
+        raise ValueError("X must be [tokens, %d]" % layer._H)
+    if X.dtype != layer._dtype or X.device != dev:
+        raise ValueError("X must have the router's dtype and device")
+    X, T = _aligned(X), shape[0]
+    with _On(dev) as stream:
+        Y = torch.empty(shape, dtype=torch.float32, device=dev) if out is None else _out(out, shape, torch.float32, dev)
+        ids = torch.empty((T, k), dtype=torch.int32, device=dev)
+        weights = torch.empty((T, k), dtype=torch.float32, device=dev)
         if workspace is None:
-            workspace = layer.workspace_for(T)
-        sketch_moe(p, layer.router, layer.gate.buf, layer.up.buf, layer.down.buf, X, Y, ids, weights, workspace)
+            wsb = layer._workspace_bytes(T)
+            workspace = torch.empty(wsb, dtype=torch.uint8, device=dev)
+        else:
+            wsb = workspace.numel() * workspace.element_size()
+        rc = _fp8_lib().sketch_moe(*layer._fixed, X.data_ptr(), T, Y.data_ptr(), ids.data_ptr(), weights.data_ptr(),
+                                   workspace.data_ptr(), wsb, stream)
+    if rc != OK:
+        raise SketchError(rc, "sketch_moe")
     return (Y, ids, weights) if return_routing else Y
