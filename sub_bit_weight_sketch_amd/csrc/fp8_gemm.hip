@@ -55,16 +55,24 @@ __device__ inline void tile_of(const GemmArgs& a, uint32_t& to, uint32_t& tt) {
     tt = g * G + in % gt;
 }
 
+// Two floats in 16 bits each, ties to even.
+template <int YD>
+__device__ inline uint32_t pack2(float a, float b) {
+    if constexpr (YD == SKETCH_BF16) {
+        const bf16x2 h = {static_cast<__bf16>(a), static_cast<__bf16>(b)};
+        return __builtin_bit_cast(uint32_t, h);
+    } else {
+        return uint32_t(f32_to_f16_bits(a)) | (uint32_t(f32_to_f16_bits(b)) << 16);
+    }
+}
+
 template <int YD>
 __device__ inline void store4(void* Y, int64_t e, f32x4 v, int64_t m, int64_t M, bool vec) {
     if (vec && m + 4 <= M) {
         if constexpr (YD == SKETCH_F32) {
             *reinterpret_cast<f32x4*>(static_cast<float*>(Y) + e) = v;
         } else {
-            uint32_t h[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) h[i] = YD == SKETCH_BF16 ? f32_to_bf16_bits(v[i]) : f32_to_f16_bits(v[i]);
-            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(Y) + e) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(Y) + e) = make_uint2(pack2<YD>(v[0], v[1]), pack2<YD>(v[2], v[3]));
         }
     } else {
 #pragma unroll
@@ -74,36 +82,39 @@ __device__ inline void store4(void* Y, int64_t e, f32x4 v, int64_t m, int64_t M,
 }
 
 // ---------------------------------------------------------------------------
-// 256 outputs x 256 tokens on the e4m3 matrix cores (16-bit Y).  8 waves, two
-// to a SIMD, each 128 x 64: 32 accumulators of 16x16.  The waves work in two
-// groups, one on each SIMD, half a step apart: while one group runs the 32
-// MFMAs of its step from registers, the other reads its 12 fragments from LDS,
-// so the matrix cores always have one wave's work and LDS the other's.  The
-// 64 KiB of a step are loaded while the step before is worked on.
+// 32 FA outputs x 256 tokens on the e4m3 matrix cores (16-bit Y).  8 waves, two
+// to a SIMD, each 16 FA x 64: 4 FA accumulators of 16x16.  FA is 8, or 7 or 6
+// where that many more tiles fill their last round over the compute units
+// better (28672 outputs x 2048 tokens: 896 tiles are 3.5 rounds, 1024 are 4).
+//  The waves work in two
+// groups, one on each SIMD, half a step apart: while one group runs the
+// MFMAs of its step from registers, the other reads its fragments from LDS,
+// so the matrix cores always have one wave's work and LDS the other's.  A
+// step's 64 KiB are loaded while the step before is worked on.
 // ---------------------------------------------------------------------------
-constexpr int kBigRows = 512;                       // 256 of W, 256 of X
-constexpr uint32_t kBigStage = kBigRows * 128;
+constexpr uint32_t kBigStage = 512 * 128;           // 32 FA rows of W in the first half, 256 of X in the second
 constexpr uint32_t kBigScales = (256 + 16) * 4;     // dwords of 4 steps: one per token, one per 16 outputs
 constexpr uint32_t kBigLds = 2 * kBigStage + 2 * kBigScales;
 
-template <int YD>
+template <int YD, int FA>
 __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void fp8_gemm_big_kernel(GemmArgs a) {
     extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
     const Fp8Product& p = a.p;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int r = lane & 15, c = lane >> 4, group = wave >> 2, wm = group * 128, wt = (wave & 3) * 64;
+    const int r = lane & 15, c = lane >> 4, group = wave >> 2, wm = group * FA * 16, wt = (wave & 3) * 64;
     uint32_t to, tt;
     tile_of(a, to, tt);
-    const int64_t o0 = int64_t(to) * 256, t0 = int64_t(tt) * 256;
+    constexpr int kRows = 32 * FA;
+    const int64_t o0 = int64_t(to) * kRows, t0 = int64_t(tt) * 256;
 
-    // loads of this wave: 4 x 8 rows of W and 4 x 8 rows of X per step
+    // loads of this wave: every eighth 8 rows of W and of X
     const uint8_t *wbase = p.w + o0 * p.ld, *xbase = p.x + t0 * p.ld;
-    const uint32_t wlast = uint32_t(min(int64_t(255), p.M - 1 - o0)), xlast = uint32_t(min(int64_t(255), p.T - 1 - t0));
+    const uint32_t wlast = uint32_t(min(int64_t(kRows - 1), p.M - 1 - o0)), xlast = uint32_t(min(int64_t(255), p.T - 1 - t0));
     const uint32_t piece = uint32_t((lane & 7) ^ (lane >> 3)) * 16, ld = uint32_t(p.ld);
     uint32_t woff[4], xoff[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint32_t row = uint32_t(wave * 32 + i * 8 + (lane >> 3));
+        const uint32_t row = uint32_t((i * 8 + wave) * 8 + (lane >> 3));
         woff[i] = min(row, wlast) * ld + piece;
         xoff[i] = min(row, xlast) * ld + piece;
     }
@@ -112,28 +123,29 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     const uint32_t srow = wave < 4 ? min(uint32_t(wave * 64 + lane), xlast)
                                    : uint32_t(min(o0 + (lane & 15) * 16, p.M - 1) / 128);
     const uint32_t soff = srow * uint32_t(p.lds);
-    const uint32_t lds0 = lds_address(lds), lw = lds0 + wave * 4096, lx = lw + 32768;
+    const uint32_t lds0 = lds_address(lds), lw = lds0 + wave * 1024, lx = lw + 32768;
     const uint32_t lsc = lds0 + 2 * kBigStage + (wave < 4 ? wave * 256 : 1024);
 
     auto load_step = [&](uint32_t k) {
         const uint32_t st = (k & 1) * kBigStage;
         const uint8_t *wk = wbase + size_t(k) * 128, *xk = xbase + size_t(k) * 128;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) dma16(wk, woff[i], lw + st + i * 1024);
+        for (int i = 0; i < 4; ++i)
+            if (i * 8 + 8 <= 4 * FA || i * 8 + wave < 4 * FA) dma16(wk, woff[i], lw + st + i * 8192);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) dma16(xk, xoff[i], lx + st + i * 1024);
+        for (int i = 0; i < 4; ++i) dma16(xk, xoff[i], lx + st + i * 8192);
         if ((k & 3) == 0) {
-            if (wave < 4 || (wave == 4 && lane < 16)) dma4(sbase + k, soff, lsc + ((k >> 2) & 1) * kBigScales);
+            if (wave < 4 || (wave == 4 && lane < 2 * FA)) dma4(sbase + k, soff, lsc + ((k >> 2) & 1) * kBigScales);
         }
     };
 
-    f32x4 acc[8][4];
+    f32x4 acc[FA][4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < FA; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
-    i32x8 af[8], bf[4];
-    int as[8], bs[4];
+    i32x8 af[FA], bf[4];
+    int as[FA], bs[4];
     const unsigned char* frag = lds + r * 128 + ((c ^ (r & 7)) << 4);
     const unsigned char* frag2 = lds + r * 128 + (((c + 4) ^ (r & 7)) << 4);
 
@@ -146,7 +158,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
             bf[j] = __builtin_shufflevector(*reinterpret_cast<const i32x4*>(g1 + j * 2048),
                                             *reinterpret_cast<const i32x4*>(g2 + j * 2048), 0, 1, 2, 3, 4, 5, 6, 7);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < FA; ++i)
             af[i] = __builtin_shufflevector(*reinterpret_cast<const i32x4*>(f1 + i * 2048),
                                             *reinterpret_cast<const i32x4*>(f2 + i * 2048), 0, 1, 2, 3, 4, 5, 6, 7);
         if ((k & 3) == 0) {
@@ -154,18 +166,18 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 #pragma unroll
             for (int j = 0; j < 4; ++j) bs[j] = sc[wt + j * 16 + r];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) as[i] = sc[256 + wm / 16 + i];
+            for (int i = 0; i < FA; ++i) as[i] = sc[256 + wm / 16 + i];
         } else {   // the next byte to the low end
 #pragma unroll
             for (int j = 0; j < 4; ++j) bs[j] = int(uint32_t(bs[j]) >> 8);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) as[i] = int(uint32_t(as[i]) >> 8);
+            for (int i = 0; i < FA; ++i) as[i] = int(uint32_t(as[i]) >> 8);
         }
     };
     auto compute = [&]() {
         __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < FA; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(af[i], bf[j], acc[i][j], 0, 0, 0, as[i],
@@ -204,15 +216,40 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
         }
     }
 
-    const bool vec = p.M % 4 == 0;
+    // Whole tiles go out through LDS, 256 contiguous bytes of a token's row and
+    // more at a time; the others element by element where they have to.
+    if (o0 + kRows <= p.M && t0 + 256 <= p.T && p.M % 8 == 0) {
+        constexpr uint32_t kRow = FA * 32;   // bytes of a token's outputs in the wave's tile
+        unsigned char* mine = lds + wave * (64 * kRow);
+        barrier();   // every wave is done reading its fragments
 #pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int i = 0; i < FA; ++i)
+                *reinterpret_cast<uint2*>(mine + (j * 16 + r) * kRow + i * 32 + c * 8) =
+                    make_uint2(pack2<YD>(acc[i][j][0], acc[i][j][1]), pack2<YD>(acc[i][j][2], acc[i][j][3]));
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        uint16_t* Y = static_cast<uint16_t*>(p.Y) + (t0 + wt) * p.M + o0 + wm;
+#pragma unroll
+        for (uint32_t n = 0; n < 64 * kRow / 1024; ++n) {
+            const uint32_t at = n * 1024 + lane * 16, t = at / kRow, m = at % kRow;
+            *reinterpret_cast<u32x4*>(Y + int64_t(t) * p.M + m / 2) = *reinterpret_cast<const u32x4*>(mine + at);
+        }
+        return;
+    }
+    const bool vec = p.M % 4 == 0;
     for (int j = 0; j < 4; ++j) {
         const int64_t t = t0 + wt + j * 16 + r;
         if (t >= p.T) continue;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < FA; ++i) {
             const int64_t m = o0 + wm + i * 16 + 4 * c;
-            store4<YD>(p.Y, t * p.M + m, acc[i][j], m, p.M, vec);
+            f32x4 v = acc[i][0];
+#pragma unroll
+            for (int q = 1; q < 4; ++q)
+                if (j == q) v = acc[i][q];
+            store4<YD>(p.Y, t * p.M + m, v, m, p.M, vec);
         }
     }
 }
@@ -359,17 +396,35 @@ __global__ __launch_bounds__(256) void fp8_add_kernel(GemmArgs a) {
 
 // Which kernel a product takes, and over how many workgroups K is split.
 struct GemmPlan {
-    bool big;
+    int fa;            // of the big kernel, 0: fp8_gemm_kernel
     uint32_t splits;
 };
 
 GemmPlan gemm_plan(int64_t M, int64_t T, uint32_t kb, int ydt) {
-    const int64_t ncu = compute_units();
-    const int64_t big = (M + 255) / 256 * ((T + 255) / 256), mid = (M + 127) / 128 * ((T + 127) / 128);
-    if (ydt != SKETCH_F32 && big >= ncu * 3 / 4) return {true, 1};
+    const int64_t ncu = compute_units(), mid = (M + 127) / 128 * ((T + 127) / 128);
+    if (ydt != SKETCH_F32) {
+        // rounds of tiles over the compute units, in units of 32 outputs
+        int64_t best = 0;
+        int fa = 0;
+        for (int f : {8, 7, 6}) {
+            const int64_t tiles = (M + 32 * f - 1) / (32 * f) * ((T + 255) / 256), cost = (tiles + ncu - 1) / ncu * f;
+            if (tiles >= ncu * 3 / 4 && (fa == 0 || cost < best)) best = cost, fa = f;
+        }
+        if (fa) return {fa, 1};
+    }
     int64_t splits = mid >= ncu ? 1 : 2 * ncu / mid;
     if (splits > kb / 4) splits = kb / 4 > 1 ? kb / 4 : 1;
-    return {false, uint32_t(splits)};
+    return {0, uint32_t(splits)};
+}
+
+template <int YD>
+void launch_big(const GemmArgs& a, int fa, unsigned grid, hipStream_t st) {
+    if (fa == 8)
+        fp8_gemm_big_kernel<YD, 8><<<grid, 512, kBigLds, st>>>(a);
+    else if (fa == 7)
+        fp8_gemm_big_kernel<YD, 7><<<grid, 512, kBigLds, st>>>(a);
+    else
+        fp8_gemm_big_kernel<YD, 6><<<grid, 512, kBigLds, st>>>(a);
 }
 
 }  // namespace
@@ -381,15 +436,15 @@ size_t fp8_gemm_workspace(int64_t M, int64_t T, uint32_t kb, int ydt) {
 
 sketch_status launch_fp8_gemm(const Fp8Product& p, void* ws, hipStream_t st) {
     const GemmPlan g = gemm_plan(p.M, p.T, p.kb, p.ydt);
-    const int64_t edge = g.big ? 256 : 128;
-    GemmArgs a{p, uint32_t((p.M + edge - 1) / edge), uint32_t((p.T + edge - 1) / edge), g.splits, static_cast<float*>(ws)};
+    const int64_t rows = g.fa ? 32 * g.fa : 128, cols = g.fa ? 256 : 128;
+    GemmArgs a{p, uint32_t((p.M + rows - 1) / rows), uint32_t((p.T + cols - 1) / cols), g.splits, static_cast<float*>(ws)};
     const int64_t tiles = int64_t(a.tiles_o) * a.tiles_t;
     if (tiles > 0x7FFFFFFF) return SKETCH_EINVAL;
-    if (g.big) {
+    if (g.fa) {
         if (p.ydt == SKETCH_BF16)
-            fp8_gemm_big_kernel<SKETCH_BF16><<<unsigned(tiles), 512, kBigLds, st>>>(a);
+            launch_big<SKETCH_BF16>(a, g.fa, unsigned(tiles), st);
         else
-            fp8_gemm_big_kernel<SKETCH_F16><<<unsigned(tiles), 512, kBigLds, st>>>(a);
+            launch_big<SKETCH_F16>(a, g.fa, unsigned(tiles), st);
         return launch_status();
     }
     auto go = [&](auto product, auto add) {
