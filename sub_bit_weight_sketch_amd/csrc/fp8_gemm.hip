@@ -86,11 +86,21 @@ __device__ inline void store4(void* Y, int64_t e, f32x4 v, int64_t m, int64_t M,
 // to a SIMD, each 16 FA x 64: 4 FA accumulators of 16x16.  FA is 8, or 7 or 6
 // where that many more tiles fill their last round over the compute units
 // better (28672 outputs x 2048 tokens: 896 tiles are 3.5 rounds, 1024 are 4).
-//  The waves work in two
-// groups, one on each SIMD, half a step apart: while one group runs the
-// MFMAs of its step from registers, the other reads its fragments from LDS,
-// so the matrix cores always have one wave's work and LDS the other's.  A
-// step's 64 KiB are loaded while the step before is worked on.
+//
+// The waves work in two groups, one on each SIMD, half a step apart: while one
+// group runs the MFMAs of its step from registers, the other reads its
+// fragments from LDS, so the matrix cores always have one wave's work and LDS
+// the other's.  Group g has the outputs 16 FA g .. of the tile.  In phase 2k
+// group 0 reads step k, in phase 2k + 1 group 1 does; each multiplies in the
+// phase after.
+//
+// Loads go out between the MFMAs, not before them: 64 of them at the start of
+// a phase held up the phase's MFMAs by as long as these take (443 -> 359 us
+// for 28672 x 8192 at 2048 tokens).  What a load overwrites has to have been
+// read: group 0 loads its rows of W of step k + 2 in phase 2k + 1; group 1 its
+// own and X, which both read, in phase 2k + 2.  The loads of steps past the
+// last repeat it, into buffers that are done with, so that every phase has the
+// same number of loads to count.
 // ---------------------------------------------------------------------------
 constexpr uint32_t kBigStage = 512 * 128;           // 32 FA rows of W in the first half, 256 of X in the second
 constexpr uint32_t kBigScales = (256 + 16) * 4;     // dwords of 4 steps: one per token, one per 16 outputs
@@ -101,42 +111,37 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
     const Fp8Product& p = a.p;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int r = lane & 15, c = lane >> 4, group = wave >> 2, wm = group * FA * 16, wt = (wave & 3) * 64;
+    const int r = lane & 15, c = lane >> 4, group = wave >> 2, w4 = wave & 3, wm = group * FA * 16, wt = w4 * 64;
     uint32_t to, tt;
     tile_of(a, to, tt);
     constexpr int kRows = 32 * FA;
+    constexpr int kTurns = (2 * FA + 3) / 4;   // loads of 8 rows that a wave has of its group's 16 FA rows of W
     const int64_t o0 = int64_t(to) * kRows, t0 = int64_t(tt) * 256;
 
-    // loads of this wave: every eighth 8 rows of W and of X
     const uint8_t *wbase = p.w + o0 * p.ld, *xbase = p.x + t0 * p.ld;
     const uint32_t wlast = uint32_t(min(int64_t(kRows - 1), p.M - 1 - o0)), xlast = uint32_t(min(int64_t(255), p.T - 1 - t0));
     const uint32_t piece = uint32_t((lane & 7) ^ (lane >> 3)) * 16, ld = uint32_t(p.ld);
-    uint32_t woff[4], xoff[4];
+    uint32_t woff[kTurns], xoff[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t row = uint32_t((i * 8 + wave) * 8 + (lane >> 3));
-        woff[i] = min(row, wlast) * ld + piece;
-        xoff[i] = min(row, xlast) * ld + piece;
-    }
-    // scales: waves 0..3 the tokens', wave 4 the outputs' (a row of 16 outputs lies in one block of 128)
-    const uint8_t* sbase = wave < 4 ? p.xs + t0 * p.lds : p.ws;
-    const uint32_t srow = wave < 4 ? min(uint32_t(wave * 64 + lane), xlast)
-                                   : uint32_t(min(o0 + (lane & 15) * 16, p.M - 1) / 128);
-    const uint32_t soff = srow * uint32_t(p.lds);
-    const uint32_t lds0 = lds_address(lds), lw = lds0 + wave * 1024, lx = lw + 32768;
-    const uint32_t lsc = lds0 + 2 * kBigStage + (wave < 4 ? wave * 256 : 1024);
+    for (int i = 0; i < kTurns; ++i)   // a turn past the group's rows repeats its last 8
+        woff[i] = min(uint32_t(wm + min(i * 4 + w4, 2 * FA - 1) * 8 + (lane >> 3)), wlast) * ld + piece;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) xoff[i] = min(uint32_t((i * 4 + w4) * 8 + (lane >> 3)), xlast) * ld + piece;
+    // scales, by group 1: each wave 64 tokens', and all of them the outputs' (16 outputs lie in one block of 128)
+    const uint8_t *xsbase = p.xs + t0 * p.lds;
+    const uint32_t xsoff = min(uint32_t(w4 * 64 + lane), xlast) * uint32_t(p.lds);
+    const uint32_t wsoff = uint32_t(min(o0 + min(lane, 2 * FA - 1) * 16, p.M - 1) / 128) * uint32_t(p.lds);
+    const uint32_t lds0 = lds_address(lds), lx = lds0 + 32768 + w4 * 1024, lsc = lds0 + 2 * kBigStage;
+    uint32_t lw[kTurns];
+#pragma unroll
+    for (int i = 0; i < kTurns; ++i) lw[i] = lds0 + uint32_t(wm / 8 + min(i * 4 + w4, 2 * FA - 1)) * 1024;
 
-    auto load_step = [&](uint32_t k) {
-        const uint32_t st = (k & 1) * kBigStage;
-        const uint8_t *wk = wbase + size_t(k) * 128, *xk = xbase + size_t(k) * 128;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (i * 8 + 8 <= 4 * FA || i * 8 + wave < 4 * FA) dma16(wk, woff[i], lw + st + i * 8192);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) dma16(xk, xoff[i], lx + st + i * 8192);
-        if ((k & 3) == 0) {
-            if (wave < 4 || (wave == 4 && lane < 2 * FA)) dma4(sbase + k, soff, lsc + ((k >> 2) & 1) * kBigScales);
-        }
+    auto load_w = [&](uint32_t k, uint32_t buf, int i) { dma16(wbase + size_t(k) * 128, woff[i], lw[i] + buf * kBigStage); };
+    auto load_x = [&](uint32_t k, uint32_t buf, int i) { dma16(xbase + size_t(k) * 128, xoff[i], lx + buf * kBigStage + i * 4096); };
+    auto load_scales = [&](uint32_t k) {   // of steps k .. k + 3
+        const uint32_t to_lds = lsc + ((k >> 2) & 1) * kBigScales;
+        dma4(xsbase + k, xsoff, to_lds + w4 * 256);
+        if (lane < 16) dma4(p.ws + k, wsoff, to_lds + 1024);
     };
 
     f32x4 acc[FA][4];
@@ -145,7 +150,8 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
     i32x8 af[FA], bf[4];
-    int as[FA], bs[4];
+    constexpr int kScales = FA == 8 ? 1 : FA;   // 128 outputs lie in one block
+    int as[kScales], bs[4];
     const unsigned char* frag = lds + r * 128 + ((c ^ (r & 7)) << 4);
     const unsigned char* frag2 = lds + r * 128 + (((c + 4) ^ (r & 7)) << 4);
 
@@ -166,55 +172,74 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 #pragma unroll
             for (int j = 0; j < 4; ++j) bs[j] = sc[wt + j * 16 + r];
 #pragma unroll
-            for (int i = 0; i < FA; ++i) as[i] = sc[256 + wm / 16 + i];
+            for (int i = 0; i < kScales; ++i) as[i] = sc[256 + wm / 16 + i];
         } else {   // the next byte to the low end
 #pragma unroll
             for (int j = 0; j < 4; ++j) bs[j] = int(uint32_t(bs[j]) >> 8);
 #pragma unroll
-            for (int i = 0; i < FA; ++i) as[i] = int(uint32_t(as[i]) >> 8);
+            for (int i = 0; i < kScales; ++i) as[i] = int(uint32_t(as[i]) >> 8);
         }
     };
-    auto compute = [&]() {
+    // the step's MFMAs, with between(n), n < 2 FA, after every two
+    auto compute = [&](auto between) {
         __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-        for (int i = 0; i < FA; ++i)
+        for (int n = 0; n < 2 * FA; ++n) {
+            const int i = n >> 1, j = 2 * (n & 1);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(af[i], bf[j], acc[i][j], 0, 0, 0, as[i],
-                                                                              0, bs[j]);
+            for (int q = j; q < j + 2; ++q)
+                acc[i][q] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(af[i], bf[q], acc[i][q], 0, 0, 0,
+                                                                              as[i % kScales], 0, bs[q]);
+            __builtin_amdgcn_sched_barrier(0);
+            between(n);
+            __builtin_amdgcn_sched_barrier(0);
+        }
         __builtin_amdgcn_s_setprio(0);
     };
 
-    // Step k is read by group 0 in phase 2k and by group 1 in phase 2k + 1;
-    // its buffer is loaded again, with step k + 2, in phase 2k + 2, and that
-    // is waited for at the end of phase 2k + 3.
-    load_step(0);
+    const uint32_t last = p.kb - 1;
+#pragma unroll
+    for (uint32_t k = 0; k < 2; ++k) {
+#pragma unroll
+        for (int i = 0; i < kTurns; ++i) load_w(min(k, last), k, i);
+        if (group == 1) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) load_x(min(k, last), k, i);
+            if (k == 0) load_scales(0);
+        }
+    }
     wait_loads();
     barrier();
     if (group == 0) {
         for (uint32_t k = 0; k < p.kb; ++k) {
-            if (k + 1 < p.kb) load_step(k + 1);
             read_step(k);
             wait_lds();
             barrier();
-            compute();
-            wait_loads();
+            compute([&](int n) {
+                if (n % 2 == 0 && n / 2 < kTurns) load_w(min(k + 2, last), k & 1, n / 2);
+            });
+            asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kTurns) : "memory");   // step k + 1 is here
             barrier();
         }
         barrier();
     } else {
-        if (p.kb > 1) load_step(1);
         barrier();
         for (uint32_t k = 0; k < p.kb; ++k) {
             read_step(k);
             wait_lds();
-            wait_loads();
+            wait_loads();   // step k + 1 is here
             barrier();
-            if (k + 2 < p.kb) load_step(k + 2);
-            compute();
+            if (((k + 2) & 3) == 0 && k + 2 < p.kb) load_scales(k + 2);
+            compute([&](int n) {
+                if (n < 8)
+                    load_x(min(k + 2, last), k & 1, n);
+                else if (n - 8 < kTurns)
+                    load_w(min(k + 2, last), k & 1, n - 8);
+            });
             barrier();
         }
     }
+    wait_loads();
 
     // Whole tiles go out through LDS, 256 contiguous bytes of a token's row and
     // more at a time; the others element by element where they have to.
