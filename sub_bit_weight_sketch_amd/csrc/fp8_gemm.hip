@@ -280,77 +280,82 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 }
 
 // ---------------------------------------------------------------------------
-// 128 outputs x 128 tokens, 4 waves of 64 x 64, two workgroups to a CU: for
+// 128 outputs x 32 FB tokens, 4 waves of 64 x 16 FB, two workgroups to a CU: for
 // fewer tiles than the big kernel needs, and (EXACT) for float32 Y, whose
 // fragments are widened to bfloat16 with their scales applied, so that every
-// product is exact and the sums are float32.  K is split over blockIdx.y when
-// the tiles alone leave compute units idle; the parts are float32 and
+// product is exact and the sums are float32.  The loads of the next step go out
+// first: between the MFMAs, as above, they came too late for a step this short
+// (4096 x 4096 at 2048 tokens 49 -> 53 us).  K is split over blockIdx.y when the
+// tiles alone leave compute units idle; the parts are float32, rows padded to 4 outputs, and
 // fp8_add_kernel adds them in their order.
 // ---------------------------------------------------------------------------
-constexpr uint32_t kMidStage = 256 * 128;
+template <int FB> constexpr uint32_t mid_stage() { return (128 + 32 * FB) * 128; }
 constexpr uint32_t kMidScales = (128 + 64) * 4;
-constexpr uint32_t kMidLds = 2 * kMidStage + 2 * kMidScales;
+template <int FB> constexpr uint32_t mid_lds() { return 2 * mid_stage<FB>() + 2 * kMidScales; }
 
-template <int YD, bool EXACT>
+template <int YD, bool EXACT, int FB>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void fp8_gemm_kernel(GemmArgs a) {
+    static_assert(FB == 4 || FB == 2, "a wave loads FB times 8 rows of X");
     extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
     const Fp8Product& p = a.p;
+    constexpr uint32_t stage = mid_stage<FB>();
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int r = lane & 15, c = lane >> 4, wm = (wave >> 1) * 64, wt = (wave & 1) * 64;
+    const int r = lane & 15, c = lane >> 4, wm = (wave >> 1) * 64, wt = (wave & 1) * 16 * FB;
     uint32_t to, tt;
     tile_of(a, to, tt);
-    const int64_t o0 = int64_t(to) * 128, t0 = int64_t(tt) * 128;
+    const int64_t o0 = int64_t(to) * 128, t0 = int64_t(tt) * (32 * FB);
     const uint32_t kend = uint32_t(uint64_t(p.kb) * (blockIdx.y + 1) / a.splits);
     const uint32_t kbeg = uint32_t(uint64_t(p.kb) * blockIdx.y / a.splits);
 
-    // loads of this wave: 32 rows of W and 32 of X per step; waves 0 and 1 the
+    // loads of this wave: 32 rows of W and 8 FB of X per step; waves 0 and 1 the
     // tokens' scales, wave 2 the outputs' (one block of 128)
     const uint8_t *wbase = p.w + o0 * p.ld, *xbase = p.x + t0 * p.ld;
-    const uint32_t wlast = uint32_t(min(int64_t(127), p.M - 1 - o0)), xlast = uint32_t(min(int64_t(127), p.T - 1 - t0));
+    const uint32_t wlast = uint32_t(min(int64_t(127), p.M - 1 - o0)),
+                   xlast = uint32_t(min(int64_t(32 * FB - 1), p.T - 1 - t0));
     const uint32_t piece = uint32_t((lane & 7) ^ (lane >> 3)) * 16, ld = uint32_t(p.ld);
-    uint32_t woff[4], xoff[4];
+    uint32_t woff[4], xoff[FB];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t row = uint32_t(wave * 32 + i * 8 + (lane >> 3));
-        woff[i] = min(row, wlast) * ld + piece;
-        xoff[i] = min(row, xlast) * ld + piece;
-    }
+    for (int i = 0; i < 4; ++i) woff[i] = min(uint32_t((i * 4 + wave) * 8 + (lane >> 3)), wlast) * ld + piece;
+#pragma unroll
+    for (int i = 0; i < FB; ++i) xoff[i] = min(uint32_t((i * 4 + wave) * 8 + (lane >> 3)), xlast) * ld + piece;
     const uint8_t* sbase = wave < 2 ? p.xs + t0 * p.lds : p.ws + o0 / 128 * p.lds;
     const uint32_t soff = wave < 2 ? min(uint32_t(wave * 64 + lane), xlast) * uint32_t(p.lds) : 0;
-    const uint32_t lds0 = lds_address(lds), lw = lds0 + wave * 4096, lx = lw + 16384;
-    const uint32_t lsc = lds0 + 2 * kMidStage + wave * 256;
-    auto load_step = [&](uint32_t k) {
-        const uint32_t st = ((k - kbeg) & 1) * kMidStage;
-        const uint8_t *wk = wbase + size_t(k) * 128, *xk = xbase + size_t(k) * 128;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) dma16(wk, woff[i], lw + st + i * 1024);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) dma16(xk, xoff[i], lx + st + i * 1024);
-        if (((k & 3) == 0 || k == kbeg) && wave < 3) dma4(sbase + (k & ~3u), soff, lsc + ((k >> 2) & 1) * kMidScales);
+    const uint32_t lds0 = lds_address(lds), lw = lds0 + wave * 1024, lx = lw + 16384;
+    const uint32_t lsc = lds0 + 2 * stage + wave * 256;
+    auto load_part = [&](uint32_t k, int i) {   // i < 4
+        const uint32_t st = ((k - kbeg) & 1) * stage;
+        dma16(wbase + size_t(k) * 128, woff[i], lw + st + i * 4096);
+        if (i < FB) dma16(xbase + size_t(k) * 128, xoff[i], lx + st + i * 4096);
+        if (i == 0 && ((k & 3) == 0 || k == kbeg) && wave < 3)
+            dma4(sbase + (k & ~3u), soff, lsc + ((k >> 2) & 1) * kMidScales);
     };
 
-    f32x4 acc[4][4];
+    f32x4 acc[4][FB];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+        for (int j = 0; j < FB; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
     const unsigned char* frag = lds + r * 128 + ((c ^ (r & 7)) << 4);
     const unsigned char* frag2 = lds + r * 128 + (((c + 4) ^ (r & 7)) << 4);
 
-    if (kbeg < kend) load_step(kbeg);
+    if (kbeg < kend)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) load_part(kbeg, i);
     for (uint32_t k = kbeg; k < kend; ++k) {
         wait_loads();
         barrier();   // step k is here, and every wave is done with step k - 1
-        if (k + 1 < kend) load_step(k + 1);
-        const uint32_t st = ((k - kbeg) & 1) * kMidStage;
+        if (k + 1 < kend)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) load_part(k + 1, i);
+        const uint32_t st = ((k - kbeg) & 1) * stage;
         const unsigned char *f1 = frag + st + wm * 128, *f2 = frag2 + st + wm * 128;
         const unsigned char *g1 = frag + st + 16384 + wt * 128, *g2 = frag2 + st + 16384 + wt * 128;
-        const int* sc = reinterpret_cast<const int*>(lds + 2 * kMidStage + ((k >> 2) & 1) * kMidScales);
+        const int* sc = reinterpret_cast<const int*>(lds + 2 * stage + ((k >> 2) & 1) * kMidScales);
         const uint32_t as = uint32_t(sc[128]) >> (8 * (k & 3)) & 255u;
-        i32x8 af[4], bf[4];
-        uint32_t bs[4];
+        i32x8 af[4], bf[FB];
+        uint32_t bs[FB];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < FB; ++j) {
             bf[j] = __builtin_shufflevector(*reinterpret_cast<const i32x4*>(g1 + j * 2048),
                                             *reinterpret_cast<const i32x4*>(g2 + j * 2048), 0, 1, 2, 3, 4, 5, 6, 7);
             bs[j] = uint32_t(sc[wt + j * 16 + r]) >> (8 * (k & 3)) & 255u;
@@ -360,73 +365,75 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
             af[i] = __builtin_shufflevector(*reinterpret_cast<const i32x4*>(f1 + i * 2048),
                                             *reinterpret_cast<const i32x4*>(f2 + i * 2048), 0, 1, 2, 3, 4, 5, 6, 7);
         if constexpr (EXACT) {
-            bf16x8 bw[4][4];
+            bf16x8 bw[FB][4];
             const float asf = fp8_scale(as);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int j = 0; j < FB; ++j)
 #pragma unroll
                 for (int q = 0; q < 4; ++q) bw[j][q] = fp8_widen(bf[j][2 * q], bf[j][2 * q + 1], fp8_scale(bs[j]));
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 4; ++i) {
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     const bf16x8 aw = fp8_widen(af[i][2 * q], af[i][2 * q + 1], asf);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
+                    for (int j = 0; j < FB; ++j)
                         acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(aw, bw[j][q], acc[i][j], 0, 0, 0);
                 }
+            }
         } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 4; ++i) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
+                for (int j = 0; j < FB; ++j)
                     acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(af[i], bf[j], acc[i][j], 0, 0, 0,
                                                                                   int(as), 0, int(bs[j]));
+            }
         }
     }
 
+    const int64_t ldy = a.splits > 1 ? (p.M + 3) / 4 * 4 : p.M;
+    float* part = a.parts + int64_t(blockIdx.y) * p.T * ldy;
     const bool vec = p.M % 4 == 0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < FB; ++j) {
         const int64_t t = t0 + wt + j * 16 + r;
         if (t >= p.T) continue;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int64_t m = o0 + wm + i * 16 + 4 * c;
-            if (a.splits > 1)
-                store4<SKETCH_F32>(a.parts + (blockIdx.y * p.T) * p.M, t * p.M + m, acc[i][j], m, p.M, vec);
-            else
+            if (a.splits > 1) {
+                if (m < p.M) *reinterpret_cast<f32x4*>(part + t * ldy + m) = acc[i][j];   // the padding too
+            } else {
                 store4<YD>(p.Y, t * p.M + m, acc[i][j], m, p.M, vec);
-        }
-    }
-}
-
-template <int YD>
-__global__ __launch_bounds__(256) void fp8_add_kernel(GemmArgs a) {
-    const int64_t n = a.p.T * a.p.M, step = int64_t(gridDim.x) * 1024;
-    for (int64_t e = (int64_t(blockIdx.x) * 256 + threadIdx.x) * 4; e < n; e += step) {
-        if (n % 4 == 0) {   // planes keep their 16-byte alignment
-            f32x4 sum = *reinterpret_cast<const f32x4*>(a.parts + e);
-            for (uint32_t s = 1; s < a.splits; ++s) sum += *reinterpret_cast<const f32x4*>(a.parts + s * n + e);
-            store4<YD>(a.p.Y, e, sum, 0, 4, true);
-        } else {
-            for (int64_t i = e; i < n && i < e + 4; ++i) {
-                float sum = a.parts[i];
-                for (uint32_t s = 1; s < a.splits; ++s) sum += a.parts[s * n + i];
-                store1_val<YD>(a.p.Y, i, sum);
             }
         }
     }
 }
 
+// Y from the parts, 4 outputs to a thread.
+template <int YD>
+__global__ __launch_bounds__(256) void fp8_add_kernel(GemmArgs a) {
+    const int64_t ldy = (a.p.M + 3) / 4 * 4, m = (int64_t(blockIdx.x) * 256 + threadIdx.x) * 4, t = blockIdx.y;
+    if (m >= a.p.M) return;
+    const float* part = a.parts + t * ldy + m;
+    f32x4 sum = *reinterpret_cast<const f32x4*>(part);
+#pragma unroll 4
+    for (uint32_t s = 1; s < a.splits; ++s) sum += *reinterpret_cast<const f32x4*>(part + s * a.p.T * ldy);
+    store4<YD>(a.p.Y, t * a.p.M + m, sum, m, a.p.M, a.p.M % 4 == 0);
+}
+
 // Which kernel a product takes, and over how many workgroups K is split.
 struct GemmPlan {
     int fa;            // of the big kernel, 0: fp8_gemm_kernel
+    int fb;            // of fp8_gemm_kernel
     uint32_t splits;
 };
 
+constexpr int kSplitTo = 2;
+
 GemmPlan gemm_plan(int64_t M, int64_t T, uint32_t kb, int ydt) {
-    const int64_t ncu = compute_units(), mid = (M + 127) / 128 * ((T + 127) / 128);
+    const int64_t ncu = compute_units();
     if (ydt != SKETCH_F32) {
         // rounds of tiles over the compute units, in units of 32 outputs
         int64_t best = 0;
@@ -435,11 +442,13 @@ GemmPlan gemm_plan(int64_t M, int64_t T, uint32_t kb, int ydt) {
             const int64_t tiles = (M + 32 * f - 1) / (32 * f) * ((T + 255) / 256), cost = (tiles + ncu - 1) / ncu * f;
             if (tiles >= ncu * 3 / 4 && (fa == 0 || cost < best)) best = cost, fa = f;
         }
-        if (fa) return {fa, 1};
+        if (fa) return {fa, 0, 1};
     }
-    int64_t splits = mid >= ncu ? 1 : 2 * ncu / mid;
+    const int fb = T <= 64 ? 2 : 4;
+    const int64_t mid = (M + 127) / 128 * ((T + 32 * fb - 1) / (32 * fb));
+    int64_t splits = mid >= ncu ? 1 : kSplitTo * ncu / mid;
     if (splits > kb / 4) splits = kb / 4 > 1 ? kb / 4 : 1;
-    return {0, uint32_t(splits)};
+    return {0, fb, uint32_t(splits)};
 }
 
 template <int YD>
@@ -456,12 +465,12 @@ void launch_big(const GemmArgs& a, int fa, unsigned grid, hipStream_t st) {
 
 size_t fp8_gemm_workspace(int64_t M, int64_t T, uint32_t kb, int ydt) {
     const GemmPlan g = gemm_plan(M, T, kb, ydt);
-    return g.splits > 1 ? align256(size_t(g.splits) * size_t(M) * size_t(T) * 4) : 0;
+    return g.splits > 1 ? align256(size_t(g.splits) * size_t((M + 3) / 4 * 4) * size_t(T) * 4) : 0;
 }
 
 sketch_status launch_fp8_gemm(const Fp8Product& p, void* ws, hipStream_t st) {
     const GemmPlan g = gemm_plan(p.M, p.T, p.kb, p.ydt);
-    const int64_t rows = g.fa ? 32 * g.fa : 128, cols = g.fa ? 256 : 128;
+    const int64_t rows = g.fa ? 32 * g.fa : 128, cols = g.fa ? 256 : 32 * g.fb;
     GemmArgs a{p, uint32_t((p.M + rows - 1) / rows), uint32_t((p.T + cols - 1) / cols), g.splits, static_cast<float*>(ws)};
     const int64_t tiles = int64_t(a.tiles_o) * a.tiles_t;
     if (tiles > 0x7FFFFFFF) return SKETCH_EINVAL;
@@ -472,17 +481,23 @@ sketch_status launch_fp8_gemm(const Fp8Product& p, void* ws, hipStream_t st) {
             launch_big<SKETCH_F16>(a, g.fa, unsigned(tiles), st);
         return launch_status();
     }
-    auto go = [&](auto product, auto add) {
-        product<<<dim3(unsigned(tiles), g.splits), 256, kMidLds, st>>>(a);
+    auto go = [&](auto four, auto two, auto add) {
+        const dim3 grid(unsigned(tiles), g.splits);
+        if (g.fb == 4)
+            four<<<grid, 256, mid_lds<4>(), st>>>(a);
+        else
+            two<<<grid, 256, mid_lds<2>(), st>>>(a);
         if (g.splits == 1) return launch_status();
         if (hipGetLastError() != hipSuccess) return SKETCH_EDEVICE;
-        const int64_t blocks = (p.T * p.M + 1023) / 1024;
-        add<<<unsigned(blocks < 2048 ? blocks : 2048), 256, 0, st>>>(a);
+        add<<<dim3(unsigned((p.M + 1023) / 1024), unsigned(p.T)), 256, 0, st>>>(a);
         return launch_status();
     };
-    return p.ydt == SKETCH_F32    ? go(fp8_gemm_kernel<SKETCH_F32, true>, fp8_add_kernel<SKETCH_F32>)
-           : p.ydt == SKETCH_BF16 ? go(fp8_gemm_kernel<SKETCH_BF16, false>, fp8_add_kernel<SKETCH_BF16>)
-                                  : go(fp8_gemm_kernel<SKETCH_F16, false>, fp8_add_kernel<SKETCH_F16>);
+    if (p.ydt == SKETCH_F32)
+        return go(fp8_gemm_kernel<SKETCH_F32, true, 4>, fp8_gemm_kernel<SKETCH_F32, true, 2>, fp8_add_kernel<SKETCH_F32>);
+    if (p.ydt == SKETCH_BF16)
+        return go(fp8_gemm_kernel<SKETCH_BF16, false, 4>, fp8_gemm_kernel<SKETCH_BF16, false, 2>,
+                  fp8_add_kernel<SKETCH_BF16>);
+    return go(fp8_gemm_kernel<SKETCH_F16, false, 4>, fp8_gemm_kernel<SKETCH_F16, false, 2>, fp8_add_kernel<SKETCH_F16>);
 }
 
 }  // namespace sketch
