@@ -58,6 +58,13 @@ __device__ inline uint16_t take_bf16(float& v) {
     return uint16_t(u >> 16);
 }
 
+__device__ inline u32x4 take8(float (&v)[8]) {
+    uint32_t h[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) h[q] = take_bf16(v[q]);
+    return u32x4{h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16)};
+}
+
 // Logits of expert blockIdx.x for NT tokens; the sums are float64,
 // so that no two logits change places by rounding.  All workgroups also share
 // out the split of x.
@@ -88,22 +95,17 @@ __global__ __launch_bounds__(256) void moe_logits_kernel(MoeArgs a) {
         float v[8];
         load_row8<DT>(a.X, t, a.H, j, v);
 #pragma unroll
-        for (int s = 0; s < x_terms<DT>(); ++s) {
-            uint32_t h[8];
-#pragma unroll
-            for (int q = 0; q < 8; ++q) h[q] = take_bf16(v[q]);
-            *reinterpret_cast<u32x4*>(a.xs + s * total + u) =
-                u32x4{h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16)};
-        }
+        for (int s = 0; s < x_terms<DT>(); ++s) *reinterpret_cast<u32x4*>(a.xs + s * total + u) = take8(v);
     }
     __syncthreads();
     if (tid < NT && t0 + tid < a.T)
         a.logits[int64_t(t0 + tid) * a.E + e] = (part[0][tid] + part[1][tid]) + (part[2][tid] + part[3][tid]);
 }
 
-// Order of the logits as unsigned integers; NaN is the largest, 0 is free.
+// Order of the logits as unsigned integers; NaN is the largest, 0 and the
+// largest uint64 are free.
 __device__ inline uint64_t order_key(double l) {
-    if (l != l) return ~0ull;
+    if (l != l) return ~0ull - 1;
     const uint64_t u = uint64_t(__double_as_longlong(l + 0.0));   // -0 -> +0
     return u >> 63 ? ~u : u | (1ull << 63);
 }
@@ -113,11 +115,13 @@ __device__ inline void top_k(const double* l, int E, int topk, int lane, int32_t
     if (E <= 64) {   // each lane counts the experts before its own
         const uint64_t key = lane < E ? order_key(l[lane]) : 0;
         int rank = 0;
-        for (int j = 0; j < E; ++j) {
-            const uint64_t other = uint64_t(uint32_t(__builtin_amdgcn_readlane(int(key >> 32), j))) << 32 |
-                                   uint32_t(__builtin_amdgcn_readlane(int(key), j));
-            rank += other > key || (other == key && j < lane);
-        }
+        for (int j0 = 0; j0 < E; j0 += 8)   // lanes past E have key 0, before nobody
+#pragma unroll
+            for (int j = j0; j < j0 + 8; ++j) {
+                const uint64_t other = uint64_t(uint32_t(__builtin_amdgcn_readlane(int(key >> 32), j))) << 32 |
+                                       uint32_t(__builtin_amdgcn_readlane(int(key), j));
+                rank += other + (j < lane) > key;   // j's earlier than the lane's come before it when equal
+            }
         if (lane < E && rank < topk) ids[rank] = lane;
         return;
     }
@@ -144,46 +148,57 @@ __device__ inline void top_k(const double* l, int E, int topk, int lane, int32_t
     }
 }
 
-// The top k of every token and the segments, by a whole workgroup.
-__device__ void build_route(const MoeArgs& a, Route& rt, int32_t* ids) {
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    for (int t = wave; t < a.T; t += kWaves) top_k(a.logits + int64_t(t) * a.E, a.E, a.topk, lane, ids + t * a.topk);
+// The top k of every token and the segments, by a whole workgroup.  An
+// expert's tokens are a bit mask: a token's place is the bits before its own.
+static_assert(SKETCH_MOE_MAX_TOKENS <= 64, "one bit per token");
+
+__device__ inline void build_route(const MoeArgs& a, const double* logits, Route& rt, int32_t* ids) {
+    __shared__ uint64_t mask[SKETCH_MOE_MAX_EXPERTS];
+    __shared__ int32_t start[SKETCH_MOE_MAX_EXPERTS];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, P = a.T * a.topk;
+    for (int e = tid; e < a.E; e += kWaves * 64) mask[e] = 0;
+    for (int t = wave; t < a.T; t += kWaves) top_k(logits + int64_t(t) * a.E, a.E, a.topk, lane, ids + t * a.topk);
     __syncthreads();
-    const int P = a.T * a.topk;
-    for (int p = tid; p < P; p += kWaves * 64) {
-        const int e = ids[p];
-        int pos = 0;
-        for (int q = 0; q < P; ++q) pos += ids[q] < e || (ids[q] == e && q < p);
-        rt.pair[pos] = p;
-    }
+    for (int p = tid; p < P; p += kWaves * 64)
+        atomicOr(reinterpret_cast<unsigned long long*>(&mask[ids[p]]), 1ull << (p / a.topk));
     __syncthreads();
     if (wave == 0) {
-        int n = 0;
-        for (int p0 = 0; p0 < P; p0 += 64) {
-            const int p = p0 + lane;
-            const int e = p < P ? ids[rt.pair[p]] : -1;
-            const bool head = p < P && (p == 0 || ids[rt.pair[p - 1]] != e);
-            const uint64_t heads = __ballot(head);
-            if (head) {
-                const int i = n + __popcll(heads & ((1ull << lane) - 1));
-                rt.expert[i] = e;
-                rt.begin[i] = p;
+        int nact = 0, pairs = 0;
+        for (int e0 = 0; e0 < a.E; e0 += 64) {
+            const int e = e0 + lane, count = e < a.E ? __popcll(mask[e]) : 0;
+            int before = count;   // inclusive sum over the lanes
+#pragma unroll
+            for (int d = 1; d < 64; d <<= 1) {
+                const int up = __shfl_up(before, d);
+                if (lane >= d) before += up;
             }
-            n += __popcll(heads);
+            const uint64_t active = __ballot(count > 0);
+            if (count > 0) {
+                const int i = nact + __popcll(active & ((1ull << lane) - 1));
+                rt.expert[i] = e;
+                rt.begin[i] = start[e] = pairs + before - count;
+            }
+            nact += __popcll(active);
+            pairs += __shfl(before, 63);
         }
         if (lane == 0) {
-            rt.nact = n;
-            rt.begin[n] = P;
+            rt.nact = nact;
+            rt.begin[nact] = P;
         }
+    }
+    __syncthreads();
+    for (int p = tid; p < P; p += kWaves * 64) {
+        const int e = ids[p];
+        rt.pair[start[e] + __popcll(mask[e] & ((1ull << (p / a.topk)) - 1))] = p;
     }
     __syncthreads();
 }
 
 // The route and the weights to memory, for the caller and the next launch.
-__device__ void publish_route(const MoeArgs& a, const Route& rt, const int32_t* ids) {
+__device__ inline void publish_route(const MoeArgs& a, const double* logits, const Route& rt, const int32_t* ids) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, P = a.T * a.topk;
     for (int t = wave; t < a.T; t += kWaves) {
-        const double* l = a.logits + int64_t(t) * a.E;
+        const double* l = logits + int64_t(t) * a.E;
         const double top = l[ids[t * a.topk]];
         double sum = 0.0;
         if (!a.renorm)
@@ -226,22 +241,66 @@ __device__ inline void keep_order() { asm volatile("" ::: "memory"); }
 // Gate and up: a workgroup takes 16 rows of one active expert at a time, its
 // waves share out the runs of kUpRun blocks of 128 columns, and their sums meet
 // in LDS.  The last workgroup only publishes the route.
+//
+// FEW (few tokens, a small router): every workgroup sums the logits for itself
+// and splits x into LDS, instead of the launch before this one (1 token, 8
+// experts of 512 x 256: 2.6 + 6.4 us in two launches, 7.0 us in one; with a
+// router of 8 x 4096 4.7 + 43.5 us against 50.2 us, no gain any more).
 constexpr int kUpRun = 2;
+constexpr int kFewTokens = 4, kFewLogits = 4 * kWaves;
+constexpr int64_t kFewTerms = 16384;   // tokens x experts x columns
+constexpr size_t kFewLds = 32 * 1024;
 
-template <int NS>
+template <int DT, bool FEW>
 __global__ __launch_bounds__(kWaves * 64) void moe_up_kernel(MoeArgs a) {
+    constexpr int NS = x_terms<DT>();
+    extern __shared__ __attribute__((aligned(16))) uint16_t xlds[];   // FEW: [terms][T][ldh]
     __shared__ Route rt;
     __shared__ int32_t ids[kMaxPairs];
     __shared__ float part[kWaves][2][16][17];
+    __shared__ double logits[FEW ? kFewLogits : 1];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r = lane & 15, c = lane >> 4;
-    build_route(a, rt, ids);
+    const int64_t plane = int64_t(a.T) * a.ldh;
+    if constexpr (FEW) {
+        constexpr int kEach = kFewLogits / kWaves;   // (token, expert) wave + 8 i
+        const int n = a.T * a.E;
+        double sum[kEach] = {};
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            const int at = wave + kWaves * i;
+            if (at >= n) break;
+            for (int64_t j = lane * 8; j < a.H; j += 512) {
+                float x[8], w[8];
+                load_row8<DT>(a.X, at / a.E, a.H, j, x);
+                load_row8<DT>(a.router, at % a.E, a.H, j, w);
+#pragma unroll
+                for (int q = 0; q < 8; ++q) sum[i] += double(x[q]) * double(w[q]);
+            }
+        }
+        for (int64_t u = tid * 8; u < plane; u += kWaves * 64 * 8) {
+            const int64_t t = u / a.ldh, j = u % a.ldh;
+            float v[8];
+            load_row8<DT>(a.X, t, a.H, j, v);
+#pragma unroll
+            for (int s = 0; s < NS; ++s) *reinterpret_cast<u32x4*>(xlds + s * plane + u) = take8(v);
+        }
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+#pragma unroll
+            for (int d = 1; d < 64; d <<= 1) sum[i] += __shfl_xor(sum[i], d);
+            if (lane == 0 && wave + kWaves * i < n) logits[wave + kWaves * i] = sum[i];
+        }
+        __syncthreads();
+    }
+    const double* l = FEW ? logits : a.logits;
+    build_route(a, l, rt, ids);
     if (blockIdx.x == gridDim.x - 1) {
-        publish_route(a, rt, ids);
+        publish_route(a, l, rt, ids);
         return;
     }
     const int tiles = int(a.ldi / 16), items = rt.nact * tiles, kbs = int(a.ldh / 128);
-    const int64_t plane = int64_t(a.T) * a.ldh, hplane = int64_t(a.T) * a.topk * a.ldi;
+    const int64_t hplane = int64_t(a.T) * a.topk * a.ldi;
     for (int it = blockIdx.x; it < items; it += gridDim.x - 1) {
         const int act = it / tiles, m0 = it % tiles * 16, e = __builtin_amdgcn_readfirstlane(rt.expert[act]);
         const int pend = __builtin_amdgcn_readfirstlane(rt.begin[act + 1]);
@@ -251,7 +310,7 @@ __global__ __launch_bounds__(kWaves * 64) void moe_up_kernel(MoeArgs a) {
         const int64_t srow = min(int64_t(m0), a.I - 1) / 128 * a.gu_lds;
         const uint8_t *gs = G + a.gu_scales + srow, *us = U + a.gu_scales + srow;
         for (int p0 = __builtin_amdgcn_readfirstlane(rt.begin[act]); p0 < pend; p0 += 16) {
-            const uint16_t* x = a.xs + int64_t(rt.pair[min(p0 + r, pend - 1)] / a.topk) * a.ldh;
+            const uint16_t* x = (FEW ? xlds : a.xs) + int64_t(rt.pair[min(p0 + r, pend - 1)] / a.topk) * a.ldh;
             f32x4 ga = {0, 0, 0, 0}, ua = {0, 0, 0, 0};
             for (int k0 = wave * kUpRun; k0 < kbs; k0 += kWaves * kUpRun) {
                 u32x4 gw[kUpRun][2], uw[kUpRun][2];
@@ -517,11 +576,16 @@ sketch_status sketch_moe(const sketch_moe_params* p, const void* router, const v
     const unsigned up_grid = unsigned(items < 2 * ncu ? items : 2 * ncu) + 1;
     const size_t lds = size_t(kWaves) * tokens * kDownRows * sizeof(float);
     const int nt = tokens == 1 ? 1 : 4;   // tokens of a workgroup that sums logits
-    auto go = [&](auto one, auto four, auto gate_up) {
-        const auto logits = tokens == 1 ? one : four;
-        logits<<<dim3(unsigned(p->E), unsigned((tokens + nt - 1) / nt)), 256, 0, st>>>(a);
-        if (hipGetLastError() != hipSuccess) return SKETCH_EDEVICE;
-        gate_up<<<up_grid, kWaves * 64, 0, st>>>(a);
+    auto go = [&](auto one, auto four, auto gate_up, auto gate_up_few, int terms) {
+        const size_t xlds = size_t(terms) * tokens * L.gu.ld * 2;
+        if (tokens <= kFewTokens && tokens * p->E <= kFewLogits && tokens * p->E * p->H <= kFewTerms && xlds <= kFewLds) {
+            gate_up_few<<<up_grid, kWaves * 64, xlds, st>>>(a);
+        } else {
+            const auto logits = tokens == 1 ? one : four;
+            logits<<<dim3(unsigned(p->E), unsigned((tokens + nt - 1) / nt)), 256, 0, st>>>(a);
+            if (hipGetLastError() != hipSuccess) return SKETCH_EDEVICE;
+            gate_up<<<up_grid, kWaves * 64, 0, st>>>(a);
+        }
         if (hipGetLastError() != hipSuccess) return SKETCH_EDEVICE;
         moe_down_kernel<<<unsigned(L.groups * L.splits), kWaves * 64, lds, st>>>(a);
         if (L.splits == 1) return launch_status();
@@ -529,9 +593,17 @@ sketch_status sketch_moe(const sketch_moe_params* p, const void* router, const v
         moe_add_kernel<<<unsigned((tokens * p->H + 255) / 256), 256, 0, st>>>(a);
         return launch_status();
     };
-    if (p->x_dtype == SKETCH_F32) return go(moe_logits_kernel<SKETCH_F32, 1>, moe_logits_kernel<SKETCH_F32, 4>, moe_up_kernel<3>);
-    if (p->x_dtype == SKETCH_BF16) return go(moe_logits_kernel<SKETCH_BF16, 1>, moe_logits_kernel<SKETCH_BF16, 4>, moe_up_kernel<1>);
-    return go(moe_logits_kernel<SKETCH_F16, 1>, moe_logits_kernel<SKETCH_F16, 4>, moe_up_kernel<2>);
+    switch (p->x_dtype) {
+        case SKETCH_F32:
+            return go(moe_logits_kernel<SKETCH_F32, 1>, moe_logits_kernel<SKETCH_F32, 4>, moe_up_kernel<SKETCH_F32, false>,
+                      moe_up_kernel<SKETCH_F32, true>, 3);
+        case SKETCH_BF16:
+            return go(moe_logits_kernel<SKETCH_BF16, 1>, moe_logits_kernel<SKETCH_BF16, 4>,
+                      moe_up_kernel<SKETCH_BF16, false>, moe_up_kernel<SKETCH_BF16, true>, 1);
+        default:
+            return go(moe_logits_kernel<SKETCH_F16, 1>, moe_logits_kernel<SKETCH_F16, 4>, moe_up_kernel<SKETCH_F16, false>,
+                      moe_up_kernel<SKETCH_F16, true>, 2);
+    }
 }
 
 }  // extern "C"
