@@ -404,6 +404,9 @@ sketch_status sketch_fp8_matmul(const sketch_fp8_params* p, const void* buf, con
         if (!workspace || !aligned16(workspace)) return SKETCH_EINVAL;
         if (workspace_bytes < need) return SKETCH_ESMALL;
     }
+    // grids of the encoding and of the tiles, before either is launched
+    const int64_t kbs = (p->N + 127) / 128;
+    if (batch * ((kbs + 3) / 4) / 4 > 0x7FFFFFF0 || (p->M / 128 + 1) * (batch / 64 + 1) > 0x7FFFFFFF) return SKETCH_EINVAL;
     const hipStream_t st = static_cast<hipStream_t>(stream);
     sketch_fp8_shape s, xs;
     const sketch_fp8_params xp{batch, p->N, 1, 1};

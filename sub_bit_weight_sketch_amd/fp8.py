@@ -7,6 +7,7 @@ Argument marshalling only, as in the rest of the package: ``sketch_fp8_layout``,
 the rest is a convenience layer over them.
 """
 import ctypes
+import functools
 
 import torch
 
@@ -137,22 +138,30 @@ def _aligned(t):
     return t if t.data_ptr() % 16 == 0 else t.clone()
 
 
+@functools.lru_cache(maxsize=1024)
+def _shape(M, N, block_rows, count):
+    """Parameters, their reference and the layout of one kind of buffer."""
+    p = Fp8Params(M, N, block_rows, count)
+    return p, ctypes.byref(p), sketch_fp8_layout(p)
+
+
 class Fp8Tables:
     """A matrix [M, N] (or a stack [count, M, N]) as e4m3 codes and block
     scales, in the buffer layout of the C ABI (a uint8 device tensor)."""
 
     def __init__(self, M, N, block_rows=128, count=None, device="cuda", buf=None):
-        _need(count is None or count > 0, "an empty stack of matrices")
+        if count is not None and count < 1:
+            raise ValueError("an empty stack of matrices")
         self.M, self.N, self.block_rows, self.count = int(M), int(N), int(block_rows), count
-        self.params = Fp8Params(self.M, self.N, self.block_rows, 1 if count is None else int(count))
-        self.layout = sketch_fp8_layout(self.params)
-        n = (1 if count is None else int(count)) * self.layout.bytes
+        stack = 1 if count is None else int(count)
+        self.params, self._ref, self.layout = _shape(self.M, self.N, self.block_rows, stack)
+        n = stack * self.layout.bytes
         if buf is None:
             buf = torch.empty(n, dtype=torch.uint8, device=device)
-        _need(buf.dtype == torch.uint8 and buf.is_contiguous() and buf.numel() >= n and buf.data_ptr() % 16 == 0,
-              "the buffer must be %d dense, 16-byte aligned bytes" % n)
-        self.buf, self.device = buf, buf.device
-        self._at, self._ref = buf.data_ptr(), ctypes.byref(self.params)
+        else:
+            _need(buf.dtype == torch.uint8 and buf.is_contiguous() and buf.numel() >= n and buf.data_ptr() % 16 == 0,
+                  "the buffer must be %d dense, 16-byte aligned bytes" % n)
+        self.buf, self.device, self._at = buf, buf.device, buf.data_ptr()
         self._ws = {}
 
     @property
@@ -185,6 +194,9 @@ def fp8_encode(W, block_rows=128, check=True, status=None):
     of one element, when given."""
     if W.dim() not in (2, 3) or not W.is_cuda:
         raise ValueError("W must be a 2-D GPU tensor, or a 3-D one for a stack of matrices")
+    if status is not None:
+        _need(status.dtype == torch.int32 and status.numel() >= 1 and status.device == W.device,
+              "status must be an int32 tensor on W's device")
     dtype_code(W)
     W = _aligned(W)
     t = Fp8Tables(W.shape[-2], W.shape[-1], block_rows, W.shape[0] if W.dim() == 3 else None, W.device)
@@ -204,6 +216,8 @@ def fp8_tables(codes, scales, block_rows=128):
     """Fp8Tables from codes [M, N] (float8_e4m3fn, or their uint8 bits) and
     biased scale exponents [row blocks, column blocks] (float8_e8m0fnu, or
     uint8), or stacks of both: a copy into the library's layout."""
+    _need(codes.dtype in (torch.uint8, torch.float8_e4m3fn) and scales.dtype in (torch.uint8, torch.float8_e8m0fnu),
+          "codes must be float8_e4m3fn and scales float8_e8m0fnu, or the uint8 bits of these")
     codes, scales = codes.view(torch.uint8), scales.view(torch.uint8)
     _need(codes.dim() in (2, 3) and codes.is_cuda and scales.device == codes.device,
           "codes and scales must be 2-D (or 3-D) tensors on one GPU")
@@ -228,8 +242,15 @@ def _workspace_bytes(t, batch, x_dtype, y_dtype):
 def fp8_workspace_for(t, batch, x_dtype, y_dtype, device):
     """Workspace for products of `batch` rows (None if not needed).  Reuse it
     across calls on one stream, never for two calls in flight at once."""
-    n = _workspace_bytes(t, batch, x_dtype, y_dtype)
+    with _On(t.device):
+        n = _workspace_bytes(t, batch, x_dtype, y_dtype)
     return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+
+
+def _given(workspace, device):
+    """Bytes of a workspace the caller gave."""
+    _need(workspace.device == device and workspace.is_contiguous(), "the workspace must be dense, on the same device")
+    return workspace.numel() * workspace.element_size()
 
 
 def _out(out, shape, dtype, device):
@@ -245,7 +266,7 @@ def fp8_matmul(t, X, out=None, workspace=None, dtype=None):
     [N]), encoded row by row on the way in; X may also be an Fp8Tables with
     block_rows=1, for rows that several linears share.  dtype: of Y, float32
     (the default, or that of `out`), bfloat16 or float16; see
-    include/sketch_fp8.h for how the sums of large batches differ."""
+    include/sketch_fp8.h for how their sums differ."""
     if t.block_rows != 128 or t.count is not None:
         raise ValueError("t must be one weight, encoded with block_rows=128")
     rows = isinstance(X, Fp8Tables)
@@ -273,7 +294,7 @@ def fp8_matmul(t, X, out=None, workspace=None, dtype=None):
             wsb = _workspace_bytes(t, batch, xdt, ydt)
             workspace = torch.empty(wsb, dtype=torch.uint8, device=device) if wsb else None
         else:
-            wsb = workspace.numel() * workspace.element_size()
+            wsb = _given(workspace, device)
         rc = _fp8_lib().sketch_fp8_matmul(t._ref, t._at, at, xdt, batch, Y.data_ptr(), ydt,
                                           workspace.data_ptr() if workspace is not None else None, wsb, stream)
     if rc != OK:
@@ -313,7 +334,9 @@ class MoE:
     def workspace_for(self, tokens):
         """Workspace for `tokens` tokens.  Reuse it across calls on one
         stream, never for two calls in flight at once."""
-        return torch.empty(self._workspace_bytes(tokens), dtype=torch.uint8, device=self._device)
+        with _On(self._device):
+            n = self._workspace_bytes(tokens)
+        return torch.empty(n, dtype=torch.uint8, device=self._device)
 
 
 def moe(layer, X, out=None, workspace=None, return_routing=False):
@@ -335,7 +358,7 @@ def moe(layer, X, out=None, workspace=None, return_routing=False):
             wsb = layer._workspace_bytes(T)
             workspace = torch.empty(wsb, dtype=torch.uint8, device=dev)
         else:
-            wsb = workspace.numel() * workspace.element_size()
+            wsb = _given(workspace, dev)
         rc = _fp8_lib().sketch_moe(*layer._fixed, X.data_ptr(), T, Y.data_ptr(), ids.data_ptr(), weights.data_ptr(),
                                    workspace.data_ptr(), wsb, stream)
     if rc != OK:

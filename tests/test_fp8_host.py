@@ -99,6 +99,8 @@ def test_encode_and_matmul_validate_before_launching():
     assert mm(ref(p), vp(256), vp(256), sk.BF16, 4096, vp(256), sk.BF16, vp(256), big - 1, None) == sk.ESMALL
     assert mm(ref(p), vp(256), vp(256), sk.BF16, 4, vp(256), 3, vp(256), 1 << 30, None) == sk.EINVAL
     assert mm(ref(p), vp(256), vp(256), 7, 4, vp(256), sk.F32, vp(256), 1 << 30, None) == sk.EINVAL
+    huge = sk.Fp8Params(1 << 24, 100, 128, 1)        # more tiles than a grid holds: nothing is enqueued
+    assert mm(ref(huge), vp(256), vp(256), sk.BF16, 1 << 24, vp(256), sk.F32, vp(256), (1 << 63) - 1, None) == sk.EINVAL
     assert mm(ref(p), vp(256), vp(256), sk.BF16, 1 << 25, vp(256), sk.F32, vp(256), 1 << 40, None) == sk.EINVAL
 
 

@@ -202,6 +202,36 @@ def test_encoded_rows_give_the_same_bits(b):
     assert torch.equal(Y, sk.fp8_matmul(t, x))                                # and again
 
 
+@pytest.mark.parametrize("M,N,b", [(100, 300, 3), (200, 700, 20), (200, 700, 150), (5000, 300, 2600)])
+def test_non_finite_rows_and_weights_in_16_bits(M, N, b):
+    """NaN in a row of X, or in a block of W, reaches its row (its outputs)
+    and nothing else, on the e4m3 matrix cores too."""
+    w, x = small_ints((M, N), 1, 3), small_ints((b, N), 2, 4)
+    x[1, 5] = float("inf")
+    t = sk.fp8_encode(w.to(dev()))
+    want = torch.from_numpy(u.to64(x) @ u.to64(w).T).to(torch.bfloat16)
+    Y = sk.fp8_matmul(t, x.to(dev()), dtype=torch.bfloat16).cpu()
+    keep = torch.arange(b) != 1
+    assert torch.isnan(Y[1].float()).all() and torch.equal(Y[keep], want[keep])
+    w[M - 1, N - 1], x[1, 5] = float("nan"), 0.0
+    t = sk.fp8_encode(w.to(dev()), check=False)
+    Y = sk.fp8_matmul(t, x.to(dev()), dtype=torch.bfloat16).cpu()
+    first = (M - 1) // 128 * 128
+    want = torch.from_numpy(u.to64(x) @ u.to64(w[:first]).T).to(torch.bfloat16)
+    assert torch.isnan(Y[:, first:].float()).all() and torch.equal(Y[:, :first], want)
+
+
+@pytest.mark.parametrize("b", [1, 9, 40])
+@pytest.mark.parametrize("y", ["f32", "bf16"])
+@pytest.mark.parametrize("scale", [2.0 ** -108, 2.0 ** 100])
+def test_far_scales(b, y, scale):
+    """Weights far from one: sums stay exact (small integers times the scale)."""
+    w, x = small_ints((130, 400), 1, 3), small_ints((b, 400), 2, 4)
+    t = sk.fp8_encode((w * scale).to(dev()))
+    want = torch.from_numpy(u.to64(x) @ u.to64(w).T * scale).to(torch.float32).to(DT[y])
+    assert torch.equal(sk.fp8_matmul(t, x.to(dev()), dtype=DT[y]).cpu(), want)
+
+
 @pytest.mark.parametrize("b", [3, 20, 150])
 def test_zero_rows_blocks_and_non_finite_rows(b):
     """Zero rows and zero blocks give zeros; NaN and infinities stay in their row."""
@@ -225,8 +255,10 @@ def test_tables_from_codes_and_scales():
     r2 = sk.fp8_tables(t.codes().view(torch.uint8), s.view(torch.float8_e8m0fnu))
     assert torch.equal(r.buf, r2.buf) and torch.equal(r.scales(), t.scales())
     assert torch.equal(r.codes().view(torch.uint8), t.codes().view(torch.uint8))
-    with pytest.raises(ValueError):
-        sk.fp8_tables(t.codes(), s[:, :1])
+    for c, e in ((t.codes(), s[:, :1]), (t.codes().view(torch.uint8).view(torch.float8_e5m2), s),
+                 (t.codes(), s.float()), (t.codes().float(), s)):
+        with pytest.raises(ValueError):
+            sk.fp8_tables(c, e)
 
 
 def test_rows_behind_the_output_are_left_alone():
@@ -256,6 +288,10 @@ def test_other_stream_and_refused_outputs():
         sk.fp8_matmul(t, xd, out=torch.empty(5, 256, device=dev(), dtype=torch.float64))
     with pytest.raises(ValueError):
         sk.fp8_matmul(t, x)                               # X on the host
+    with pytest.raises(ValueError):
+        sk.fp8_matmul(t, xd, workspace=torch.empty(1 << 20, dtype=torch.uint8))
+    with pytest.raises(ValueError):
+        sk.fp8_encode(w.to(dev()), check=False, status=torch.zeros(1, dtype=torch.int32))
     assert sk.fp8_matmul(t, xd[:0]).shape == (0, 256)
     assert np.array_equal(u.to64(sk.fp8_matmul(t, xd[2])), u.to64(x)[2] @ u.to64(w).T)
 
