@@ -380,8 +380,8 @@ __global__ __launch_bounds__(kWaves * 64) void moe_up_kernel(MoeArgs a) {
 // row group adding them up was measured: the fences that takes cost 75 us).
 // The three terms of h are 12 loads to a block, so they serve 32 outputs, and
 // come with the weights' 4 loads, not after them.
-constexpr int kDownTiles = 2, kDownRows = 16 * kDownTiles;
-constexpr int kDownRun = 2;   // blocks a wave has in flight
+constexpr int kDownTiles = 4, kDownRows = 16 * kDownTiles;
+constexpr int kDownRun = 1;   // blocks a wave has in flight
 
 __global__ __launch_bounds__(kWaves * 64) void moe_down_kernel(MoeArgs a) {
     extern __shared__ __attribute__((aligned(16))) float ytile[];   // [kWaves][T][kDownRows]
@@ -479,7 +479,7 @@ __global__ __launch_bounds__(256) void moe_add_kernel(MoeArgs a) {
 // Workgroups to a row group of the down kernel: about two per compute unit in
 // all, each with some blocks for every wave to go through (every token has topk experts).
 int down_splits(const sketch_moe_params* p, int64_t kbs) {
-    const int64_t groups = (p->H + kDownRows - 1) / kDownRows, steps = (p->topk * kbs + kWaves - 1) / kWaves;
+    const int64_t groups = (p->H + kDownRows - 1) / kDownRows, steps = (p->topk * kbs + kWaves / 2 - 1) / (kWaves / 2);
     int64_t s = (2 * compute_units() + groups - 1) / groups;
     if (s > steps) s = steps;
     return int(s < 1 ? 1 : s);
