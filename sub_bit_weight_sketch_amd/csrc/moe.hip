@@ -370,18 +370,19 @@ __global__ __launch_bounds__(kWaves * 64) void moe_up_kernel(MoeArgs a) {
     }
 }
 
-// Down and the weighted sum.  A workgroup owns kDownRows outputs and a run of
+// Down and the weighted sum.  A workgroup owns 16 TILES outputs and a run of
 // the active experts' blocks of 128 columns, which its waves take in turns;
 // each wave sums into a tile of its own, the tiles are added in the order of
 // the waves, and the runs in theirs by moe_add_kernel (the last workgroup of a
 // row group adding them up was measured: the fences that takes cost 75 us).
-// The three terms of h are 12 loads to a block, so they serve 32 outputs, and
-// come with the weights' 4 loads, not after them.
-constexpr int kDownTiles = 4, kDownRows = 16 * kDownTiles;
-constexpr int kDownRun = 1;   // blocks a wave has in flight
-
+// The three terms of h are 12 loads to a block, so they serve 64 outputs (2
+// experts of 4096 x 11008 at 1 token: 25 us, 27 us with 32 outputs and two
+// blocks in flight) and come with the weights' loads, not after them; layers
+// too small to fill half the chip that way take 16 (512 x 256: 8.2 -> 5.9 us).
+template <int TILES>
 __global__ __launch_bounds__(kWaves * 64) void moe_down_kernel(MoeArgs a) {
-    extern __shared__ __attribute__((aligned(16))) float ytile[];   // [kWaves][T][kDownRows]
+    constexpr int kRows = 16 * TILES;
+    extern __shared__ __attribute__((aligned(16))) float ytile[];   // [kWaves][T][kRows]
     __shared__ Route rt;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r = lane & 15, c = lane >> 4;
@@ -397,17 +398,17 @@ __global__ __launch_bounds__(kWaves * 64) void moe_down_kernel(MoeArgs a) {
         }
         if (tid == 0) rt.nact = a.route->nact;
     }
-    for (int u = tid; u < kWaves * a.T * kDownRows; u += kWaves * 64) ytile[u] = 0.0f;
+    for (int u = tid; u < kWaves * a.T * kRows; u += kWaves * 64) ytile[u] = 0.0f;
     __syncthreads();
-    float* y = ytile + wave * a.T * kDownRows;
+    float* y = ytile + wave * a.T * kRows;
     const int group = blockIdx.x % a.groups, split = blockIdx.x / a.groups;
-    const int64_t m0 = int64_t(group) * kDownRows;
+    const int64_t m0 = int64_t(group) * kRows;
     const int kbs = int(a.ldi / 128), nact = __builtin_amdgcn_readfirstlane(rt.nact);
     const int u0 = int(int64_t(nact) * kbs * split / a.splits), u1 = int(int64_t(nact) * kbs * (split + 1) / a.splits);
     const int64_t hplane = int64_t(a.T) * a.topk * a.ldi;
-    int64_t roff[kDownTiles];
+    int64_t roff[TILES];
 #pragma unroll
-    for (int i = 0; i < kDownTiles; ++i) roff[i] = min(m0 + 16 * i + r, a.H - 1) * a.ldi + 16 * c;
+    for (int i = 0; i < TILES; ++i) roff[i] = min(m0 + 16 * i + r, a.H - 1) * a.ldi + 16 * c;
     for (int act = u0 / kbs; act * kbs < u1; ++act) {
         const int e = __builtin_amdgcn_readfirstlane(rt.expert[act]), pend = __builtin_amdgcn_readfirstlane(rt.begin[act + 1]);
         const int kend = min(u1 - act * kbs, kbs), kfirst = max(u0 - act * kbs, 0) + wave;
@@ -415,53 +416,43 @@ __global__ __launch_bounds__(kWaves * 64) void moe_down_kernel(MoeArgs a) {
         for (int p0 = __builtin_amdgcn_readfirstlane(rt.begin[act]); p0 < pend; p0 += 16) {
             const int pair = rt.pair[min(p0 + r, pend - 1)];
             const uint16_t* h = a.hs + int64_t(pair) * a.ldi;
-            f32x4 acc[kDownTiles];
+            f32x4 acc[TILES];
 #pragma unroll
-            for (int i = 0; i < kDownTiles; ++i) acc[i] = f32x4{0, 0, 0, 0};
-            for (int k0 = kfirst; k0 < kend; k0 += kDownRun * kWaves) {
-                u32x4 w[kDownRun][kDownTiles][2];
-                bf16x8 hv[kDownRun][3][4];
-                float scale[kDownRun];
+            for (int i = 0; i < TILES; ++i) acc[i] = f32x4{0, 0, 0, 0};
+            for (int kb = kfirst; kb < kend; kb += kWaves) {
+                u32x4 w[TILES][2];
+                bf16x8 hv[3][4];
 #pragma unroll
-                for (int v = 0; v < kDownRun; ++v) {
-                    const int kb = min(k0 + v * kWaves, kend - 1);
+                for (int i = 0; i < TILES; ++i) load_w(D + kb * 128 + roff[i], 0, w[i]);
 #pragma unroll
-                    for (int i = 0; i < kDownTiles; ++i) load_w(D + kb * 128 + roff[i], 0, w[v][i]);
-#pragma unroll
-                    for (int s = 0; s < 3; ++s) load_x(h + s * hplane + kb * 128, c, hv[v][s]);
-                    scale[v] = fp8_scale(ds[kb]);
-                }
+                for (int s = 0; s < 3; ++s) load_x(h + s * hplane + kb * 128, c, hv[s]);
+                const float scale = fp8_scale(ds[kb]);
                 keep_order();
 #pragma unroll
-                for (int v = 0; v < kDownRun; ++v) {
-                    if (k0 + v * kWaves >= kend) break;
+                for (int i = 0; i < TILES; ++i)
 #pragma unroll
-                    for (int i = 0; i < kDownTiles; ++i)
+                    for (int j = 0; j < 4; ++j) {
+                        const bf16x8 wb = fp8_widen(w[i][j >> 1][2 * (j & 1)], w[i][j >> 1][2 * (j & 1) + 1], scale);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const bf16x8 wb = fp8_widen(w[v][i][j >> 1][2 * (j & 1)], w[v][i][j >> 1][2 * (j & 1) + 1], scale[v]);
-#pragma unroll
-                            for (int s = 0; s < 3; ++s)
-                                acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb, hv[v][s][j], acc[i], 0, 0, 0);
-                        }
-                }
+                        for (int s = 0; s < 3; ++s) acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb, hv[s][j], acc[i], 0, 0, 0);
+                    }
             }
             if (p0 + r < pend) {
                 const float w = rt.weight[pair];
-                f32x4* dst = reinterpret_cast<f32x4*>(y + pair / a.topk * kDownRows + 4 * c);
+                f32x4* dst = reinterpret_cast<f32x4*>(y + pair / a.topk * kRows + 4 * c);
 #pragma unroll
-                for (int i = 0; i < kDownTiles; ++i) dst[4 * i] += w * acc[i];
+                for (int i = 0; i < TILES; ++i) dst[4 * i] += w * acc[i];
             }
         }
     }
     __syncthreads();
     float* out = a.splits > 1 ? a.parts + int64_t(split) * a.T * a.H : a.Y;
-    for (int u = tid; u < a.T * kDownRows; u += kWaves * 64) {
-        const int64_t m = m0 + u % kDownRows;
+    for (int u = tid; u < a.T * kRows; u += kWaves * 64) {
+        const int64_t m = m0 + u % kRows;
         float sum = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) sum += ytile[w * a.T * kDownRows + u];
-        if (m < a.H) out[int64_t(u / kDownRows) * a.H + m] = sum;
+        for (int w = 0; w < kWaves; ++w) sum += ytile[w * a.T * kRows + u];
+        if (m < a.H) out[int64_t(u / kRows) * a.H + m] = sum;
     }
 }
 
@@ -473,19 +464,30 @@ __global__ __launch_bounds__(256) void moe_add_kernel(MoeArgs a) {
     a.Y[i] = sum;
 }
 
-// Workgroups to a row group of the down kernel: about two per compute unit in
-// all, each with some blocks for every wave to go through (every token has topk experts).
-int down_splits(const sketch_moe_params* p, int64_t kbs) {
-    const int64_t groups = (p->H + kDownRows - 1) / kDownRows, steps = (p->topk * kbs + kWaves / 2 - 1) / (kWaves / 2);
-    int64_t s = (2 * compute_units() + groups - 1) / groups;
-    if (s > steps) s = steps;
-    return int(s < 1 ? 1 : s);
+// How down is cut: 64 or 16 outputs to a row group, and the workgroups of a row
+// group, about two per compute unit in all, each with some blocks to go through
+// (every token has topk experts).
+struct DownCut {
+    int tiles, groups, splits;
+};
+
+DownCut down_cut(const sketch_moe_params* p, int64_t kbs) {
+    const int64_t ncu = compute_units(), steps = (p->topk * kbs + kWaves / 2 - 1) / (kWaves / 2);
+    DownCut d{};
+    for (int tiles : {4, 1}) {
+        const int64_t rows = 16 * tiles, groups = (p->H + rows - 1) / rows;
+        int64_t s = (2 * ncu + groups - 1) / groups;
+        if (s > steps) s = steps;
+        d = {tiles, int(groups), int(s < 1 ? 1 : s)};
+        if (groups * d.splits >= ncu / 2) break;
+    }
+    return d;
 }
 
 struct MoeLayout {
     sketch_fp8_shape gu, d;
     size_t xs, hs, route, parts, total;
-    int splits, groups;
+    DownCut cut;
 };
 
 sketch_status moe_layout(const sketch_moe_params* p, int64_t tokens, MoeLayout* L) {
@@ -503,9 +505,8 @@ sketch_status moe_layout(const sketch_moe_params* p, int64_t tokens, MoeLayout* 
     L->hs = align256(L->xs + terms * size_t(tokens) * L->gu.ld * 2);
     L->route = align256(L->hs + 3 * size_t(tokens) * p->topk * L->d.ld * 2);
     L->parts = align256(L->route + sizeof(Route));
-    L->splits = down_splits(p, L->d.col_blocks);
-    L->groups = int((p->H + kDownRows - 1) / kDownRows);
-    L->total = align256(L->parts + (L->splits > 1 ? size_t(L->splits) * size_t(tokens) * size_t(p->H) * 4 : 0));
+    L->cut = down_cut(p, L->d.col_blocks);
+    L->total = align256(L->parts + (L->cut.splits > 1 ? size_t(L->cut.splits) * size_t(tokens) * size_t(p->H) * 4 : 0));
     return SKETCH_OK;
 }
 
@@ -552,8 +553,8 @@ sketch_status sketch_moe(const sketch_moe_params* p, const void* router, const v
     a.hs = reinterpret_cast<uint16_t*>(ws + L.hs);
     a.route = reinterpret_cast<Route*>(ws + L.route);
     a.parts = reinterpret_cast<float*>(ws + L.parts);
-    a.splits = L.splits;
-    a.groups = L.groups;
+    a.splits = L.cut.splits;
+    a.groups = L.cut.groups;
     a.H = p->H;
     a.I = p->I;
     a.ldh = L.gu.ld;
@@ -571,7 +572,7 @@ sketch_status sketch_moe(const sketch_moe_params* p, const void* router, const v
     const int64_t ncu = compute_units();
     const int64_t items = (tokens * p->topk < p->E ? tokens * p->topk : int64_t(p->E)) * (L.d.ld / kUpRows);
     const unsigned up_grid = unsigned(items < 2 * ncu ? items : 2 * ncu) + 1;
-    const size_t lds = size_t(kWaves) * tokens * kDownRows * sizeof(float);
+    const size_t lds = size_t(kWaves) * tokens * 16 * L.cut.tiles * sizeof(float);
     const int nt = tokens == 1 ? 1 : 4;   // tokens of a workgroup that sums logits
     auto go = [&](auto one, auto four, auto gate_up, auto gate_up_few, int terms) {
         const size_t xlds = size_t(terms) * tokens * L.gu.ld * 2;
@@ -584,8 +585,12 @@ sketch_status sketch_moe(const sketch_moe_params* p, const void* router, const v
             gate_up<<<up_grid, kWaves * 64, 0, st>>>(a);
         }
         if (hipGetLastError() != hipSuccess) return SKETCH_EDEVICE;
-        moe_down_kernel<<<unsigned(L.groups * L.splits), kWaves * 64, lds, st>>>(a);
-        if (L.splits == 1) return launch_status();
+        const unsigned grid = unsigned(L.cut.groups) * unsigned(L.cut.splits);
+        if (L.cut.tiles == 4)
+            moe_down_kernel<4><<<grid, kWaves * 64, lds, st>>>(a);
+        else
+            moe_down_kernel<1><<<grid, kWaves * 64, lds, st>>>(a);
+        if (L.cut.splits == 1) return launch_status();
         if (hipGetLastError() != hipSuccess) return SKETCH_EDEVICE;
         moe_add_kernel<<<unsigned((tokens * p->H + 255) / 256), 256, 0, st>>>(a);
         return launch_status();

@@ -50,7 +50,8 @@ def check(layer, X, what=""):
                                               (130, 700, 16, 4, 33, True), (1000, 333, 5, 3, 64, False),
                                               (256, 128, 512, 16, 5, True), (300, 64, 3, 1, 64, True),
                                               (2049, 150, 8, 2, 4, False), (500, 200, 32, 3, 1, True),
-                                              (1500, 130, 4, 2, 2, True), (999, 130, 4, 3, 4, False)])
+                                              (1500, 130, 4, 2, 2, True), (999, 130, 4, 3, 4, False),
+                                              (2048, 2000, 8, 4, 5, True), (1030, 4100, 4, 2, 64, True)])
 def test_layer(H, I, E, k, T, renorm, dt):
     layer = make(H, I, E, k, dt, H + I + E, renorm)
     X = torch.randn(T, H, generator=torch.Generator().manual_seed(T)).to(DT[dt]).to(dev())
