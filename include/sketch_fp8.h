@@ -26,7 +26,8 @@
  * blocks rounded up to 4, the rounding's bytes zero.  `count` matrices of one
  * shape (the experts of a layer) lie `bytes` apart.  Codes and scales from
  * elsewhere may be copied into such a buffer; the products read every byte
- * of it, so the padding has to be zero.
+ * of it, so the padding has to be zero.  An element that stands for less than
+ * 2^-126 (float32's least normal number) may count as zero in a product.
  */
 #ifndef SUB_BIT_WEIGHT_SKETCH_FP8_H
 #define SUB_BIT_WEIGHT_SKETCH_FP8_H

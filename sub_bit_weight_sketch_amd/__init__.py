@@ -9,6 +9,8 @@ The C ABI (``include/sketch.h``) has the same names:
 ``sketch_matmul``, ``sketch_matmul_noalloc``, ``sketch_group_bytes``, ``sketch_group_plan``,
 ``sketch_matmul_group``, ``sketch_decode``, ``sketch_decode_hashed``,
 ``sketch_block_importance``, ``sketch_alloc_plan``, ``sketch_status_str``.
+The 8-bit floating-point linears and the mixture-of-experts layer
+(``include/sketch_fp8.h``) are bound in ``fp8.py`` and re-exported here.
 
 High-level use::
 
