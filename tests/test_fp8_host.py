@@ -3,6 +3,7 @@ GPU): exports, buffer layout, and refusals before anything is enqueued."""
 import ctypes
 import os
 import re
+import subprocess
 
 import numpy as np
 import pytest
@@ -22,6 +23,13 @@ def test_library_exports_every_declared_function():
     assert names == set(sk.FP8_EXPORTS)
     for n in names:
         assert hasattr(sk.lib(), n) and callable(getattr(sk, n)), n
+
+
+def test_header_is_plain_c(tmp_path):
+    src = tmp_path / "h.c"
+    src.write_text('#include "%s"\nsketch_fp8_params p; sketch_moe_params q;\nint main(void) { return SKETCH_FP8_ROWS - 3; }\n'
+                   % HEADER)
+    assert subprocess.run(["gcc", "-std=c99", "-Wall", "-Werror", "-fsyntax-only", str(src)]).returncode == 0
 
 
 def test_plain_form_agrees_with_the_formats():

@@ -209,7 +209,8 @@ def test_non_finite_rows_and_weights_in_16_bits(M, N, b):
     w, x = small_ints((M, N), 1, 3), small_ints((b, N), 2, 4)
     x[1, 5] = float("inf")
     t = sk.fp8_encode(w.to(dev()))
-    want = torch.from_numpy(u.to64(x) @ u.to64(w).T).to(torch.bfloat16)
+    with np.errstate(invalid="ignore"):
+        want = torch.from_numpy(u.to64(x) @ u.to64(w).T).to(torch.bfloat16)
     Y = sk.fp8_matmul(t, x.to(dev()), dtype=torch.bfloat16).cpu()
     keep = torch.arange(b) != 1
     assert torch.isnan(Y[1].float()).all() and torch.equal(Y[keep], want[keep])
@@ -294,6 +295,28 @@ def test_other_stream_and_refused_outputs():
         sk.fp8_encode(w.to(dev()), check=False, status=torch.zeros(1, dtype=torch.int32))
     assert sk.fp8_matmul(t, xd[:0]).shape == (0, 256)
     assert np.array_equal(u.to64(sk.fp8_matmul(t, xd[2])), u.to64(x)[2] @ u.to64(w).T)
+
+
+def test_offsets_beyond_32_bits():
+    """A weight of more than 4 GiB of codes: its last block encoded, and read
+    by every kind of product."""
+    M, N = 70016, 65536
+    g = torch.Generator(device=dev()).manual_seed(1)
+    W = torch.zeros((M, N), dtype=torch.bfloat16, device=dev())
+    W[-128:] = torch.randint(-3, 4, (128, N), generator=g, device=dev()).to(torch.bfloat16)
+    W[-128:, ::128] = 3
+    t = sk.fp8_encode(W, check=False)
+    last = W[-128:].clone()
+    del W
+    one = sk.fp8_encode(last)
+    assert torch.equal(t.codes()[-128:].view(torch.uint8), one.codes().view(torch.uint8))
+    assert torch.equal(t.scales()[-1], one.scales()[0]) and not t.codes()[:-128].view(torch.uint8).any()
+    for b, y in ((1, "f32"), (9, "bf16"), (33, "f32"), (200, "bf16")):
+        x = torch.randint(-3, 4, (b, N), generator=g, device=dev()).to(torch.bfloat16)
+        x[:, ::128] = 3
+        want = (x.double() @ last.double().t()).float().to(DT[y])
+        Y = sk.fp8_matmul(t, x, dtype=DT[y])
+        assert torch.equal(Y[:, -128:], want) and not Y[:, :-128].any()
 
 
 @pytest.mark.parametrize("b", [1, 16, 40, 300])

@@ -51,7 +51,8 @@ def check(layer, X, what=""):
                                               (256, 128, 512, 16, 5, True), (300, 64, 3, 1, 64, True),
                                               (2049, 150, 8, 2, 4, False), (500, 200, 32, 3, 1, True),
                                               (1500, 130, 4, 2, 2, True), (999, 130, 4, 3, 4, False),
-                                              (2048, 2000, 8, 4, 5, True), (1030, 4100, 4, 2, 64, True)])
+                                              (2048, 2000, 8, 4, 5, True), (1030, 4100, 4, 2, 64, True),
+                                              (48, 40, 512, 16, 64, False)])
 def test_layer(H, I, E, k, T, renorm, dt):
     layer = make(H, I, E, k, dt, H + I + E, renorm)
     X = torch.randn(T, H, generator=torch.Generator().manual_seed(T)).to(DT[dt]).to(dev())
@@ -168,6 +169,34 @@ def test_captured_and_replayed(T):
             torch.cuda.synchronize()
             assert torch.equal(Y, ref[i])
             assert torch.equal(sk.moe(layer, Xs[i]), ref[i])
+
+
+def test_experts_beyond_32_bits():
+    """The last of 64 experts of 67 MB lies beyond 4 GiB; all others are zero."""
+    H = I = 8192
+    E = 64
+    g = torch.Generator(device=dev()).manual_seed(2)
+    stacks, last = [], []
+    for _ in range(3):
+        w = torch.randn((8192, 8192), generator=g, device=dev()) / 90
+        one = sk.fp8_encode(w)
+        t = sk.Fp8Tables(8192, 8192, 128, E, dev())
+        t.buf.zero_()
+        t.buf[-one.layout.bytes:] = one.buf
+        stacks.append(t)
+        last.append(one)
+    router = torch.zeros((E, H), device=dev())
+    router[-1] = 1.0
+    X = torch.rand((3, H), generator=g, device=dev())
+    Y, ids, w = sk.moe(sk.MoE(router, *stacks, 2), X, return_routing=True)
+    assert (ids[:, 0] == E - 1).all() and (ids[:, 1] == 0).all()
+    val = [t.codes().double() * torch.exp2(t.scales().double() - 127).repeat_interleave(128, 0).repeat_interleave(128, 1)
+           for t in last]
+    gv, uv = X.double() @ val[0].t(), X.double() @ val[1].t()
+    want = w[:, :1].double() * ((gv * torch.sigmoid(gv) * uv) @ val[2].t())
+    # as in check(): the walks of two float32 sums, on the size of a row
+    size = want.square().mean(1, keepdim=True).sqrt()
+    assert ((Y - want).abs() / size).max() <= (6 * np.sqrt(H + I) + 16) * u.EPS32
 
 
 def test_refusals():
