@@ -13,6 +13,8 @@
 //
 // Three launches: the logits and the split of x; gate and up; down and the
 // weighted sum; and a fourth that adds the parts where down is split.
+#include <type_traits>
+
 #include "fp8.h"
 
 namespace sketch {
@@ -48,6 +50,15 @@ struct MoeArgs {
     int32_t T, E, topk, renorm;
     int32_t splits, groups;   // of the down kernel
 };
+
+// An expert with few tokens has their NS terms in a tile's 16 columns, column
+// NS t + s the term s of token t: one load and one matrix instruction for the
+// terms of 16 / NS tokens, whose sums are added at the end.  With more tokens
+// the terms follow one another.  (Down of 2 experts of 4096 x 11008 at 1 token:
+// 25 -> 20 us; gate and up of 64 of 2048 x 1408 in binary16, 7 tokens: 39 ->
+// 36 us.  Two tiles of columns at once for up to 10 tokens took more registers
+// than two workgroups to a CU leave and lost: 20 -> 23 us.)
+template <int NS> constexpr int kTokensOf = 16 / NS;
 
 template <int DT> constexpr int x_terms() { return DT == SKETCH_BF16 ? 1 : DT == SKETCH_F16 ? 2 : 3; }
 
@@ -246,7 +257,7 @@ __device__ inline void keep_order() { asm volatile("" ::: "memory"); }
 //
 // FEW (few tokens, a small router): every workgroup sums the logits for itself
 // and splits x into LDS, instead of the launch before this one (1 token, 8
-// experts of 512 x 256: 2.6 + 6.4 us in two launches, 7.0 us in one; with a
+// experts of 512 x 256: 2.6 + 6.6 us in two launches, 7.9 us in one; with a
 // router of 8 x 4096 4.7 + 43.5 us against 50.2 us, no gain any more).
 constexpr int kUpTiles = 2, kUpRows = 16 * kUpTiles;
 constexpr int kFewTokens = 4, kFewLogits = 4 * kWaves;
@@ -305,28 +316,31 @@ __global__ __launch_bounds__(kWaves * 64) void moe_up_kernel(MoeArgs a) {
     const int64_t hplane = int64_t(a.T) * a.topk * a.ldi;
     for (int it = blockIdx.x; it < items; it += gridDim.x - 1) {
         const int act = it / tiles, m0 = it % tiles * kUpRows, e = __builtin_amdgcn_readfirstlane(rt.expert[act]);
-        const int pend = __builtin_amdgcn_readfirstlane(rt.begin[act + 1]);
+        const int begin = __builtin_amdgcn_readfirstlane(rt.begin[act]), pend = __builtin_amdgcn_readfirstlane(rt.begin[act + 1]);
         const uint8_t *G = a.gate + e * a.gu_bytes, *U = a.up + e * a.gu_bytes;
         int64_t roff[kUpTiles];
 #pragma unroll
         for (int i = 0; i < kUpTiles; ++i) roff[i] = min(int64_t(m0 + 16 * i + r), a.I - 1) * a.ldh;
         const int64_t srow = min(int64_t(m0), a.I - 1) / 128 * a.gu_lds;   // kUpRows rows lie in one block of 128
         const uint8_t *gs = G + a.gu_scales + srow, *us = U + a.gu_scales + srow;
-        for (int p0 = __builtin_amdgcn_readfirstlane(rt.begin[act]); p0 < pend; p0 += 16) {
-            const uint16_t* x = (FEW ? xlds : a.xs) + int64_t(rt.pair[min(p0 + r, pend - 1)] / a.topk) * a.ldh;
+        auto tokens = [&](auto in_columns, int first) {
+            constexpr bool COLUMNS = decltype(in_columns)::value;
+            constexpr int SEQ = COLUMNS ? 1 : NS, COL = COLUMNS ? NS : 1;   // terms one after the other, in columns
+            const uint16_t* x = (FEW ? xlds : a.xs) + int64_t(rt.pair[min(first + r / COL, pend - 1)] / a.topk) * a.ldh +
+                                r % COL * plane;
             f32x4 ga[kUpTiles], ua[kUpTiles];
 #pragma unroll
             for (int i = 0; i < kUpTiles; ++i) ga[i] = ua[i] = f32x4{0, 0, 0, 0};
             for (int kb = wave; kb < kbs; kb += kWaves) {
                 u32x4 gw[kUpTiles][2], uw[kUpTiles][2];
-                bf16x8 xv[NS][4];
+                bf16x8 xv[SEQ][4];
 #pragma unroll
                 for (int i = 0; i < kUpTiles; ++i) {
                     load_w(G + roff[i] + kb * 128, c, gw[i]);
                     load_w(U + roff[i] + kb * 128, c, uw[i]);
                 }
 #pragma unroll
-                for (int s = 0; s < NS; ++s) load_x(x + s * plane + kb * 128, c, xv[s]);
+                for (int s = 0; s < SEQ; ++s) load_x(x + s * plane + kb * 128, c, xv[s]);
                 const float gsc = fp8_scale(gs[kb]), usc = fp8_scale(us[kb]);
                 keep_order();
 #pragma unroll
@@ -336,7 +350,7 @@ __global__ __launch_bounds__(kWaves * 64) void moe_up_kernel(MoeArgs a) {
                         const bf16x8 gb = fp8_widen(gw[i][j >> 1][2 * (j & 1)], gw[i][j >> 1][2 * (j & 1) + 1], gsc);
                         const bf16x8 ub = fp8_widen(uw[i][j >> 1][2 * (j & 1)], uw[i][j >> 1][2 * (j & 1) + 1], usc);
 #pragma unroll
-                        for (int s = 0; s < NS; ++s) {
+                        for (int s = 0; s < SEQ; ++s) {
                             ga[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(gb, xv[s][j], ga[i], 0, 0, 0);
                             ua[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ub, xv[s][j], ua[i], 0, 0, 0);
                         }
@@ -350,22 +364,31 @@ __global__ __launch_bounds__(kWaves * 64) void moe_up_kernel(MoeArgs a) {
                     part[wave][1][r][16 * i + 4 * c + v] = ua[i][v];
                 }
             __syncthreads();
-            for (int u = tid; u < 16 * kUpRows; u += kWaves * 64) {
+            for (int u = tid; u < 16 / COL * kUpRows; u += kWaves * 64) {
                 const int tok = u / kUpRows, row = u % kUpRows;
+                if (first + tok >= pend) break;
                 float gv = 0.0f, uv = 0.0f;
 #pragma unroll
-                for (int w = 0; w < kWaves; ++w) {
-                    gv += part[w][0][tok][row];
-                    uv += part[w][1][tok][row];
-                }
-                float h = m0 + row < a.I ? gv / (1.0f + expf(-gv)) * uv : 0.0f;
-                if (p0 + tok < pend) {
-                    uint16_t* dst = a.hs + int64_t(rt.pair[p0 + tok]) * a.ldi + m0 + row;
+                for (int s = 0; s < COL; ++s)
 #pragma unroll
-                    for (int s = 0; s < 3; ++s) dst[s * hplane] = take_bf16(h);
-                }
+                    for (int w = 0; w < kWaves; ++w) {
+                        gv += part[w][0][tok * COL + s][row];
+                        uv += part[w][1][tok * COL + s][row];
+                    }
+                float h = m0 + row < a.I ? gv / (1.0f + expf(-gv)) * uv : 0.0f;
+                uint16_t* dst = a.hs + int64_t(rt.pair[first + tok]) * a.ldi + m0 + row;
+#pragma unroll
+                for (int s = 0; s < 3; ++s) dst[s * hplane] = take_bf16(h);
             }
             __syncthreads();
+        };
+        if constexpr (FEW) {
+            static_assert(kFewTokens <= kTokensOf<NS>, "one tile of columns");
+            tokens(std::true_type{}, begin);
+        } else if (NS > 1 && pend - begin <= kTokensOf<NS>) {
+            tokens(std::true_type{}, begin);
+        } else {
+            for (int p0 = begin; p0 < pend; p0 += 16) tokens(std::false_type{}, p0);
         }
     }
 }
@@ -375,10 +398,10 @@ __global__ __launch_bounds__(kWaves * 64) void moe_up_kernel(MoeArgs a) {
 // each wave sums into a tile of its own, the tiles are added in the order of
 // the waves, and the runs in theirs by moe_add_kernel (the last workgroup of a
 // row group adding them up was measured: the fences that takes cost 75 us).
-// The three terms of h are 12 loads to a block, so they serve 64 outputs (2
-// experts of 4096 x 11008 at 1 token: 25 us, 27 us with 32 outputs and two
-// blocks in flight) and come with the weights' loads, not after them; layers
-// too small to fill half the chip that way take 16 (512 x 256: 8.2 -> 5.9 us).
+// The loads of h, 4 or 12 to a block, serve 64 outputs (2 experts of 4096 x
+// 11008 at 1 token: 20 us, 21 us with 32; 8 with 16 tokens 89 us and 100 us)
+// and come with the weights' loads, not after them; layers too small to fill
+// half the chip that way take 16 (512 x 256: 8.2 -> 5.9 us).
 template <int TILES>
 __global__ __launch_bounds__(kWaves * 64) void moe_down_kernel(MoeArgs a) {
     constexpr int kRows = 16 * TILES;
@@ -409,41 +432,56 @@ __global__ __launch_bounds__(kWaves * 64) void moe_down_kernel(MoeArgs a) {
     int64_t roff[TILES];
 #pragma unroll
     for (int i = 0; i < TILES; ++i) roff[i] = min(m0 + 16 * i + r, a.H - 1) * a.ldi + 16 * c;
-    for (int act = u0 / kbs; act * kbs < u1; ++act) {
-        const int e = __builtin_amdgcn_readfirstlane(rt.expert[act]), pend = __builtin_amdgcn_readfirstlane(rt.begin[act + 1]);
+    // Tokens first .. pend - 1 of one expert, up to 5 with their terms in columns
+    // of their own, or up to 16 with one term after the other.
+    auto expert = [&](auto in_columns, int act, int first, int pend) {
+        constexpr bool COLUMNS = decltype(in_columns)::value;
+        constexpr int NS = COLUMNS ? 1 : 3;
+        const int e = __builtin_amdgcn_readfirstlane(rt.expert[act]);
         const int kend = min(u1 - act * kbs, kbs), kfirst = max(u0 - act * kbs, 0) + wave;
         const uint8_t *D = a.down + e * a.d_bytes, *ds = D + a.d_scales + m0 / 128 * a.d_lds;
-        for (int p0 = __builtin_amdgcn_readfirstlane(rt.begin[act]); p0 < pend; p0 += 16) {
-            const int pair = rt.pair[min(p0 + r, pend - 1)];
-            const uint16_t* h = a.hs + int64_t(pair) * a.ldi;
-            f32x4 acc[TILES];
+        const int tok = first + (COLUMNS ? r / 3 : r), pair = rt.pair[min(tok, pend - 1)];
+        const uint16_t* h = a.hs + int64_t(pair) * a.ldi + (COLUMNS ? r % 3 * hplane : 0);
+        f32x4 acc[TILES];
 #pragma unroll
-            for (int i = 0; i < TILES; ++i) acc[i] = f32x4{0, 0, 0, 0};
-            for (int kb = kfirst; kb < kend; kb += kWaves) {
-                u32x4 w[TILES][2];
-                bf16x8 hv[3][4];
+        for (int i = 0; i < TILES; ++i) acc[i] = f32x4{0, 0, 0, 0};
+        for (int kb = kfirst; kb < kend; kb += kWaves) {
+            u32x4 w[TILES][2];
+            bf16x8 hv[NS][4];
 #pragma unroll
-                for (int i = 0; i < TILES; ++i) load_w(D + kb * 128 + roff[i], 0, w[i]);
+            for (int i = 0; i < TILES; ++i) load_w(D + kb * 128 + roff[i], 0, w[i]);
 #pragma unroll
-                for (int s = 0; s < 3; ++s) load_x(h + s * hplane + kb * 128, c, hv[s]);
-                const float scale = fp8_scale(ds[kb]);
-                keep_order();
+            for (int s = 0; s < NS; ++s) load_x(h + s * hplane + kb * 128, c, hv[s]);
+            const float scale = fp8_scale(ds[kb]);
+            keep_order();
 #pragma unroll
-                for (int i = 0; i < TILES; ++i)
+            for (int i = 0; i < TILES; ++i)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const bf16x8 wb = fp8_widen(w[i][j >> 1][2 * (j & 1)], w[i][j >> 1][2 * (j & 1) + 1], scale);
+                for (int j = 0; j < 4; ++j) {
+                    const bf16x8 wb = fp8_widen(w[i][j >> 1][2 * (j & 1)], w[i][j >> 1][2 * (j & 1) + 1], scale);
 #pragma unroll
-                        for (int s = 0; s < 3; ++s) acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb, hv[s][j], acc[i], 0, 0, 0);
-                    }
-            }
-            if (p0 + r < pend) {
-                const float w = rt.weight[pair];
-                f32x4* dst = reinterpret_cast<f32x4*>(y + pair / a.topk * kRows + 4 * c);
-#pragma unroll
-                for (int i = 0; i < TILES; ++i) dst[4 * i] += w * acc[i];
-            }
+                    for (int s = 0; s < NS; ++s) acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb, hv[s][j], acc[i], 0, 0, 0);
+                }
         }
+        if constexpr (COLUMNS) {
+#pragma unroll
+            for (int i = 0; i < TILES; ++i)
+#pragma unroll
+                for (int v = 0; v < 4; ++v) acc[i][v] = (acc[i][v] + __shfl_down(acc[i][v], 1)) + __shfl_down(acc[i][v], 2);
+        }
+        if (tok < pend && (!COLUMNS || r % 3 == 0)) {
+            const float w = rt.weight[pair];
+            f32x4* dst = reinterpret_cast<f32x4*>(y + pair / a.topk * kRows + 4 * c);
+#pragma unroll
+            for (int i = 0; i < TILES; ++i) dst[4 * i] += w * acc[i];
+        }
+    };
+    for (int act = u0 / kbs; act * kbs < u1; ++act) {
+        const int begin = __builtin_amdgcn_readfirstlane(rt.begin[act]), pend = __builtin_amdgcn_readfirstlane(rt.begin[act + 1]);
+        if (pend - begin <= kTokensOf<3>)
+            expert(std::true_type{}, act, begin, pend);
+        else
+            for (int p0 = begin; p0 < pend; p0 += 16) expert(std::false_type{}, act, p0, pend);
     }
     __syncthreads();
     float* out = a.splits > 1 ? a.parts + int64_t(split) * a.T * a.H : a.Y;

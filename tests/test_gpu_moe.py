@@ -69,6 +69,24 @@ def test_all_tokens_at_one_expert(T):
     check(layer, X)
 
 
+@pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("T", [4, 5, 6, 7, 8, 9, 15, 17])
+def test_few_tokens_at_an_expert(T, dt):
+    """One expert with all tokens, others with the even or the odd ones, about
+    the numbers at which activations of several terms change their layout."""
+    H, I = 300, 150
+    layer = make(H, I, 8, 2, dt, 14)
+    X = torch.randn(T, H, generator=torch.Generator().manual_seed(T))
+    layer.router[:, :2] = 0
+    layer.router[5, 0], layer.router[1, 1], layer.router[6, 1] = 40.0, 30.0, -30.0
+    X[:, 0] = 1.0
+    X[:, 1] = 1.0 - 2.0 * (torch.arange(T) % 2)
+    X = X.to(DT[dt]).to(dev())
+    ids = sk.moe(layer, X, return_routing=True)[1].cpu()
+    assert (ids[:, 0] == 5).all() and (ids[::2, 1] == 1).all() and (ids[1::2, 1] == 6).all()
+    check(layer, X)
+
+
 def test_each_index_path():
     """Gate, up and down pick single entries, so that every output is one known
     term: y[t][i] = sum_e w_e silu(x[a]) x[b], with a, b known from (e, i).
@@ -125,6 +143,49 @@ def test_non_finite_tokens_stay_in_their_row(bad, dt):
     assert not torch.isfinite(Yz[2]).any()
     assert torch.isfinite(Yz[keep]).all() and (Yz[keep] - Y[keep]).abs().max() <= 1e-5 * Y.abs().max()
     assert ((ids >= 0) & (ids < 8)).all() and int(ids[2, 0]) != int(ids[2, 1])
+
+
+@pytest.mark.parametrize("code", [0.0, 1.0])
+def test_a_nan_scale_in_an_expert(code):
+    """The scale byte 255 in one block of an expert's down weight, of its gate
+    or up weight: NaN for the tokens that chose it (the outputs of the block,
+    or all of them), and for nobody else."""
+    H, I, E, T = 300, 200, 4, 20
+    g = torch.Generator().manual_seed(12)
+    router = torch.randn(E, H, generator=g).to(dev())
+    X = torch.randn(T, H, generator=g).to(dev())
+    for which in range(3):
+        w = [torch.randn(*s, generator=g) for s in ((E, I, H), (E, I, H), (E, H, I))]
+        ref = sk.moe(sk.MoE(router, *(sk.fp8_encode(v.to(dev())) for v in w), 1), X)
+        w[which][1, 128:256, 128:256] = code
+        t = [sk.fp8_encode(v.to(dev())) for v in w]
+        t[which].scales()[1, 1, 1] = 255
+        Y, ids, _ = sk.moe(sk.MoE(router, *t, 1), X, return_routing=True)
+        hit = ids[:, 0] == 1
+        assert 0 < int(hit.sum()) < T
+        cols = slice(128, 256) if which == 2 else slice(None)
+        assert torch.isnan(Y[hit][:, cols]).all() and torch.equal(Y[~hit], ref[~hit])
+        if which == 2:
+            assert torch.equal(Y[hit][:, :128], ref[hit][:, :128]) and torch.equal(Y[hit][:, 256:], ref[hit][:, 256:])
+
+
+@pytest.mark.parametrize("byte,scale", [(0, 2.0 ** -127), (247, 2.0 ** 120)])
+def test_far_scales_in_an_expert(byte, scale):
+    """Gate and up as ordinary, down at the ends of the scales: the result of
+    ones there, scaled by a power of two (the sums are the same, unless they
+    leave float32's normal range: h is made large, or small, enough)."""
+    H, I, E, T = 256, 128, 2, 5
+    g = torch.Generator().manual_seed(13)
+    router = torch.randn(E, H, generator=g).to(dev())
+    X = torch.randn(T, H, generator=g).to(dev())
+    gate = sk.fp8_encode((torch.randn(E, I, H, generator=g) / 16).to(dev()))
+    lift = 2.0 ** 60 if scale < 1 else 2.0 ** -60
+    up = sk.fp8_encode((torch.randn(E, I, H, generator=g) * lift).to(dev()))
+    codes = (torch.randint(1, 8, (E, H, I), generator=g) * 2).float().to(dev()).to(torch.float8_e4m3fn)
+    s = torch.full((E, 2, 1), 127, dtype=torch.uint8, device=dev())
+    one = sk.moe(sk.MoE(router, gate, up, sk.fp8_tables(codes, s), 1), X)
+    far = sk.moe(sk.MoE(router, gate, up, sk.fp8_tables(codes, torch.full_like(s, byte)), 1), X)
+    assert torch.equal(far.double(), one.double() * scale)
 
 
 def test_repeats_are_identical_and_streams_do_not_mix():
