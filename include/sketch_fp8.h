@@ -25,9 +25,11 @@
  * zero; at byte scales_offset, scale bytes [row blocks][lds], lds = column
  * blocks rounded up to 4, the rounding's bytes zero.  `count` matrices of one
  * shape (the experts of a layer) lie `bytes` apart.  Codes and scales from
- * elsewhere may be copied into such a buffer; the products read every byte
- * of it, so the padding has to be zero.  An element that stands for less than
- * 2^-126 (float32's least normal number) may count as zero in a product.
+ * elsewhere may be copied into such a buffer; the products read the padding of
+ * rows, so it has to be zero.  An element that stands for less than 2^-126
+ * (float32's least normal number) may count as zero in a product, one of 2^128
+ * or more as infinite.  The scale byte 255 makes its whole block NaN, whatever
+ * the codes.
  */
 #ifndef SUB_BIT_WEIGHT_SKETCH_FP8_H
 #define SUB_BIT_WEIGHT_SKETCH_FP8_H
@@ -71,8 +73,8 @@ sketch_status sketch_fp8_layout(const sketch_fp8_params* p, sketch_fp8_shape* sh
 
 /*
  * sketch_fp8_encode -- W [count][M][N] of w_dtype (float32, bfloat16 or
- * binary16, dense) into `buf` (count * bytes of sketch_fp8_layout, every byte
- * up to the last scale written).
+ * binary16, dense) into `buf` (count * bytes of sketch_fp8_layout; every code
+ * and scale byte is written, with the padding of their rows).
  *   status_dev  one device int32 that the kernel ORs SKETCH_FLAG_WEIGHT_RANGE
  *               into when some element is NaN or infinite, or NULL.
  */

@@ -57,7 +57,8 @@ __device__ inline uint32_t fp8_pack4(float a, float b, float c, float d) {
     return uint32_t(v);
 }
 
-// 2^(byte - 127); 255, the NaN scale, gives infinity, and its codes are NaN.
+// The byte as the exponent of a float32, the form in which the widening takes a
+// scale: it reads that field alone, 0 as 2^-127 and 255 as NaN.
 __device__ inline float fp8_scale(uint32_t byte) { return __uint_as_float(byte << 23); }
 
 // 8 codes (two dwords) -> 8 bfloat16 values times a power of two (exact).

@@ -116,6 +116,8 @@ class _On:
         self.index, self.other = device.index, None
 
     def __enter__(self):
+        if self.index is None:
+            raise ValueError("tensors must be on a GPU")
         if torch.cuda.current_device() != self.index:
             self.other = torch.cuda.device(self.index)
             self.other.__enter__()
@@ -161,8 +163,13 @@ class Fp8Tables:
         else:
             _need(buf.dtype == torch.uint8 and buf.is_contiguous() and buf.numel() >= n and buf.data_ptr() % 16 == 0,
                   "the buffer must be %d dense, 16-byte aligned bytes" % n)
-        self.buf, self.device, self._at = buf, buf.device, buf.data_ptr()
+        self._buf, self.device, self._at = buf, buf.device, buf.data_ptr()
         self._ws = {}
+
+    @property
+    def buf(self):
+        """The buffer; its bytes may be changed, not the buffer."""
+        return self._buf
 
     @property
     def shape(self):
@@ -190,8 +197,8 @@ def fp8_encode(W, block_rows=128, check=True, status=None):
 
     With check=True the call waits for the device and raises SketchError when
     an element is NaN or infinite; with check=False it stays asynchronous (such
-    a block encodes to NaN) and ORs flags into `status`, an int32 device tensor
-    of one element, when given."""
+    a block encodes to NaN) and ORs flags into `status`, a zeroed int32 device
+    tensor of one element, when given."""
     if W.dim() not in (2, 3) or not W.is_cuda:
         raise ValueError("W must be a 2-D GPU tensor, or a 3-D one for a stack of matrices")
     if status is not None:
@@ -306,7 +313,9 @@ class MoE:
     """A mixture-of-experts layer: router [E, H] (float32, bfloat16 or
     float16, the dtype its tokens have) and the experts' weights, stacks of E
     encoded matrices: gate and up [E, I, H], down [E, H, I].  renorm: whether
-    the weights of the chosen experts are scaled to sum to one."""
+    the weights of the chosen experts are scaled to sum to one.  The layer
+    reads these tensors' values at each call (a copy of a router that is not
+    dense and 16-byte aligned: layer.router)."""
 
     def __init__(self, router, gate, up, down, topk, renorm=True):
         _need(router.dim() == 2 and router.is_cuda, "router must be a 2-D GPU tensor")
@@ -317,13 +326,21 @@ class MoE:
         I = gate.M
         _need(gate.shape == up.shape == (E, I, H) and down.shape == (E, H, I),
               "gate and up must be [E, I, H], down [E, H, I], the router [E, H]")
-        self.router, self.gate, self.up, self.down = _aligned(router), gate, up, down
-        self.topk, self.renorm = int(topk), bool(renorm)
-        self.params = MoEParams(H, I, E, self.topk, int(self.renorm), dtype_code(router))
+        self._tensors = _aligned(router), gate, up, down
+        self._topk, self._renorm = int(topk), bool(renorm)
+        self.params = MoEParams(H, I, E, self._topk, int(self._renorm), dtype_code(router))
         self._fixed = (ctypes.byref(self.params), self.router.data_ptr(), gate._at, up._at, down._at)
         self._H, self._dtype, self._device = H, router.dtype, router.device
         sketch_moe_workspace_bytes(self.params, 0)   # checks the sizes
         self._ws = {}
+
+    # a layer's values may be changed in place, its tensors and sizes not
+    router = property(lambda self: self._tensors[0])
+    gate = property(lambda self: self._tensors[1])
+    up = property(lambda self: self._tensors[2])
+    down = property(lambda self: self._tensors[3])
+    topk = property(lambda self: self._topk)
+    renorm = property(lambda self: self._renorm)
 
     def _workspace_bytes(self, tokens):
         n = self._ws.get(tokens)
@@ -344,7 +361,7 @@ def moe(layer, X, out=None, workspace=None, return_routing=False):
     MOE_MAX_TOKENS tokens, of the router's dtype); with return_routing also
     the chosen experts int32 [tokens, topk], by descending logit, and their
     weights float32 [tokens, topk]."""
-    shape, dev, k = X.shape, layer._device, layer.topk
+    shape, dev, k = X.shape, layer._device, layer._topk
     if len(shape) != 2 or shape[1] != layer._H:
         raise ValueError("X must be [tokens, %d]" % layer._H)
     if X.dtype != layer._dtype or X.device != dev:

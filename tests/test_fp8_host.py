@@ -151,7 +151,23 @@ def test_python_refusals():
     with pytest.raises(TypeError):
         sk.fp8_matmul(t, torch.zeros(2, 200, dtype=torch.float64))
     with pytest.raises(ValueError):
+        sk.fp8_matmul(t, torch.zeros(2, 200))            # both on the host
+    with pytest.raises(ValueError):
+        sk.fp8_matmul(t, sk.Fp8Tables(2, 200, 1, None, "cpu"))
+    with pytest.raises(ValueError):
+        sk.fp8_workspace_for(t, 4, sk.F32, sk.F32, "cpu")
+    with pytest.raises(ValueError):
         sk.MoE(torch.zeros(8, 64), None, None, None, 2)
+
+
+def test_a_buffer_stays_its_own():
+    """Replacing a buffer would leave the calls with the old one: refused."""
+    t = sk.Fp8Tables(4, 200, 128, None, "cpu")
+    with pytest.raises(AttributeError):
+        t.buf = t.buf.clone()
+    for name in ("router", "gate", "up", "down", "topk", "renorm"):
+        with pytest.raises(AttributeError):
+            setattr(sk.MoE.__new__(sk.MoE), name, None)
 
 
 def test_views_of_a_buffer():

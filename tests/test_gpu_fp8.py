@@ -233,6 +233,49 @@ def test_far_scales(b, y, scale):
     assert torch.equal(sk.fp8_matmul(t, x.to(dev()), dtype=DT[y]).cpu(), want)
 
 
+@pytest.mark.parametrize("M,b,y", [(130, 1, "f32"), (130, 1, "bf16"), (130, 9, "f32"), (130, 9, "bf16"), (130, 40, "f32"),
+                                   (130, 200, "bf16"), (5000, 2600, "bf16")])
+@pytest.mark.parametrize("byte,other", [(0, 217), (1, 187), (9, 150), (247, 60), (254, 50)])
+def test_scale_bytes_at_their_ends(M, b, y, byte, other):
+    """Tables from elsewhere with scales up to the ends of their range, on the
+    weight and on the rows: even integers, so that at 2^-127 every element is
+    at least 2^-126, and at 2^127 only ones; sums stay exact."""
+    N = 300
+    w, x = small_ints((M, N), 1, 3), small_ints((b, N), 2, 3)
+    w, x = (w.clamp(-1, 1), x.clamp(-1, 1)) if byte == 254 else (w * 2, x * 2)
+    codes = lambda a: a.to(dev()).to(torch.float8_e4m3fn)
+    full = lambda rows, e: torch.full((rows, 3), e, dtype=torch.uint8, device=dev())
+    for we, xe in ((byte, other), (other, byte)):
+        t = sk.fp8_tables(codes(w), full(u.blocks(M, 128), we))
+        r = sk.fp8_tables(codes(x), full(b, xe), block_rows=1)
+        want = torch.from_numpy(u.to64(x) @ u.to64(w).T * 2.0 ** (we + xe - 254)).to(torch.float32).to(DT[y])
+        assert torch.equal(sk.fp8_matmul(t, r, dtype=DT[y]).cpu(), want), (we, xe)
+
+
+@pytest.mark.parametrize("M,b,y", [(300, 1, "f32"), (300, 3, "bf16"), (300, 9, "f32"), (300, 40, "f32"),
+                                   (300, 200, "bf16"), (5000, 2600, "bf16")])
+@pytest.mark.parametrize("code", [0.0, 1.0, -448.0])
+def test_a_nan_scale_is_nan_whatever_its_codes(M, b, y, code):
+    """The scale byte 255 over ordinary codes, zeros among them, in a block of
+    the weight and in a row's block: NaN for its outputs, its row, no others."""
+    N = 300
+    w, x = small_ints((M, N), 1, 3), small_ints((b, N), 2, 3)
+    w[128:256, 256:] = code
+    t, r = sk.fp8_encode(w.to(dev())), sk.fp8_encode(x.to(dev()), block_rows=1)
+    t.scales()[1, 2] = 255
+    Y = sk.fp8_matmul(t, r, dtype=DT[y]).cpu()
+    keep = torch.ones(M, dtype=torch.bool)
+    keep[128:256] = False
+    want = torch.from_numpy(u.to64(x) @ u.to64(w).T).to(torch.float32).to(DT[y])
+    assert torch.isnan(Y[:, ~keep]).all() and torch.equal(Y[:, keep], want[:, keep])
+    x[b // 2, 128:256] = code
+    r = sk.fp8_encode(x.to(dev()), block_rows=1)
+    r.scales()[b // 2, 1] = 255
+    Y = sk.fp8_matmul(t, r, dtype=DT[y]).cpu()
+    rows = torch.arange(b) != b // 2
+    assert torch.isnan(Y[b // 2]).all() and torch.equal(Y[rows][:, keep], want[rows][:, keep])
+
+
 @pytest.mark.parametrize("b", [3, 20, 150])
 def test_zero_rows_blocks_and_non_finite_rows(b):
     """Zero rows and zero blocks give zeros; NaN and infinities stay in their row."""
