@@ -316,8 +316,12 @@ sketch_status launch_few(const Fp8Product& p, int x_dtype, int64_t N, hipStream_
         return p.T == 1 ? tokens(fp8_tokens_kernel<SKETCH_BF16, EXACT, 1>) : tokens(fp8_tokens_kernel<SKETCH_BF16, EXACT, 4>);
     if (x_dtype == SKETCH_F16)
         return p.T == 1 ? tokens(fp8_tokens_kernel<SKETCH_F16, EXACT, 1>) : tokens(fp8_tokens_kernel<SKETCH_F16, EXACT, 4>);
-    // 32 outputs to a workgroup halve the reads of X; with few workgroups 16 fill the chip better
-    return p.M >= 64 * int64_t(compute_units()) ? rows(fp8_rows_kernel<2, EXACT>, 32) : rows(fp8_rows_kernel<1, EXACT>, 16);
+    // 32 outputs to a workgroup halve the reads of X (16 rows, 5000 x 28672: 61 us with 16 outputs, 48 us with 32;
+    // 8192 x 28672 68 and 57); where those of 16 all have a compute unit to themselves (4096 x 28672: 38 and 48), or a
+    // wave has but one run (11008 x 4096: 17.7 and 18.7), 16 have the shorter way
+    const int64_t ncu = compute_units();
+    const bool two = p.M >= 64 * ncu || (p.M > 16 * ncu && p.kb > kWaves * kRun);
+    return two ? rows(fp8_rows_kernel<2, EXACT>, 32) : rows(fp8_rows_kernel<1, EXACT>, 16);
 }
 
 bool valid_dtype(int d) { return d == SKETCH_F32 || d == SKETCH_BF16 || d == SKETCH_F16; }

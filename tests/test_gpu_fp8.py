@@ -146,7 +146,8 @@ def test_product_exact(M, N, b):
 
 @pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("M,N,b", [(300, 4001, 1), (300, 4001, 9), (2050, 640, 40), (700, 900, 300), (4096, 11008, 3),
-                                   (384, 300, 2000), (130, 11008, 140), (2100, 2500, 1300)])
+                                   (384, 300, 2000), (130, 11008, 140), (2100, 2500, 1300),
+                                   (4333, 4300, 13), (16400, 200, 16)])
 def test_product_exact_larger(M, N, b, dt):
     w, x = exact_case(M, N, b, dt, 5)
     t = sk.fp8_encode(w.to(dev()))
