@@ -6,6 +6,8 @@
 // fragment be read without bank conflicts.  A fragment is 16 rows x 128
 // columns: lane l holds row l % 16 and the columns 16c..16c+15 and
 // 64+16c..64+16c+15, c = l / 16, the same ones in both operands.
+#include <utility>
+
 #include "fp8.h"
 
 namespace sketch {
@@ -280,59 +282,64 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 }
 
 // ---------------------------------------------------------------------------
-// 128 outputs x 32 FB tokens, 4 waves of 64 x 16 FB, two workgroups to a CU: for
-// fewer tiles than the big kernel needs, and (EXACT) for float32 Y, whose
-// fragments are widened to bfloat16 with their scales applied, so that every
-// product is exact and the sums are float32.  The loads of the next step go out
-// first: between the MFMAs, as above, they came too late for a step this short
-// (4096 x 4096 at 2048 tokens 49 -> 53 us).  K is split over blockIdx.y when the
-// tiles alone leave compute units idle; the parts are float32, rows padded to 4 outputs, and
-// fp8_add_kernel adds them in their order.
+// 32 FA outputs x 32 FB tokens (128 or 96 x 128 or 64), 4 waves of 16 FA x 16 FB,
+// two workgroups to a CU: for fewer tiles than the big kernel needs, and (EXACT)
+// for float32 Y, whose fragments are widened to bfloat16 with their scales
+// applied, so that every product is exact and the sums are float32.  The loads
+// of the next step go out first: between the MFMAs, as above, they came too late
+// for a step this short (4096 x 4096 at 2048 tokens 49 -> 53 us).  Loads two
+// steps ahead, and widening between the MFMAs, changed nothing (11008 x 4096 at
+// 512 tokens in float32: 66, 68 and 66 us); what costs there is that some compute
+// units have two tiles and others one.  K is split over blockIdx.y when the
+// tiles alone leave compute units idle; the parts are float32, rows padded to 4
+// outputs, and fp8_add_kernel adds them in their order.
 // ---------------------------------------------------------------------------
-template <int FB> constexpr uint32_t mid_stage() { return (128 + 32 * FB) * 128; }
-constexpr uint32_t kMidScales = (128 + 64) * 4;
-template <int FB> constexpr uint32_t mid_lds() { return 2 * mid_stage<FB>() + 2 * kMidScales; }
+template <int FA, int FB> constexpr uint32_t mid_stage() { return (32 * FA + 32 * FB) * 128; }
+constexpr uint32_t kMidScales = (128 + 64) * 4;   // dwords of 4 steps: one per token, one per 16 outputs
+template <int FA, int FB> constexpr uint32_t mid_lds() { return 2 * mid_stage<FA, FB>() + 2 * kMidScales; }
 
-template <int YD, bool EXACT, int FB>
+template <int YD, bool EXACT, int FA, int FB>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void fp8_gemm_kernel(GemmArgs a) {
-    static_assert(FB == 4 || FB == 2, "a wave loads FB times 8 rows of X");
+    static_assert(FA <= 4 && FB <= 4, "a wave loads FA times 8 rows of W and FB times 8 of X");
+    constexpr int kRows = 32 * FA;
     extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
     const Fp8Product& p = a.p;
-    constexpr uint32_t stage = mid_stage<FB>();
+    constexpr uint32_t stage = mid_stage<FA, FB>();
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int r = lane & 15, c = lane >> 4, wm = (wave >> 1) * 64, wt = (wave & 1) * 16 * FB;
+    const int r = lane & 15, c = lane >> 4, wm = (wave >> 1) * 16 * FA, wt = (wave & 1) * 16 * FB;
     uint32_t to, tt;
     tile_of(a, to, tt);
-    const int64_t o0 = int64_t(to) * 128, t0 = int64_t(tt) * (32 * FB);
+    const int64_t o0 = int64_t(to) * kRows, t0 = int64_t(tt) * (32 * FB);
     const uint32_t kend = uint32_t(uint64_t(p.kb) * (blockIdx.y + 1) / a.splits);
     const uint32_t kbeg = uint32_t(uint64_t(p.kb) * blockIdx.y / a.splits);
 
-    // loads of this wave: 32 rows of W and 8 FB of X per step; waves 0 and 1 the
-    // tokens' scales, wave 2 the outputs' (one block of 128)
+    // loads of this wave: 8 FA rows of W and 8 FB of X per step; waves 0 and 1 the
+    // tokens' scales, wave 2 the outputs' (16 outputs lie in one block of 128)
     const uint8_t *wbase = p.w + o0 * p.ld, *xbase = p.x + t0 * p.ld;
-    const uint32_t wlast = uint32_t(min(int64_t(127), p.M - 1 - o0)),
+    const uint32_t wlast = uint32_t(min(int64_t(kRows - 1), p.M - 1 - o0)),
                    xlast = uint32_t(min(int64_t(32 * FB - 1), p.T - 1 - t0));
     const uint32_t piece = uint32_t((lane & 7) ^ (lane >> 3)) * 16, ld = uint32_t(p.ld);
-    uint32_t woff[4], xoff[FB];
+    uint32_t woff[FA], xoff[FB];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) woff[i] = min(uint32_t((i * 4 + wave) * 8 + (lane >> 3)), wlast) * ld + piece;
+    for (int i = 0; i < FA; ++i) woff[i] = min(uint32_t((i * 4 + wave) * 8 + (lane >> 3)), wlast) * ld + piece;
 #pragma unroll
     for (int i = 0; i < FB; ++i) xoff[i] = min(uint32_t((i * 4 + wave) * 8 + (lane >> 3)), xlast) * ld + piece;
-    const uint8_t* sbase = wave < 2 ? p.xs + t0 * p.lds : p.ws + o0 / 128 * p.lds;
-    const uint32_t soff = wave < 2 ? min(uint32_t(wave * 64 + lane), xlast) * uint32_t(p.lds) : 0;
-    const uint32_t lds0 = lds_address(lds), lw = lds0 + wave * 1024, lx = lw + 16384;
+    const uint8_t* sbase = wave < 2 ? p.xs + t0 * p.lds : p.ws;
+    const uint32_t soff = (wave < 2 ? min(uint32_t(wave * 64 + lane), xlast)
+                                    : uint32_t(min(o0 + min(lane, 2 * FA - 1) * 16, p.M - 1) / 128)) * uint32_t(p.lds);
+    const uint32_t lds0 = lds_address(lds), lw = lds0 + wave * 1024, lx = lw + kRows * 128;
     const uint32_t lsc = lds0 + 2 * stage + wave * 256;
     auto load_part = [&](uint32_t k, int i) {   // i < 4
         const uint32_t st = ((k - kbeg) & 1) * stage;
-        dma16(wbase + size_t(k) * 128, woff[i], lw + st + i * 4096);
+        if (i < FA) dma16(wbase + size_t(k) * 128, woff[i], lw + st + i * 4096);
         if (i < FB) dma16(xbase + size_t(k) * 128, xoff[i], lx + st + i * 4096);
         if (i == 0 && ((k & 3) == 0 || k == kbeg) && wave < 3)
             dma4(sbase + (k & ~3u), soff, lsc + ((k >> 2) & 1) * kMidScales);
     };
 
-    f32x4 acc[4][FB];
+    f32x4 acc[FA][FB];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < FA; ++i)
 #pragma unroll
         for (int j = 0; j < FB; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
     const unsigned char* frag = lds + r * 128 + ((c ^ (r & 7)) << 4);
@@ -349,11 +356,13 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
             for (int i = 0; i < 4; ++i) load_part(k + 1, i);
         const uint32_t st = ((k - kbeg) & 1) * stage;
         const unsigned char *f1 = frag + st + wm * 128, *f2 = frag2 + st + wm * 128;
-        const unsigned char *g1 = frag + st + 16384 + wt * 128, *g2 = frag2 + st + 16384 + wt * 128;
+        const unsigned char *g1 = frag + st + (kRows + wt) * 128, *g2 = frag2 + st + (kRows + wt) * 128;
         const int* sc = reinterpret_cast<const int*>(lds + 2 * stage + ((k >> 2) & 1) * kMidScales);
-        const uint32_t as = uint32_t(sc[128]) >> (8 * (k & 3)) & 255u;
-        i32x8 af[4], bf[FB];
-        uint32_t bs[FB];
+        constexpr int kScales = FA == 4 ? 1 : FA;   // 128 outputs lie in one block
+        i32x8 af[FA], bf[FB];
+        uint32_t as[kScales], bs[FB];
+#pragma unroll
+        for (int i = 0; i < kScales; ++i) as[i] = uint32_t(sc[128 + wm / 16 + i]) >> (8 * (k & 3)) & 255u;
 #pragma unroll
         for (int j = 0; j < FB; ++j) {
             bf[j] = __builtin_shufflevector(*reinterpret_cast<const i32x4*>(g1 + j * 2048),
@@ -361,21 +370,20 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
             bs[j] = uint32_t(sc[wt + j * 16 + r]) >> (8 * (k & 3)) & 255u;
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < FA; ++i)
             af[i] = __builtin_shufflevector(*reinterpret_cast<const i32x4*>(f1 + i * 2048),
                                             *reinterpret_cast<const i32x4*>(f2 + i * 2048), 0, 1, 2, 3, 4, 5, 6, 7);
         if constexpr (EXACT) {
             bf16x8 bw[FB][4];
-            const float asf = fp8_scale(as);
 #pragma unroll
             for (int j = 0; j < FB; ++j)
 #pragma unroll
                 for (int q = 0; q < 4; ++q) bw[j][q] = fp8_widen(bf[j][2 * q], bf[j][2 * q + 1], fp8_scale(bs[j]));
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < FA; ++i) {
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    const bf16x8 aw = fp8_widen(af[i][2 * q], af[i][2 * q + 1], asf);
+                    const bf16x8 aw = fp8_widen(af[i][2 * q], af[i][2 * q + 1], fp8_scale(as[i % kScales]));
 #pragma unroll
                     for (int j = 0; j < FB; ++j)
                         acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(aw, bw[j][q], acc[i][j], 0, 0, 0);
@@ -383,11 +391,11 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < FA; ++i) {
 #pragma unroll
                 for (int j = 0; j < FB; ++j)
                     acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(af[i], bf[j], acc[i][j], 0, 0, 0,
-                                                                                  int(as), 0, int(bs[j]));
+                                                                                  int(as[i % kScales]), 0, int(bs[j]));
             }
         }
     }
@@ -400,7 +408,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
         const int64_t t = t0 + wt + j * 16 + r;
         if (t >= p.T) continue;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < FA; ++i) {
             const int64_t m = o0 + wm + i * 16 + 4 * c;
             if (a.splits > 1) {
                 if (m < p.M) *reinterpret_cast<f32x4*>(part + t * ldy + m) = acc[i][j];   // the padding too
@@ -425,8 +433,8 @@ __global__ __launch_bounds__(256) void fp8_add_kernel(GemmArgs a) {
 
 // Which kernel a product takes, and over how many workgroups K is split.
 struct GemmPlan {
-    int fa;            // of the big kernel, 0: fp8_gemm_kernel
-    int fb;            // of fp8_gemm_kernel
+    bool big;          // fp8_gemm_big_kernel, or fp8_gemm_kernel
+    int fa, fb;        // outputs and tokens of a tile, in units of 32
     uint32_t splits;
 };
 
@@ -442,13 +450,20 @@ GemmPlan gemm_plan(int64_t M, int64_t T, uint32_t kb, int ydt) {
             const int64_t tiles = (M + 32 * f - 1) / (32 * f) * ((T + 255) / 256), cost = (tiles + ncu - 1) / ncu * f;
             if (tiles >= ncu * 3 / 4 && (fa == 0 || cost < best)) best = cost, fa = f;
         }
-        if (fa) return {fa, 0, 1};
+        if (fa) return {true, fa, 8, 1};
     }
+    // K split so that there are about two workgroups to a compute unit
     const int fb = T <= 64 ? 2 : 4;
-    const int64_t mid = (M + 127) / 128 * ((T + 32 * fb - 1) / (32 * fb));
-    int64_t splits = mid >= ncu ? 1 : kSplitTo * ncu / mid;
-    if (splits > kb / 4) splits = kb / 4 > 1 ? kb / 4 : 1;
-    return {0, fb, uint32_t(splits)};
+    auto plan = [&](int fa) {
+        const int64_t tiles = (M + 32 * fa - 1) / (32 * fa) * ((T + 32 * fb - 1) / (32 * fb));
+        int64_t splits = tiles >= ncu ? 1 : kSplitTo * ncu / tiles;
+        if (splits > kb / 4) splits = kb / 4 > 1 ? kb / 4 : 1;
+        const int64_t rounds = (tiles * splits + ncu - 1) / ncu;
+        return std::pair{GemmPlan{false, fa, fb, uint32_t(splits)}, double(rounds * fa) / double(splits)};
+    };
+    // 96 outputs to a tile where these take fewer rounds (11008 x 4096 in float32, 512 tokens: 66 us with 128, 60 us)
+    const auto four = plan(4), three = plan(3);
+    return fb == 4 && three.second < four.second ? three.first : four.first;
 }
 
 template <int YD>
@@ -470,34 +485,38 @@ size_t fp8_gemm_workspace(int64_t M, int64_t T, uint32_t kb, int ydt) {
 
 sketch_status launch_fp8_gemm(const Fp8Product& p, void* ws, hipStream_t st) {
     const GemmPlan g = gemm_plan(p.M, p.T, p.kb, p.ydt);
-    const int64_t rows = g.fa ? 32 * g.fa : 128, cols = g.fa ? 256 : 32 * g.fb;
+    const int64_t rows = 32 * g.fa, cols = 32 * g.fb;
     GemmArgs a{p, uint32_t((p.M + rows - 1) / rows), uint32_t((p.T + cols - 1) / cols), g.splits, static_cast<float*>(ws)};
     const int64_t tiles = int64_t(a.tiles_o) * a.tiles_t;
     if (tiles > 0x7FFFFFFF) return SKETCH_EINVAL;
-    if (g.fa) {
+    if (g.big) {
         if (p.ydt == SKETCH_BF16)
             launch_big<SKETCH_BF16>(a, g.fa, unsigned(tiles), st);
         else
             launch_big<SKETCH_F16>(a, g.fa, unsigned(tiles), st);
         return launch_status();
     }
-    auto go = [&](auto four, auto two, auto add) {
+    auto go = [&](auto four, auto three, auto two, auto add) {
         const dim3 grid(unsigned(tiles), g.splits);
-        if (g.fb == 4)
-            four<<<grid, 256, mid_lds<4>(), st>>>(a);
+        if (g.fb == 2)
+            two<<<grid, 256, mid_lds<4, 2>(), st>>>(a);
+        else if (g.fa == 4)
+            four<<<grid, 256, mid_lds<4, 4>(), st>>>(a);
         else
-            two<<<grid, 256, mid_lds<2>(), st>>>(a);
+            three<<<grid, 256, mid_lds<3, 4>(), st>>>(a);
         if (g.splits == 1) return launch_status();
         if (hipGetLastError() != hipSuccess) return SKETCH_EDEVICE;
         add<<<dim3(unsigned((p.M + 1023) / 1024), unsigned(p.T)), 256, 0, st>>>(a);
         return launch_status();
     };
     if (p.ydt == SKETCH_F32)
-        return go(fp8_gemm_kernel<SKETCH_F32, true, 4>, fp8_gemm_kernel<SKETCH_F32, true, 2>, fp8_add_kernel<SKETCH_F32>);
+        return go(fp8_gemm_kernel<SKETCH_F32, true, 4, 4>, fp8_gemm_kernel<SKETCH_F32, true, 3, 4>,
+                  fp8_gemm_kernel<SKETCH_F32, true, 4, 2>, fp8_add_kernel<SKETCH_F32>);
     if (p.ydt == SKETCH_BF16)
-        return go(fp8_gemm_kernel<SKETCH_BF16, false, 4>, fp8_gemm_kernel<SKETCH_BF16, false, 2>,
-                  fp8_add_kernel<SKETCH_BF16>);
-    return go(fp8_gemm_kernel<SKETCH_F16, false, 4>, fp8_gemm_kernel<SKETCH_F16, false, 2>, fp8_add_kernel<SKETCH_F16>);
+        return go(fp8_gemm_kernel<SKETCH_BF16, false, 4, 4>, fp8_gemm_kernel<SKETCH_BF16, false, 3, 4>,
+                  fp8_gemm_kernel<SKETCH_BF16, false, 4, 2>, fp8_add_kernel<SKETCH_BF16>);
+    return go(fp8_gemm_kernel<SKETCH_F16, false, 4, 4>, fp8_gemm_kernel<SKETCH_F16, false, 3, 4>,
+              fp8_gemm_kernel<SKETCH_F16, false, 4, 2>, fp8_add_kernel<SKETCH_F16>);
 }
 
 }  // namespace sketch

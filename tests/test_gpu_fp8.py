@@ -147,7 +147,7 @@ def test_product_exact(M, N, b):
 @pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("M,N,b", [(300, 4001, 1), (300, 4001, 9), (2050, 640, 40), (700, 900, 300), (4096, 11008, 3),
                                    (384, 300, 2000), (130, 11008, 140), (2100, 2500, 1300),
-                                   (4333, 4300, 13), (16400, 200, 16)])
+                                   (4333, 4300, 13), (16400, 200, 16), (11008, 500, 480), (6000, 1000, 130)])
 def test_product_exact_larger(M, N, b, dt):
     w, x = exact_case(M, N, b, dt, 5)
     t = sk.fp8_encode(w.to(dev()))
@@ -155,7 +155,7 @@ def test_product_exact_larger(M, N, b, dt):
 
 
 @pytest.mark.parametrize("M,N,b", [(16, 128, 70), (700, 900, 1), (513, 1300, 65), (1000, 1111, 300), (2050, 640, 128),
-                                   (4300, 300, 3000), (4097, 1, 3001), (5000, 1155, 2570), (130, 11008, 140)])
+                                   (4300, 300, 3000), (4097, 1, 3001), (5000, 1155, 2570), (130, 11008, 140), (11000, 900, 250), (6001, 1000, 129)])
 @pytest.mark.parametrize("y", ["bf16", "f16"])
 def test_product_in_16_bits(M, N, b, y):
     """Small integers: groups of 8 products, and all sums, are exact on either
