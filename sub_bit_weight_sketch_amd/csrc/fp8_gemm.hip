@@ -452,16 +452,26 @@ GemmPlan gemm_plan(int64_t M, int64_t T, uint32_t kb, int ydt) {
         }
         if (fa) return {true, fa, 8, 1};
     }
-    // K split so that there are about two workgroups to a compute unit
+    // K split over idle compute units, up to about two workgroups to each, into
+    // the number of parts that should take least: a block of 128 columns takes a
+    // workgroup about 0.75 us, adding the parts a launch (6 us with its gaps) and
+    // their way to memory and back (4096 x 1024 at 200 tokens: 14.8 us in 2
+    // parts, 11.7 us in one; 4096 x 4096 at 256: 25.5 us in 8, 23.7 us in 4, 35 us
+    // in one).
     const int fb = T <= 64 ? 2 : 4;
     auto plan = [&](int fa) {
         const int64_t tiles = (M + 32 * fa - 1) / (32 * fa) * ((T + 32 * fb - 1) / (32 * fb));
-        int64_t splits = tiles >= ncu ? 1 : kSplitTo * ncu / tiles;
-        if (splits > kb / 4) splits = kb / 4 > 1 ? kb / 4 : 1;
+        const int64_t most = tiles >= ncu ? 1 : kSplitTo * ncu / tiles;
+        int64_t splits = 1;
+        double least = 0.75 * kb;
+        for (int64_t n = 2; n <= most && n <= kb / 4; ++n) {
+            const double us = 0.75 * double((kb + n - 1) / n) + 6.0 + 1e-6 * double(n * M * T);
+            if (us < least) least = us, splits = n;
+        }
         const int64_t rounds = (tiles * splits + ncu - 1) / ncu;
         return std::pair{GemmPlan{false, fa, fb, uint32_t(splits)}, double(rounds * fa) / double(splits)};
     };
-    // 96 outputs to a tile where these take fewer rounds (11008 x 4096 in float32, 512 tokens: 66 us with 128, 60 us)
+    // 96 outputs to a tile where these take fewer rounds (11008 x 4096 in float32, 512 tokens: 66 us with 128, 61 us)
     const auto four = plan(4), three = plan(3);
     return fb == 4 && three.second < four.second ? three.first : four.first;
 }
