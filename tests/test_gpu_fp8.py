@@ -385,3 +385,38 @@ def test_captured_and_replayed(b):
         eager = sk.fp8_matmul(t, xi)
         assert torch.equal(Y, eager)
         assert np.array_equal(u.to64(Y), u.to64(xi) @ u.to64(w).T)
+
+
+def test_many_rows_of_a_narrow_weight():
+    """More tokens than a grid's second dimension holds, few outputs."""
+    w, x = small_ints((40, 200), 1, 3), small_ints((70001, 200), 2, 4)
+    t = sk.fp8_encode(w.to(dev()))
+    want = torch.from_numpy(u.to64(x) @ u.to64(w).T).to(torch.float32)
+    for y in ("f32", "bf16"):
+        assert torch.equal(sk.fp8_matmul(t, x.to(dev()), dtype=DT[y]).cpu(), want.to(DT[y]))
+
+
+def test_encoder_captured_and_replayed():
+    """New weights and new rows at each replay, between eager calls."""
+    ws = [randn((200, 300), 20 + i, 0.1).to(dev()) for i in range(3)]
+    xs = [randn((9, 300), 30 + i, 1.0, "bf16").to(dev()) for i in range(3)]
+    W, X, flags = ws[0].clone(), xs[0].clone(), torch.zeros(1, dtype=torch.int32, device=dev())
+
+    def step():
+        rows = sk.fp8_encode(X, block_rows=1, check=False)
+        return sk.fp8_matmul(sk.fp8_encode(W, check=False, status=flags), rows)
+
+    step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        Y = step()
+    for w, x in zip(ws, xs):
+        W.copy_(w), X.copy_(x)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(Y, sk.fp8_matmul(sk.fp8_encode(w), x)) and int(flags.item()) == 0
+    W[3, 4] = float("inf")
+    g.replay()
+    torch.cuda.synchronize()
+    assert int(flags.item()) == sk.FLAG_WEIGHT_RANGE and torch.isnan(Y[:, :128]).all()

@@ -260,6 +260,24 @@ def test_experts_beyond_32_bits():
     assert ((Y - want).abs() / size).max() <= (6 * np.sqrt(H + I) + 16) * u.EPS32
 
 
+def test_strided_and_in_place():
+    """Rows of a wider tensor, a misaligned router, and the output written
+    over the tokens: all of x is read before any of y is written."""
+    H = 200
+    layer = make(H, 130, 8, 2, "f32", 15)
+    g = torch.Generator().manual_seed(16)
+    for T in (2, 30):
+        wide = torch.randn(T, 2 * H, generator=g).to(dev())
+        X = wide[:, 1:H + 1]
+        ref = sk.moe(layer, X.contiguous())
+        assert torch.equal(sk.moe(layer, X), ref)
+        off = torch.cat([torch.zeros(1, device=dev()), layer.router.flatten()])[1:].view(8, H)
+        assert off.data_ptr() % 16 != 0
+        assert torch.equal(sk.moe(sk.MoE(off, layer.gate, layer.up, layer.down, 2), X), ref)
+        Y = X.contiguous()
+        assert sk.moe(layer, Y, out=Y) is Y and torch.equal(Y, ref)
+
+
 def test_refusals():
     layer = make(128, 64, 8, 2, "bf16", 9)
     X = torch.zeros(4, 128, dtype=torch.bfloat16, device=dev())
