@@ -84,10 +84,13 @@ __device__ inline void store4(void* Y, int64_t e, f32x4 v, int64_t m, int64_t M,
 }
 
 // ---------------------------------------------------------------------------
-// 32 FA outputs x 256 tokens on the e4m3 matrix cores (16-bit Y).  8 waves, two
-// to a SIMD, each 16 FA x 64: 4 FA accumulators of 16x16.  FA is 8, or 7 or 6
-// where that many more tiles fill their last round over the compute units
-// better (28672 outputs x 2048 tokens: 896 tiles are 3.5 rounds, 1024 are 4).
+// 32 FA outputs x 256 tokens.  8 waves, two to a SIMD, each 16 FA x 64: 4 FA
+// accumulators of 16x16.  FA is 8, or 7 or 6 where that many more tiles fill
+// their last round over the compute units better (28672 outputs x 2048 tokens:
+// 896 tiles are 3.5 rounds, 1024 are 4).  For a 16-bit Y the e4m3 matrix cores
+// take the codes; for a float32 Y (EXACT, FA 4 or 3) both fragments are widened
+// to bfloat16 with their scales applied, a quarter of a block at a time, between
+// the MFMAs (28672 x 8192 at 2048 tokens: 758 us, 803 us without the two groups).
 //
 // The waves work in two groups, one on each SIMD, half a step apart: while one
 // group runs the MFMAs of its step from registers, the other reads its
@@ -108,7 +111,7 @@ constexpr uint32_t kBigStage = 512 * 128;           // 32 FA rows of W in the fi
 constexpr uint32_t kBigScales = (256 + 16) * 4;     // dwords of 4 steps: one per token, one per 16 outputs
 constexpr uint32_t kBigLds = 2 * kBigStage + 2 * kBigScales;
 
-template <int YD, int FA>
+template <int YD, int FA, bool EXACT>
 __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void fp8_gemm_big_kernel(GemmArgs a) {
     extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
     const Fp8Product& p = a.p;
@@ -182,9 +185,45 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
             for (int i = 0; i < kScales; ++i) as[i] = int(uint32_t(as[i]) >> 8);
         }
     };
-    // the step's MFMAs, with between(n), n < 2 FA, after every two
+    // the step's MFMAs, with between(n) among them, n < kBetween
+    constexpr int kBetween = EXACT ? 4 * FA : 2 * FA;
     auto compute = [&](auto between) {
         __builtin_amdgcn_s_setprio(1);
+        if constexpr (EXACT) {
+            // quarters of the block; what the next 4 MFMAs need is widened before the 4 that
+            // run meanwhile
+            float asf[kScales], bsf[4];
+#pragma unroll
+            for (int i = 0; i < kScales; ++i) asf[i] = fp8_scale(uint32_t(as[i]) & 255u);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) bsf[j] = fp8_scale(uint32_t(bs[j]) & 255u);
+            bf16x8 aw[2], bw[2][4];
+            auto widen_a = [&](int n) {   // n = q FA + i
+                const int i = n % FA, q = n / FA;
+                aw[n & 1] = fp8_widen(af[i][2 * q], af[i][2 * q + 1], asf[i % kScales]);
+            };
+            auto widen_b = [&](int q, int j) { bw[q & 1][j] = fp8_widen(bf[j][2 * q], bf[j][2 * q + 1], bsf[j]); };
+            widen_a(0);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) widen_b(0, j);
+#pragma unroll
+            for (int n = 0; n < 4 * FA; ++n) {
+                const int i = n % FA, q = n / FA;
+                if (n + 1 < 4 * FA) widen_a(n + 1);
+                if (q < 3) {
+#pragma unroll
+                    for (int j = i * 4 / FA; j < (i + 1) * 4 / FA; ++j) widen_b(q + 1, j);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(aw[n & 1], bw[q & 1][j], acc[i][j], 0, 0, 0);
+                __builtin_amdgcn_sched_barrier(0);
+                between(n);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            __builtin_amdgcn_s_setprio(0);
+            return;
+        }
 #pragma unroll
         for (int n = 0; n < 2 * FA; ++n) {
             const int i = n >> 1, j = 2 * (n & 1);
@@ -200,6 +239,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     };
 
     const uint32_t last = p.kb - 1;
+    constexpr int kLoads = 8 + kTurns;   // of a wave of group 1
 #pragma unroll
     for (uint32_t k = 0; k < 2; ++k) {
 #pragma unroll
@@ -233,10 +273,13 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
             barrier();
             if (((k + 2) & 3) == 0 && k + 2 < p.kb) load_scales(k + 2);
             compute([&](int n) {
-                if (n < 8)
-                    load_x(min(k + 2, last), k & 1, n);
-                else if (n - 8 < kTurns)
-                    load_w(min(k + 2, last), k & 1, n - 8);
+#pragma unroll
+                for (int i = n * kLoads / kBetween; i < (n + 1) * kLoads / kBetween; ++i) {
+                    if (i < 8)
+                        load_x(min(k + 2, last), k & 1, i);
+                    else
+                        load_w(min(k + 2, last), k & 1, i - 8);
+                }
             });
             barrier();
         }
@@ -245,7 +288,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 
     // Whole tiles go out through LDS, 256 contiguous bytes of a token's row and
     // more at a time; the others element by element where they have to.
-    if (o0 + kRows <= p.M && t0 + 256 <= p.T && p.M % 8 == 0) {
+    if (!EXACT && o0 + kRows <= p.M && t0 + 256 <= p.T && p.M % 8 == 0) {
         constexpr uint32_t kRow = FA * 32;   // bytes of a token's outputs in the wave's tile
         unsigned char* mine = lds + wave * (64 * kRow);
         barrier();   // every wave is done reading its fragments
@@ -283,14 +326,11 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 
 // ---------------------------------------------------------------------------
 // 32 FA outputs x 32 FB tokens (128 or 96 x 128 or 64), 4 waves of 16 FA x 16 FB,
-// two workgroups to a CU: for fewer tiles than the big kernel needs, and (EXACT)
-// for float32 Y, whose fragments are widened to bfloat16 with their scales
-// applied, so that every product is exact and the sums are float32.  The loads
-// of the next step go out first: between the MFMAs, as above, they came too late
-// for a step this short (4096 x 4096 at 2048 tokens 49 -> 53 us).  Loads two
-// steps ahead, and widening between the MFMAs, changed nothing (11008 x 4096 at
-// 512 tokens in float32: 66, 68 and 66 us); what costs there is that some compute
-// units have two tiles and others one.  K is split over blockIdx.y when the
+// two workgroups to a CU: for fewer tiles than the big kernel needs.  EXACT is as
+// above.  The loads of the next step go out first: between the MFMAs, as above,
+// they came too late for a step this short (4096 x 4096 at 2048 tokens 49 -> 53
+// us).  Loads two steps ahead, and widening between the MFMAs, changed nothing
+// (11008 x 4096 at 512 tokens in float32: 66, 68 and 66 us).  K is split over blockIdx.y when the
 // tiles alone leave compute units idle; the parts are float32, rows padded to 4
 // outputs, and fp8_add_kernel adds them in their order.
 // ---------------------------------------------------------------------------
@@ -442,16 +482,15 @@ constexpr int kSplitTo = 2;
 
 GemmPlan gemm_plan(int64_t M, int64_t T, uint32_t kb, int ydt) {
     const int64_t ncu = compute_units();
-    if (ydt != SKETCH_F32) {
-        // rounds of tiles over the compute units, in units of 32 outputs
-        int64_t best = 0;
-        int fa = 0;
-        for (int f : {8, 7, 6}) {
-            const int64_t tiles = (M + 32 * f - 1) / (32 * f) * ((T + 255) / 256), cost = (tiles + ncu - 1) / ncu * f;
-            if (tiles >= ncu * 3 / 4 && (fa == 0 || cost < best)) best = cost, fa = f;
-        }
-        if (fa) return {true, fa, 8, 1};
+    // rounds of the big kernel's tiles over the compute units, in units of 32 outputs
+    int64_t best = 0;
+    int big = 0;
+    for (int f : {8, 7, 6, 4, 3}) {
+        if ((f < 6) != (ydt == SKETCH_F32)) continue;
+        const int64_t tiles = (M + 32 * f - 1) / (32 * f) * ((T + 255) / 256), cost = (tiles + ncu - 1) / ncu * f;
+        if (tiles >= ncu * 3 / 4 && (big == 0 || cost < best)) best = cost, big = f;
     }
+    if (big) return {true, big, 8, 1};
     // K split over idle compute units, up to about two workgroups to each, into
     // the number of parts that should take least: a block of 128 columns takes a
     // workgroup about 0.75 us, adding the parts a launch (6 us with its gaps) and
@@ -471,19 +510,23 @@ GemmPlan gemm_plan(int64_t M, int64_t T, uint32_t kb, int ydt) {
         const int64_t rounds = (tiles * splits + ncu - 1) / ncu;
         return std::pair{GemmPlan{false, fa, fb, uint32_t(splits)}, double(rounds * fa) / double(splits)};
     };
-    // 96 outputs to a tile where these take fewer rounds (11008 x 4096 in float32, 512 tokens: 66 us with 128, 61 us)
+    // 96 outputs to a tile where these take fewer rounds (11008 x 4096, 256 tokens: 37 us with 128, 34 us)
     const auto four = plan(4), three = plan(3);
     return fb == 4 && three.second < four.second ? three.first : four.first;
 }
 
-template <int YD>
 void launch_big(const GemmArgs& a, int fa, unsigned grid, hipStream_t st) {
-    if (fa == 8)
-        fp8_gemm_big_kernel<YD, 8><<<grid, 512, kBigLds, st>>>(a);
-    else if (fa == 7)
-        fp8_gemm_big_kernel<YD, 7><<<grid, 512, kBigLds, st>>>(a);
+    auto go = [&](auto kernel) { kernel<<<grid, 512, kBigLds, st>>>(a); };
+    if (a.p.ydt == SKETCH_F32)
+        fa == 4 ? go(fp8_gemm_big_kernel<SKETCH_F32, 4, true>) : go(fp8_gemm_big_kernel<SKETCH_F32, 3, true>);
+    else if (a.p.ydt == SKETCH_BF16)
+        fa == 8   ? go(fp8_gemm_big_kernel<SKETCH_BF16, 8, false>)
+        : fa == 7 ? go(fp8_gemm_big_kernel<SKETCH_BF16, 7, false>)
+                  : go(fp8_gemm_big_kernel<SKETCH_BF16, 6, false>);
     else
-        fp8_gemm_big_kernel<YD, 6><<<grid, 512, kBigLds, st>>>(a);
+        fa == 8   ? go(fp8_gemm_big_kernel<SKETCH_F16, 8, false>)
+        : fa == 7 ? go(fp8_gemm_big_kernel<SKETCH_F16, 7, false>)
+                  : go(fp8_gemm_big_kernel<SKETCH_F16, 6, false>);
 }
 
 }  // namespace
@@ -500,10 +543,7 @@ sketch_status launch_fp8_gemm(const Fp8Product& p, void* ws, hipStream_t st) {
     const int64_t tiles = int64_t(a.tiles_o) * a.tiles_t;
     if (tiles > 0x7FFFFFFF) return SKETCH_EINVAL;
     if (g.big) {
-        if (p.ydt == SKETCH_BF16)
-            launch_big<SKETCH_BF16>(a, g.fa, unsigned(tiles), st);
-        else
-            launch_big<SKETCH_F16>(a, g.fa, unsigned(tiles), st);
+        launch_big(a, g.fa, unsigned(tiles), st);
         return launch_status();
     }
     auto go = [&](auto four, auto three, auto two, auto add) {

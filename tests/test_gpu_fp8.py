@@ -147,7 +147,7 @@ def test_product_exact(M, N, b):
 @pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("M,N,b", [(300, 4001, 1), (300, 4001, 9), (2050, 640, 40), (700, 900, 300), (4096, 11008, 3),
                                    (384, 300, 2000), (130, 11008, 140), (2100, 2500, 1300),
-                                   (4333, 4300, 13), (16400, 200, 16), (11008, 500, 480), (6000, 1000, 130)])
+                                   (4333, 4300, 13), (16400, 200, 16), (11008, 500, 480), (6000, 1000, 130), (8200, 1155, 1030), (4099, 1, 3001)])
 def test_product_exact_larger(M, N, b, dt):
     w, x = exact_case(M, N, b, dt, 5)
     t = sk.fp8_encode(w.to(dev()))
@@ -235,7 +235,7 @@ def test_far_scales(b, y, scale):
 
 
 @pytest.mark.parametrize("M,b,y", [(130, 1, "f32"), (130, 1, "bf16"), (130, 9, "f32"), (130, 9, "bf16"), (130, 40, "f32"),
-                                   (130, 200, "bf16"), (5000, 2600, "bf16")])
+                                   (130, 200, "bf16"), (5000, 2600, "bf16"), (5001, 2600, "f32")])
 @pytest.mark.parametrize("byte,other", [(0, 217), (1, 187), (9, 150), (247, 60), (254, 50)])
 def test_scale_bytes_at_their_ends(M, b, y, byte, other):
     """Tables from elsewhere with scales up to the ends of their range, on the
@@ -254,7 +254,7 @@ def test_scale_bytes_at_their_ends(M, b, y, byte, other):
 
 
 @pytest.mark.parametrize("M,b,y", [(300, 1, "f32"), (300, 3, "bf16"), (300, 9, "f32"), (300, 40, "f32"),
-                                   (300, 200, "bf16"), (5000, 2600, "bf16")])
+                                   (300, 200, "bf16"), (5000, 2600, "bf16"), (5001, 2600, "f32")])
 @pytest.mark.parametrize("code", [0.0, 1.0, -448.0])
 def test_a_nan_scale_is_nan_whatever_its_codes(M, b, y, code):
     """The scale byte 255 over ordinary codes, zeros among them, in a block of
