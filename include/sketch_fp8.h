@@ -57,6 +57,12 @@ typedef struct {
 /* x_dtype of rows that sketch_fp8_encode wrote (block_rows 1). */
 #define SKETCH_FP8_ROWS 3
 
+/* With y_dtype SKETCH_BF16: float32 sums for any number of rows. */
+#define SKETCH_FP8_F32_SUMS 256
+
+/* Rows of a product up to which a bfloat16 Y has float32 sums anyway. */
+#define SKETCH_FP8_EXACT_BATCH 64
+
 /* Limits (SKETCH_EINVAL beyond them). */
 #define SKETCH_FP8_MAX_N 1048576
 #define SKETCH_FP8_MAX_M 16777216
@@ -85,9 +91,9 @@ sketch_status sketch_fp8_encode(const sketch_fp8_params* p, const void* W, sketc
  * sketch_fp8_workspace_bytes -- device scratch sketch_fp8_matmul needs for
  * `batch` rows of X on the current device (host only): the encoded rows, and
  * the float32 parts where K is split over workgroups.  Its contents need no initialisation; calls
- * that overlap in time need separate workspaces.
+ * that overlap in time need separate workspaces.  y_dtype as for the product.
  */
-sketch_status sketch_fp8_workspace_bytes(const sketch_fp8_params* p, int64_t batch, int x_dtype, sketch_dtype y_dtype,
+sketch_status sketch_fp8_workspace_bytes(const sketch_fp8_params* p, int64_t batch, int x_dtype, int y_dtype,
                                          size_t* bytes);
 
 /*
@@ -97,17 +103,24 @@ sketch_status sketch_fp8_workspace_bytes(const sketch_fp8_params* p, int64_t bat
  *            with block_rows 1 does; or, with x_dtype SKETCH_FP8_ROWS, the
  *            buffer of such an encode of {batch, N, 1, 1}, for rows that
  *            several linears share.  Both give the same bits.
- *   Y        [batch][M] of y_dtype, overwritten (rounded once from float32).
- * Products of e4m3 codes are exact.  With y_dtype SKETCH_F32 they are summed
- * in float32, on the bfloat16 matrix cores.  With a 16-bit y_dtype the sums run
- * on the e4m3 matrix cores, twice as fast, which add 8 neighbouring products
- * at a time with 13 bits below the largest of them, and those sums in float32:
- * within the sum, over the groups of 8, of 7 * 2^-13 * max |product|, far below
- * the rounding of Y.  A row of X that holds NaN or an infinity gives a row of
- * NaN in Y; other rows are unaffected.  batch == 0 or M == 0 is a no-op.
+ *   Y        [batch][M] of y_dtype (SKETCH_F32, SKETCH_BF16, SKETCH_F16, or
+ *            SKETCH_BF16 | SKETCH_FP8_F32_SUMS), overwritten (rounded once from
+ *            float32).
+ * Products of e4m3 codes are exact, and are summed in float32, on the bfloat16
+ * matrix cores.  The one exception is SKETCH_BF16 with more than
+ * SKETCH_FP8_EXACT_BATCH rows: there the sums run on the e4m3 matrix cores,
+ * twice as fast, which add 8 neighbouring products at a time with 13 bits below
+ * the largest of them, and those sums in float32.  At worst that is off by the
+ * sum, over the groups of 8, of 7 * 2^-13 * max |product|, which can exceed the
+ * rounding of Y: an output much smaller than the products that it sums (these
+ * cancel) may lose its digits.  On ordinary data it measured 1.5e-5 to 5e-5 of
+ * an output's size, a thirtieth or less of what the rounding to bfloat16 does.
+ * SKETCH_FP8_F32_SUMS is the way around it.  A row of X that holds NaN or an
+ * infinity gives a row of NaN in Y; other rows are unaffected.  batch == 0 or
+ * M == 0 is a no-op.
  */
 sketch_status sketch_fp8_matmul(const sketch_fp8_params* p, const void* buf, const void* X, int x_dtype,
-                                int64_t batch, void* Y, sketch_dtype y_dtype, void* workspace,
+                                int64_t batch, void* Y, int y_dtype, void* workspace,
                                 size_t workspace_bytes, void* stream);
 
 /*

@@ -101,10 +101,11 @@ struct Fp8Product {
     int64_t M, T, ld, lds;
     uint32_t kb;   // blocks of 128 columns
     int ydt;
+    bool exact;    // float32 sums
 };
 
 // Products of many rows (fp8_gemm.hip): scratch (parts of a split of K), launch.
-size_t fp8_gemm_workspace(int64_t M, int64_t T, uint32_t kb, int ydt);
+size_t fp8_gemm_workspace(int64_t M, int64_t T, uint32_t kb, bool exact);
 sketch_status launch_fp8_gemm(const Fp8Product& p, void* ws, hipStream_t st);
 
 sketch_status launch_fp8_encode(const sketch_fp8_params* p, const sketch_fp8_shape& s, const void* W,

@@ -135,11 +135,11 @@ __global__ __launch_bounds__(256) void fp8_encode_rows_kernel(EncodeArgs a) {
 // D: token l % 16, outputs 4c..4c+3.  The waves' sums meet in LDS and are
 // added in their order.
 //
-// EXACT (float32 Y): both fragments are widened to bfloat16 with their scales
-// applied, four 16x16x32 MFMAs, exact products, float32 sums.  Otherwise one
-// 16x16x128 MFMA on the codes, which applies the scales itself: its sums of 8
-// neighbouring products keep 13 bits below the largest, which a 16-bit Y does
-// not show, and nothing is spent on widening.
+// Both fragments are widened to bfloat16 with their scales applied, four 16x16x32
+// MFMAs, exact products, float32 sums.  (One 16x16x128 MFMA on the codes applies
+// the scales itself, but its sums of 8 neighbouring products keep only 13 bits
+// below the largest; it saves 0 to 3 us here: 11008 x 4096 at 4 rows 17.2 -> 14.4
+// us, at 16 rows 17.9 -> 17.8 us.)
 // ---------------------------------------------------------------------------
 constexpr int kWaves = 8;
 constexpr int kRun = 4;      // blocks of 128 columns in a wave's run
@@ -151,17 +151,12 @@ __device__ inline i32x8 load_frag(const uint8_t* lo, const uint8_t* hi) {
 }
 
 // acc += A B for a block: the fragments and their scale bytes.
-template <bool EXACT>
 __device__ inline f32x4 multiply(const i32x8& a, uint32_t as, const i32x8& b, uint32_t bs, f32x4 acc) {
-    if constexpr (EXACT) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fp8_widen(a[2 * q], a[2 * q + 1], fp8_scale(as)),
-                                                          fp8_widen(b[2 * q], b[2 * q + 1], fp8_scale(bs)), acc, 0, 0, 0);
-        return acc;
-    } else {
-        return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, acc, 0, 0, 0, int(as), 0, int(bs));
-    }
+    for (int q = 0; q < 4; ++q)
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fp8_widen(a[2 * q], a[2 * q + 1], fp8_scale(as)),
+                                                      fp8_widen(b[2 * q], b[2 * q + 1], fp8_scale(bs)), acc, 0, 0, 0);
+    return acc;
 }
 
 __device__ inline void store_y(const Fp8Product& p, int64_t t, int64_t m, float v) {
@@ -222,7 +217,7 @@ __device__ inline void add_and_store(const Fp8Product& p, float (*part)[16][RT *
 // blocks of its own run, 16 lanes to a (block, row), into its own part of LDS.
 // Repeated by all workgroups, this costs more than the launch beyond a few
 // rows (28672 x 8192, 16 rows: 114 us against 66 us in two launches).
-template <int XD, bool EXACT, int NP>
+template <int XD, int NP>
 __global__ __launch_bounds__(kWaves * 64) void fp8_tokens_kernel(Fp8Product p, int64_t N) {
     __shared__ __attribute__((aligned(16))) uint8_t codes[kWaves][4 * NP][128];
     __shared__ uint32_t scales[kWaves][4 * NP];
@@ -259,7 +254,7 @@ __global__ __launch_bounds__(kWaves * 64) void fp8_tokens_kernel(Fp8Product p, i
             if (k + u >= p.kb) break;
             const int at = u * T + min(r, T - 1);   // tokens past the last are not stored
             const i32x8 xf = load_frag(&codes[wave][at][(c ^ (at & 7)) << 4], &codes[wave][at][((c + 4) ^ (at & 7)) << 4]);
-            acc[0] = multiply<EXACT>(w.f[0][u], w.scales >> (8 * u) & 255u, xf, scales[wave][at], acc[0]);
+            acc[0] = multiply(w.f[0][u], w.scales >> (8 * u) & 255u, xf, scales[wave][at], acc[0]);
         }
     }
     add_and_store<1>(p, part, acc, m0);
@@ -267,7 +262,7 @@ __global__ __launch_bounds__(kWaves * 64) void fp8_tokens_kernel(Fp8Product p, i
 
 // Up to 16 encoded rows, read from memory (they stay in the caches).  The
 // sums run in the same order as in fp8_tokens_kernel.
-template <int RT, bool EXACT>
+template <int RT>
 __global__ __launch_bounds__(kWaves * 64) void fp8_rows_kernel(Fp8Product p) {
     __shared__ float part[kWaves][16][RT * 16 + 1];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -293,14 +288,12 @@ __global__ __launch_bounds__(kWaves * 64) void fp8_rows_kernel(Fp8Product p) {
             if (k + u >= p.kb) break;
 #pragma unroll
             for (int i = 0; i < RT; ++i)
-                acc[i] = multiply<EXACT>(w.f[i][u], w.scales >> (8 * u) & 255u, xr.f[0][u], xr.scales >> (8 * u) & 255u,
-                                         acc[i]);
+                acc[i] = multiply(w.f[i][u], w.scales >> (8 * u) & 255u, xr.f[0][u], xr.scales >> (8 * u) & 255u, acc[i]);
         }
     }
     add_and_store<RT>(p, part, acc, m0);
 }
 
-template <bool EXACT>
 sketch_status launch_few(const Fp8Product& p, int x_dtype, int64_t N, hipStream_t st) {
     auto tokens = [&](auto kernel) {
         kernel<<<unsigned((p.M + 15) / 16), kWaves * 64, 0, st>>>(p, N);
@@ -311,20 +304,33 @@ sketch_status launch_few(const Fp8Product& p, int x_dtype, int64_t N, hipStream_
         return launch_status();
     };
     if (x_dtype == SKETCH_F32)
-        return p.T == 1 ? tokens(fp8_tokens_kernel<SKETCH_F32, EXACT, 1>) : tokens(fp8_tokens_kernel<SKETCH_F32, EXACT, 4>);
+        return p.T == 1 ? tokens(fp8_tokens_kernel<SKETCH_F32, 1>) : tokens(fp8_tokens_kernel<SKETCH_F32, 4>);
     if (x_dtype == SKETCH_BF16)
-        return p.T == 1 ? tokens(fp8_tokens_kernel<SKETCH_BF16, EXACT, 1>) : tokens(fp8_tokens_kernel<SKETCH_BF16, EXACT, 4>);
+        return p.T == 1 ? tokens(fp8_tokens_kernel<SKETCH_BF16, 1>) : tokens(fp8_tokens_kernel<SKETCH_BF16, 4>);
     if (x_dtype == SKETCH_F16)
-        return p.T == 1 ? tokens(fp8_tokens_kernel<SKETCH_F16, EXACT, 1>) : tokens(fp8_tokens_kernel<SKETCH_F16, EXACT, 4>);
+        return p.T == 1 ? tokens(fp8_tokens_kernel<SKETCH_F16, 1>) : tokens(fp8_tokens_kernel<SKETCH_F16, 4>);
     // 32 outputs to a workgroup halve the reads of X (16 rows, 5000 x 28672: 61 us with 16 outputs, 48 us with 32;
     // 8192 x 28672 68 and 57); where those of 16 all have a compute unit to themselves (4096 x 28672: 38 and 48), or a
     // wave has but one run (11008 x 4096: 17.7 and 18.7), 16 have the shorter way
     const int64_t ncu = compute_units();
     const bool two = p.M >= 64 * ncu || (p.M > 16 * ncu && p.kb > kWaves * kRun);
-    return two ? rows(fp8_rows_kernel<2, EXACT>, 32) : rows(fp8_rows_kernel<1, EXACT>, 16);
+    return two ? rows(fp8_rows_kernel<2>, 32) : rows(fp8_rows_kernel<1>, 16);
 }
 
 bool valid_dtype(int d) { return d == SKETCH_F32 || d == SKETCH_BF16 || d == SKETCH_F16; }
+
+// y_dtype of a product: the type of Y, and how the products are summed.  Only
+// the rounding to bfloat16 (rms 1.7e-3 of an output) hides the e4m3 matrix
+// cores' sums (up to 5e-5); that to binary16 (2.1e-4) does not, and up to
+// SKETCH_FP8_EXACT_BATCH rows the product is bound by its bytes and gains
+// nothing to speak of (11008 x 4096 at 64 rows 23.1 us either way; 28672 x 8192
+// at 2048 rows 364 us, with float32 sums 760 us).
+bool y_type(int y_dtype, int64_t batch, int* type, bool* exact) {
+    const bool asked = y_dtype == (SKETCH_BF16 | SKETCH_FP8_F32_SUMS);
+    *type = asked ? int(SKETCH_BF16) : y_dtype;
+    *exact = *type != SKETCH_BF16 || asked || batch <= SKETCH_FP8_EXACT_BATCH;
+    return valid_dtype(*type);
+}
 
 }  // namespace
 
@@ -378,13 +384,15 @@ sketch_status sketch_fp8_encode(const sketch_fp8_params* p, const void* W, sketc
     return launch_fp8_encode(p, s, W, w_dtype, buf, status_dev, static_cast<hipStream_t>(stream));
 }
 
-sketch_status sketch_fp8_workspace_bytes(const sketch_fp8_params* p, int64_t batch, int x_dtype, sketch_dtype y_dtype,
+sketch_status sketch_fp8_workspace_bytes(const sketch_fp8_params* p, int64_t batch, int x_dtype, int y_dtype,
                                          size_t* bytes) {
     sketch_fp8_shape s, xs;
     sketch_status rc = fp8_shape(p, &s);
     if (rc != SKETCH_OK) return rc;
+    int ydt;
+    bool exact;
     if (!bytes || batch < 0 || p->block_rows != 128 || p->count > 1 || (!valid_dtype(x_dtype) && x_dtype != SKETCH_FP8_ROWS) ||
-        !valid_dtype(y_dtype))
+        !y_type(y_dtype, batch, &ydt, &exact))
         return SKETCH_EINVAL;
     const sketch_fp8_params xp{batch, p->N, 1, 1};
     rc = fp8_shape(&xp, &xs);
@@ -392,12 +400,12 @@ sketch_status sketch_fp8_workspace_bytes(const sketch_fp8_params* p, int64_t bat
     *bytes = 0;
     if (batch == 0 || p->M == 0) return SKETCH_OK;
     if (x_dtype != SKETCH_FP8_ROWS && batch > kTokens) *bytes += xs.bytes;
-    if (batch > 16) *bytes += fp8_gemm_workspace(p->M, batch, uint32_t(s.col_blocks), y_dtype);
+    if (batch > 16) *bytes += fp8_gemm_workspace(p->M, batch, uint32_t(s.col_blocks), exact);
     return SKETCH_OK;
 }
 
 sketch_status sketch_fp8_matmul(const sketch_fp8_params* p, const void* buf, const void* X, int x_dtype,
-                                int64_t batch, void* Y, sketch_dtype y_dtype, void* workspace,
+                                int64_t batch, void* Y, int y_dtype, void* workspace,
                                 size_t workspace_bytes, void* stream) {
     size_t need = 0;
     sketch_status rc = sketch_fp8_workspace_bytes(p, batch, x_dtype, y_dtype, &need);
@@ -425,11 +433,11 @@ sketch_status sketch_fp8_matmul(const sketch_fp8_params* p, const void* buf, con
         x8 = ws;
         ws += xs.bytes;
     }
-    const Fp8Product a{w8, w8 + s.scales_offset, x8, x8 + xs.scales_offset, Y, p->M, batch, s.ld, s.lds,
-                       uint32_t(s.col_blocks), int(y_dtype)};
+    Fp8Product a{w8, w8 + s.scales_offset, x8, x8 + xs.scales_offset, Y, p->M, batch, s.ld, s.lds,
+                 uint32_t(s.col_blocks), 0, true};
+    (void)y_type(y_dtype, batch, &a.ydt, &a.exact);
     if (batch > 16) return launch_fp8_gemm(a, ws, st);
-    const int few = encode ? int(SKETCH_FP8_ROWS) : x_dtype;
-    return y_dtype == SKETCH_F32 ? launch_few<true>(a, few, p->N, st) : launch_few<false>(a, few, p->N, st);
+    return launch_few(a, encode ? int(SKETCH_FP8_ROWS) : x_dtype, p->N, st);
 }
 
 }  // extern "C"

@@ -87,8 +87,8 @@ __device__ inline void store4(void* Y, int64_t e, f32x4 v, int64_t m, int64_t M,
 // 32 FA outputs x 256 tokens.  8 waves, two to a SIMD, each 16 FA x 64: 4 FA
 // accumulators of 16x16.  FA is 8, or 7 or 6 where that many more tiles fill
 // their last round over the compute units better (28672 outputs x 2048 tokens:
-// 896 tiles are 3.5 rounds, 1024 are 4).  For a 16-bit Y the e4m3 matrix cores
-// take the codes; for a float32 Y (EXACT, FA 4 or 3) both fragments are widened
+// 896 tiles are 3.5 rounds, 1024 are 4).  The e4m3 matrix cores take the codes, or,
+// for float32 sums (EXACT, FA 4 or 3), both fragments are widened
 // to bfloat16 with their scales applied, a quarter of a block at a time, between
 // the MFMAs (28672 x 8192 at 2048 tokens: 758 us, 803 us without the two groups).
 //
@@ -288,7 +288,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 
     // Whole tiles go out through LDS, 256 contiguous bytes of a token's row and
     // more at a time; the others element by element where they have to.
-    if (!EXACT && o0 + kRows <= p.M && t0 + 256 <= p.T && p.M % 8 == 0) {
+    if (YD != SKETCH_F32 && o0 + kRows <= p.M && t0 + 256 <= p.T && p.M % 8 == 0) {
         constexpr uint32_t kRow = FA * 32;   // bytes of a token's outputs in the wave's tile
         unsigned char* mine = lds + wave * (64 * kRow);
         barrier();   // every wave is done reading its fragments
@@ -480,13 +480,13 @@ struct GemmPlan {
 
 constexpr int kSplitTo = 2;
 
-GemmPlan gemm_plan(int64_t M, int64_t T, uint32_t kb, int ydt) {
+GemmPlan gemm_plan(int64_t M, int64_t T, uint32_t kb, bool exact) {
     const int64_t ncu = compute_units();
     // rounds of the big kernel's tiles over the compute units, in units of 32 outputs
     int64_t best = 0;
     int big = 0;
     for (int f : {8, 7, 6, 4, 3}) {
-        if ((f < 6) != (ydt == SKETCH_F32)) continue;
+        if ((f < 6) != exact) continue;
         const int64_t tiles = (M + 32 * f - 1) / (32 * f) * ((T + 255) / 256), cost = (tiles + ncu - 1) / ncu * f;
         if (tiles >= ncu * 3 / 4 && (big == 0 || cost < best)) best = cost, big = f;
     }
@@ -517,27 +517,27 @@ GemmPlan gemm_plan(int64_t M, int64_t T, uint32_t kb, int ydt) {
 
 void launch_big(const GemmArgs& a, int fa, unsigned grid, hipStream_t st) {
     auto go = [&](auto kernel) { kernel<<<grid, 512, kBigLds, st>>>(a); };
-    if (a.p.ydt == SKETCH_F32)
-        fa == 4 ? go(fp8_gemm_big_kernel<SKETCH_F32, 4, true>) : go(fp8_gemm_big_kernel<SKETCH_F32, 3, true>);
-    else if (a.p.ydt == SKETCH_BF16)
+    if (!a.p.exact)
         fa == 8   ? go(fp8_gemm_big_kernel<SKETCH_BF16, 8, false>)
         : fa == 7 ? go(fp8_gemm_big_kernel<SKETCH_BF16, 7, false>)
                   : go(fp8_gemm_big_kernel<SKETCH_BF16, 6, false>);
+    else if (a.p.ydt == SKETCH_F32)
+        fa == 4 ? go(fp8_gemm_big_kernel<SKETCH_F32, 4, true>) : go(fp8_gemm_big_kernel<SKETCH_F32, 3, true>);
+    else if (a.p.ydt == SKETCH_BF16)
+        fa == 4 ? go(fp8_gemm_big_kernel<SKETCH_BF16, 4, true>) : go(fp8_gemm_big_kernel<SKETCH_BF16, 3, true>);
     else
-        fa == 8   ? go(fp8_gemm_big_kernel<SKETCH_F16, 8, false>)
-        : fa == 7 ? go(fp8_gemm_big_kernel<SKETCH_F16, 7, false>)
-                  : go(fp8_gemm_big_kernel<SKETCH_F16, 6, false>);
+        fa == 4 ? go(fp8_gemm_big_kernel<SKETCH_F16, 4, true>) : go(fp8_gemm_big_kernel<SKETCH_F16, 3, true>);
 }
 
 }  // namespace
 
-size_t fp8_gemm_workspace(int64_t M, int64_t T, uint32_t kb, int ydt) {
-    const GemmPlan g = gemm_plan(M, T, kb, ydt);
+size_t fp8_gemm_workspace(int64_t M, int64_t T, uint32_t kb, bool exact) {
+    const GemmPlan g = gemm_plan(M, T, kb, exact);
     return g.splits > 1 ? align256(size_t(g.splits) * size_t((M + 3) / 4 * 4) * size_t(T) * 4) : 0;
 }
 
 sketch_status launch_fp8_gemm(const Fp8Product& p, void* ws, hipStream_t st) {
-    const GemmPlan g = gemm_plan(p.M, p.T, p.kb, p.ydt);
+    const GemmPlan g = gemm_plan(p.M, p.T, p.kb, p.exact);
     const int64_t rows = 32 * g.fa, cols = 32 * g.fb;
     GemmArgs a{p, uint32_t((p.M + rows - 1) / rows), uint32_t((p.T + cols - 1) / cols), g.splits, static_cast<float*>(ws)};
     const int64_t tiles = int64_t(a.tiles_o) * a.tiles_t;
@@ -562,11 +562,15 @@ sketch_status launch_fp8_gemm(const Fp8Product& p, void* ws, hipStream_t st) {
     if (p.ydt == SKETCH_F32)
         return go(fp8_gemm_kernel<SKETCH_F32, true, 4, 4>, fp8_gemm_kernel<SKETCH_F32, true, 3, 4>,
                   fp8_gemm_kernel<SKETCH_F32, true, 4, 2>, fp8_add_kernel<SKETCH_F32>);
-    if (p.ydt == SKETCH_BF16)
-        return go(fp8_gemm_kernel<SKETCH_BF16, false, 4, 4>, fp8_gemm_kernel<SKETCH_BF16, false, 3, 4>,
-                  fp8_gemm_kernel<SKETCH_BF16, false, 4, 2>, fp8_add_kernel<SKETCH_BF16>);
-    return go(fp8_gemm_kernel<SKETCH_F16, false, 4, 4>, fp8_gemm_kernel<SKETCH_F16, false, 3, 4>,
-              fp8_gemm_kernel<SKETCH_F16, false, 4, 2>, fp8_add_kernel<SKETCH_F16>);
+    if (p.ydt == SKETCH_F16)
+        return go(fp8_gemm_kernel<SKETCH_F16, true, 4, 4>, fp8_gemm_kernel<SKETCH_F16, true, 3, 4>,
+                  fp8_gemm_kernel<SKETCH_F16, true, 4, 2>, fp8_add_kernel<SKETCH_F16>);
+    if (p.exact)
+        return go(fp8_gemm_kernel<SKETCH_BF16, true, 4, 4>, fp8_gemm_kernel<SKETCH_BF16, true, 3, 4>,
+                  fp8_gemm_kernel<SKETCH_BF16, true, 4, 2>, fp8_add_kernel<SKETCH_BF16>);
+    static_assert(SKETCH_FP8_EXACT_BATCH >= 64, "tiles of 64 tokens have float32 sums");
+    return go(fp8_gemm_kernel<SKETCH_BF16, false, 4, 4>, fp8_gemm_kernel<SKETCH_BF16, false, 3, 4>,
+              fp8_gemm_kernel<SKETCH_BF16, true, 4, 2>, fp8_add_kernel<SKETCH_BF16>);
 }
 
 }  // namespace sketch

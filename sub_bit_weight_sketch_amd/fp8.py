@@ -11,9 +11,11 @@ import functools
 
 import torch
 
-from . import OK, SketchError, _check, _ptr, _stream_handle, dtype_code, lib, sketch_encode_status
+from . import BF16, OK, SketchError, _check, _ptr, _stream_handle, dtype_code, lib, sketch_encode_status
 
 FP8_ROWS = 3                # x_dtype of rows that sketch_fp8_encode wrote
+FP8_F32_SUMS = 256          # with y_dtype BF16: float32 sums for any number of rows
+FP8_EXACT_BATCH = 64        # rows up to which a bfloat16 Y has them anyway
 MOE_MAX_EXPERTS, MOE_MAX_TOPK, MOE_MAX_TOKENS = 512, 16, 64
 FP8_EXPORTS = ("sketch_fp8_layout", "sketch_fp8_encode", "sketch_fp8_workspace_bytes", "sketch_fp8_matmul",
                "sketch_moe_workspace_bytes", "sketch_moe")
@@ -72,6 +74,11 @@ def sketch_fp8_encode(p, W, buf, status=None, stream=None):
            "sketch_fp8_encode")
 
 
+def _y_dtype(Y, float32_sums):
+    code = dtype_code(Y)
+    return code | FP8_F32_SUMS if float32_sums and code == BF16 else code
+
+
 def sketch_fp8_workspace_bytes(p, batch, x_dtype, y_dtype):
     n = ctypes.c_size_t()
     _check(_fp8_lib().sketch_fp8_workspace_bytes(ctypes.byref(p), int(batch), int(x_dtype), int(y_dtype),
@@ -79,11 +86,11 @@ def sketch_fp8_workspace_bytes(p, batch, x_dtype, y_dtype):
     return n.value
 
 
-def sketch_fp8_matmul(p, buf, X, x_dtype, batch, Y, workspace, stream=None):
+def sketch_fp8_matmul(p, buf, X, x_dtype, batch, Y, workspace, stream=None, float32_sums=False):
     stream = stream if stream is not None else _stream_handle(Y.device)
     wsb = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(_fp8_lib().sketch_fp8_matmul(ctypes.byref(p), _ptr(buf), _ptr(X), int(x_dtype), int(batch), _ptr(Y),
-                                        dtype_code(Y), _ptr(workspace), wsb, stream), "sketch_fp8_matmul")
+                                        _y_dtype(Y, float32_sums), _ptr(workspace), wsb, stream), "sketch_fp8_matmul")
 
 
 def sketch_moe_workspace_bytes(p, tokens):
@@ -248,7 +255,8 @@ def _workspace_bytes(t, batch, x_dtype, y_dtype):
 
 def fp8_workspace_for(t, batch, x_dtype, y_dtype, device):
     """Workspace for products of `batch` rows (None if not needed).  Reuse it
-    across calls on one stream, never for two calls in flight at once."""
+    across calls on one stream, never for two calls in flight at once.  y_dtype:
+    the code of Y's type, BF16 | FP8_F32_SUMS for float32_sums."""
     with _On(t.device):
         n = _workspace_bytes(t, batch, x_dtype, y_dtype)
     return torch.empty(n, dtype=torch.uint8, device=device) if n else None
@@ -268,12 +276,14 @@ def _out(out, shape, dtype, device):
     return out
 
 
-def fp8_matmul(t, X, out=None, workspace=None, dtype=None):
+def fp8_matmul(t, X, out=None, workspace=None, dtype=None, float32_sums=False):
     """Y = X8 . W8^T [batch, M] for an encoded weight t and X [batch, N] (or
     [N]), encoded row by row on the way in; X may also be an Fp8Tables with
     block_rows=1, for rows that several linears share.  dtype: of Y, float32
-    (the default, or that of `out`), bfloat16 or float16; see
-    include/sketch_fp8.h for how their sums differ."""
+    (the default, or that of `out`), bfloat16 or float16.  Sums are float32, but
+    for a bfloat16 Y of more than FP8_EXACT_BATCH rows, which is summed on the
+    e4m3 matrix cores (twice as fast; include/sketch_fp8.h states the error)
+    unless float32_sums is true."""
     if t.block_rows != 128 or t.count is not None:
         raise ValueError("t must be one weight, encoded with block_rows=128")
     rows = isinstance(X, Fp8Tables)
@@ -296,7 +306,7 @@ def fp8_matmul(t, X, out=None, workspace=None, dtype=None):
         dtype = torch.float32 if out is None else out.dtype
     with _On(device) as stream:
         Y = torch.empty(shape, dtype=dtype, device=device) if out is None else _out(out, shape, dtype, device)
-        ydt = dtype_code(Y)
+        ydt = _y_dtype(Y, float32_sums)
         if workspace is None:
             wsb = _workspace_bytes(t, batch, xdt, ydt)
             workspace = torch.empty(wsb, dtype=torch.uint8, device=device) if wsb else None
