@@ -83,6 +83,7 @@ sketch_status sketch_fp8_layout(const sketch_fp8_params* p, sketch_fp8_shape* sh
  * and scale byte is written, with the padding of their rows).
  *   status_dev  one device int32 that the kernel ORs SKETCH_FLAG_WEIGHT_RANGE
  *               into when some element is NaN or infinite, or NULL.
+ * SKETCH_EINVAL when W and buf share memory.
  */
 sketch_status sketch_fp8_encode(const sketch_fp8_params* p, const void* W, sketch_dtype w_dtype, void* buf,
                                 int32_t* status_dev, void* stream);
@@ -118,7 +119,11 @@ sketch_status sketch_fp8_workspace_bytes(const sketch_fp8_params* p, int64_t bat
  * SKETCH_FP8_F32_SUMS is the way around it.  A row of X that holds NaN or an
  * infinity gives a row of NaN in Y; other rows are unaffected.  batch == 0 or
  * M == 0 is a no-op.
+ * Y may share memory with X where X is encoded into the workspace first, that
+ * is with more than SKETCH_FP8_TOKENS rows that are not SKETCH_FP8_ROWS; any
+ * other overlap of Y or the workspace with another buffer gives SKETCH_EINVAL.
  */
+#define SKETCH_FP8_TOKENS 4
 sketch_status sketch_fp8_matmul(const sketch_fp8_params* p, const void* buf, const void* X, int x_dtype,
                                 int64_t batch, void* Y, int y_dtype, void* workspace,
                                 size_t workspace_bytes, void* stream);
@@ -154,7 +159,9 @@ sketch_status sketch_moe_workspace_bytes(const sketch_moe_params* p, int64_t tok
  *            experts by descending logit and their weights (overwritten).
  * A token with NaN or an infinity in x gives non-finite values in its row of
  * Y; other tokens are unaffected.  tokens == 0 is a no-op; tokens above the
- * limit give SKETCH_EINVAL.
+ * limit give SKETCH_EINVAL.  Y may share memory with X (all of X is read before
+ * any of Y is written); any other overlap of what is written or of the workspace
+ * with another buffer gives SKETCH_EINVAL.
  */
 sketch_status sketch_moe(const sketch_moe_params* p, const void* router, const void* gate, const void* up,
                          const void* down, const void* X, int64_t tokens, float* Y, int32_t* ids, float* weights,

@@ -442,7 +442,7 @@ def decode(t, dtype=torch.bfloat16, out=None, hashed=False):
 
 
 # 8-bit floating-point linears and the mixture-of-experts layer
-from .fp8 import (FP8_EXACT_BATCH, FP8_EXPORTS, FP8_F32_SUMS, FP8_ROWS, MOE_MAX_EXPERTS, MOE_MAX_TOKENS,  # noqa: E402
-                  MOE_MAX_TOPK, Fp8Params, Fp8Shape, Fp8Tables, MoE, MoEParams, fp8_encode, fp8_matmul, fp8_tables,
+from .fp8 import (FP8_EXACT_BATCH, FP8_EXPORTS, FP8_F32_SUMS, FP8_ROWS, FP8_TOKENS, MOE_MAX_EXPERTS,  # noqa: E402
+                  MOE_MAX_TOKENS, MOE_MAX_TOPK, Fp8Params, Fp8Shape, Fp8Tables, MoE, MoEParams, fp8_encode, fp8_matmul, fp8_tables,
                   fp8_workspace_for, moe, sketch_fp8_encode, sketch_fp8_layout, sketch_fp8_matmul,
                   sketch_fp8_workspace_bytes, sketch_moe, sketch_moe_workspace_bytes)

@@ -23,6 +23,19 @@ sketch_status fp8_shape(const sketch_fp8_params* p, sketch_fp8_shape* s);
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// Memory of a call, to refuse buffers that share it.
+struct Range {
+    const void* p;
+    size_t bytes;
+};
+
+inline bool overlap(const Range& a, const Range& b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return a.bytes > 0 && b.bytes > 0 && (x < y ? y - x < a.bytes : x - y < b.bytes);
+}
+
+inline size_t elem_bytes(int dtype) { return dtype == SKETCH_F32 ? 4 : 2; }
+
 // Compute units of the current device, asked for once per device (256 when
 // none answers).
 inline int compute_units() {

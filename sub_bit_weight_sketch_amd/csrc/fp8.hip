@@ -143,7 +143,7 @@ __global__ __launch_bounds__(256) void fp8_encode_rows_kernel(EncodeArgs a) {
 // ---------------------------------------------------------------------------
 constexpr int kWaves = 8;
 constexpr int kRun = 4;      // blocks of 128 columns in a wave's run
-constexpr int kTokens = 4;   // rows that fp8_tokens_kernel takes
+constexpr int kTokens = SKETCH_FP8_TOKENS;   // rows that fp8_tokens_kernel takes
 
 __device__ inline i32x8 load_frag(const uint8_t* lo, const uint8_t* hi) {
     return __builtin_shufflevector(*reinterpret_cast<const i32x4*>(lo), *reinterpret_cast<const i32x4*>(hi), 0, 1, 2,
@@ -381,6 +381,8 @@ sketch_status sketch_fp8_encode(const sketch_fp8_params* p, const void* W, sketc
     if (!valid_dtype(w_dtype) || (reinterpret_cast<uintptr_t>(status_dev) & 3u)) return SKETCH_EINVAL;
     if (p->M == 0) return SKETCH_OK;
     if (!W || !buf || !aligned16(W) || !aligned16(buf)) return SKETCH_EINVAL;
+    const size_t count = p->count > 1 ? size_t(p->count) : 1;
+    if (overlap({W, count * size_t(p->M) * size_t(p->N) * elem_bytes(w_dtype)}, {buf, count * s.bytes})) return SKETCH_EINVAL;
     return launch_fp8_encode(p, s, W, w_dtype, buf, status_dev, static_cast<hipStream_t>(stream));
 }
 
@@ -426,18 +428,24 @@ sketch_status sketch_fp8_matmul(const sketch_fp8_params* p, const void* buf, con
     (void)fp8_shape(&xp, &xs);
     const uint8_t *w8 = static_cast<const uint8_t*>(buf), *x8 = static_cast<const uint8_t*>(X);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    const bool encode = x_dtype != SKETCH_FP8_ROWS && batch > kTokens;
-    if (encode) {
-        rc = launch_fp8_encode(&xp, xs, X, sketch_dtype(x_dtype), ws, nullptr, st);
-        if (rc != SKETCH_OK) return rc;
-        x8 = ws;
-        ws += xs.bytes;
-    }
+    const bool rows = x_dtype == SKETCH_FP8_ROWS, encode = !rows && batch > kTokens;
     Fp8Product a{w8, w8 + s.scales_offset, x8, x8 + xs.scales_offset, Y, p->M, batch, s.ld, s.lds,
                  uint32_t(s.col_blocks), 0, true};
     (void)y_type(y_dtype, batch, &a.ydt, &a.exact);
+    // workgroups that are done store Y while others still read
+    const Range ry{Y, size_t(batch) * size_t(p->M) * elem_bytes(a.ydt)}, rw{buf, s.bytes}, rs{workspace, need},
+        rx{X, rows ? xs.bytes : size_t(batch) * size_t(p->N) * elem_bytes(x_dtype)};
+    if (overlap(ry, rw) || overlap(ry, rs) || (!encode && overlap(ry, rx)) || overlap(rs, rw) || overlap(rs, rx))
+        return SKETCH_EINVAL;
+    if (encode) {
+        rc = launch_fp8_encode(&xp, xs, X, sketch_dtype(x_dtype), ws, nullptr, st);
+        if (rc != SKETCH_OK) return rc;
+        a.x = ws;
+        a.xs = ws + xs.scales_offset;
+        ws += xs.bytes;
+    }
     if (batch > 16) return launch_fp8_gemm(a, ws, st);
-    return launch_few(a, encode ? int(SKETCH_FP8_ROWS) : x_dtype, p->N, st);
+    return launch_few(a, encode ? SKETCH_FP8_ROWS : x_dtype, p->N, st);
 }
 
 }  // extern "C"

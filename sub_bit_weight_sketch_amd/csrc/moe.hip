@@ -583,6 +583,14 @@ sketch_status sketch_moe(const sketch_moe_params* p, const void* router, const v
                           static_cast<const void*>(weights), static_cast<const void*>(workspace)})
         if (!q || !aligned16(q)) return SKETCH_EINVAL;
     if (workspace_bytes < L.total) return SKETCH_ESMALL;
+    const size_t T = size_t(tokens), E = size_t(p->E), H = size_t(p->H), es = elem_bytes(p->x_dtype);
+    const Range rx{X, T * H * es}, in[] = {{router, E * H * es}, {gate, E * L.gu.bytes}, {up, E * L.gu.bytes}, {down, E * L.d.bytes}},
+                out[] = {{Y, T * H * 4}, {ids, T * p->topk * 4}, {weights, T * p->topk * 4}, {workspace, L.total}};
+    for (int i = 0; i < 4; ++i) {
+        if (i > 0 && overlap(out[i], rx)) return SKETCH_EINVAL;   // Y is written when X is done with
+        for (int j = 0; j < 4; ++j)
+            if (overlap(out[i], in[j]) || (j < i && overlap(out[i], out[j]))) return SKETCH_EINVAL;
+    }
     const hipStream_t st = static_cast<hipStream_t>(stream);
     char* ws = static_cast<char*>(workspace);
     MoeArgs a;

@@ -16,6 +16,7 @@ from . import BF16, OK, SketchError, _check, _ptr, _stream_handle, dtype_code, l
 FP8_ROWS = 3                # x_dtype of rows that sketch_fp8_encode wrote
 FP8_F32_SUMS = 256          # with y_dtype BF16: float32 sums for any number of rows
 FP8_EXACT_BATCH = 64        # rows up to which a bfloat16 Y has them anyway
+FP8_TOKENS = 4              # rows that a product encodes as it reads them
 MOE_MAX_EXPERTS, MOE_MAX_TOPK, MOE_MAX_TOKENS = 512, 16, 64
 FP8_EXPORTS = ("sketch_fp8_layout", "sketch_fp8_encode", "sketch_fp8_workspace_bytes", "sketch_fp8_matmul",
                "sketch_moe_workspace_bytes", "sketch_moe")
@@ -276,6 +277,12 @@ def _out(out, shape, dtype, device):
     return out
 
 
+def _shared(a, b):
+    """Whether two dense tensors have bytes in common."""
+    p, q = a.data_ptr(), b.data_ptr()
+    return p < q + b.numel() * b.element_size() and q < p + a.numel() * a.element_size()
+
+
 def fp8_matmul(t, X, out=None, workspace=None, dtype=None, float32_sums=False):
     """Y = X8 . W8^T [batch, M] for an encoded weight t and X [batch, N] (or
     [N]), encoded row by row on the way in; X may also be an Fp8Tables with
@@ -283,7 +290,8 @@ def fp8_matmul(t, X, out=None, workspace=None, dtype=None, float32_sums=False):
     (the default, or that of `out`), bfloat16 or float16.  Sums are float32, but
     for a bfloat16 Y of more than FP8_EXACT_BATCH rows, which is summed on the
     e4m3 matrix cores (twice as fast; include/sketch_fp8.h states the error)
-    unless float32_sums is true."""
+    unless float32_sums is true.  `out` may share memory with X (of up to
+    FP8_TOKENS rows a copy is made), not with the weight or with encoded rows."""
     if t.block_rows != 128 or t.count is not None:
         raise ValueError("t must be one weight, encoded with block_rows=128")
     rows = isinstance(X, Fp8Tables)
@@ -300,6 +308,8 @@ def fp8_matmul(t, X, out=None, workspace=None, dtype=None, float32_sums=False):
         xdt, at = FP8_ROWS, X._at
     else:
         xdt, x = dtype_code(X), _aligned(X)
+        if out is not None and batch <= FP8_TOKENS and _shared(x, out):
+            x = x.clone()
         at = x.data_ptr()
     shape = (t.M,) if squeeze else (batch, t.M)
     if dtype is None:
@@ -370,7 +380,7 @@ def moe(layer, X, out=None, workspace=None, return_routing=False):
     """Y float32 [tokens, H] of a MoE layer for X [tokens, H] (up to
     MOE_MAX_TOKENS tokens, of the router's dtype); with return_routing also
     the chosen experts int32 [tokens, topk], by descending logit, and their
-    weights float32 [tokens, topk]."""
+    weights float32 [tokens, topk].  `out` may share memory with X."""
     shape, dev, k = X.shape, layer._device, layer._topk
     if len(shape) != 2 or shape[1] != layer._H:
         raise ValueError("X must be [tokens, %d]" % layer._H)
