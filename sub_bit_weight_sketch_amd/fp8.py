@@ -150,34 +150,41 @@ def _aligned(t):
 
 @functools.lru_cache(maxsize=1024)
 def _shape(M, N, block_rows, count):
-    """Parameters, their reference and the layout of one kind of buffer."""
+    """Parameters, their reference and the layout of one kind of buffer, shared
+    by all of it: never handed out."""
     p = Fp8Params(M, N, block_rows, count)
     return p, ctypes.byref(p), sketch_fp8_layout(p)
 
 
 class Fp8Tables:
     """A matrix [M, N] (or a stack [count, M, N]) as e4m3 codes and block
-    scales, in the buffer layout of the C ABI (a uint8 device tensor)."""
+    scales, in the buffer layout of the C ABI (a uint8 device tensor).  Its
+    values may be changed, its shape and buffer not: `params` and `layout` are
+    copies."""
 
     def __init__(self, M, N, block_rows=128, count=None, device="cuda", buf=None):
         if count is not None and count < 1:
             raise ValueError("an empty stack of matrices")
-        self.M, self.N, self.block_rows, self.count = int(M), int(N), int(block_rows), count
         stack = 1 if count is None else int(count)
-        self.params, self._ref, self.layout = _shape(self.M, self.N, self.block_rows, stack)
-        n = stack * self.layout.bytes
+        self._M, self._N, self._block_rows, self._count = int(M), int(N), int(block_rows), None if count is None else stack
+        self._params, self._ref, self._layout = _shape(self._M, self._N, self._block_rows, stack)
+        n = stack * self._layout.bytes
         if buf is None:
             buf = torch.empty(n, dtype=torch.uint8, device=device)
         else:
             _need(buf.dtype == torch.uint8 and buf.is_contiguous() and buf.numel() >= n and buf.data_ptr() % 16 == 0,
                   "the buffer must be %d dense, 16-byte aligned bytes" % n)
-        self._buf, self.device, self._at = buf, buf.device, buf.data_ptr()
+        self._buf, self._device, self._at = buf, buf.device, buf.data_ptr()
         self._ws = {}
 
-    @property
-    def buf(self):
-        """The buffer; its bytes may be changed, not the buffer."""
-        return self._buf
+    M = property(lambda self: self._M)
+    N = property(lambda self: self._N)
+    block_rows = property(lambda self: self._block_rows)
+    count = property(lambda self: self._count)
+    device = property(lambda self: self._device)
+    buf = property(lambda self: self._buf)
+    params = property(lambda self: Fp8Params.from_buffer_copy(self._params))
+    layout = property(lambda self: Fp8Shape.from_buffer_copy(self._layout))
 
     @property
     def shape(self):
@@ -185,16 +192,16 @@ class Fp8Tables:
 
     def _view(self, rows, cols, ld, at):
         if self.count is None:
-            return self.buf.as_strided((rows, cols), (ld, 1), self.buf.storage_offset() + at)
-        return self.buf.as_strided((self.count, rows, cols), (self.layout.bytes, ld, 1), self.buf.storage_offset() + at)
+            return self._buf.as_strided((rows, cols), (ld, 1), self._buf.storage_offset() + at)
+        return self._buf.as_strided((self._count, rows, cols), (self._layout.bytes, ld, 1), self._buf.storage_offset() + at)
 
     def codes(self):
         """The codes as a float8_e4m3fn view (rows are padded: not contiguous unless N % 128 == 0)."""
-        return self._view(self.M, self.N, self.layout.ld, 0).view(torch.float8_e4m3fn)
+        return self._view(self._M, self._N, self._layout.ld, 0).view(torch.float8_e4m3fn)
 
     def scales(self):
         """The biased scale exponents, uint8 [row blocks, column blocks] (a view): scale = 2^(byte - 127)."""
-        s = self.layout
+        s = self._layout
         return self._view(s.row_blocks, s.col_blocks, s.lds, s.scales_offset)
 
 
@@ -218,7 +225,7 @@ def fp8_encode(W, block_rows=128, check=True, status=None):
     with _On(W.device) as stream:
         if check and status is None:
             status = torch.zeros(1, dtype=torch.int32, device=W.device)
-        sketch_fp8_encode(t.params, W, t.buf, status, stream)
+        sketch_fp8_encode(t._params, W, t.buf, status, stream)
         if check:
             flags = int(status.item())
             rc = sketch_encode_status(flags)
@@ -238,10 +245,10 @@ def fp8_tables(codes, scales, block_rows=128):
           "codes and scales must be 2-D (or 3-D) tensors on one GPU")
     count = codes.shape[0] if codes.dim() == 3 else None
     t = Fp8Tables(codes.shape[-2], codes.shape[-1], block_rows, count, codes.device)
-    want = (t.layout.row_blocks, t.layout.col_blocks)
+    want = (t._layout.row_blocks, t._layout.col_blocks)
     _need(tuple(scales.shape) == (want if count is None else (count,) + want), "scales must have shape %s" % (want,))
     t.buf.zero_()
-    t._view(t.M, t.N, t.layout.ld, 0).copy_(codes)
+    t._view(t.M, t.N, t._layout.ld, 0).copy_(codes)
     t.scales().copy_(scales)
     return t
 
@@ -250,7 +257,7 @@ def _workspace_bytes(t, batch, x_dtype, y_dtype):
     key = (batch, x_dtype, y_dtype)
     n = t._ws.get(key)
     if n is None:
-        n = t._ws[key] = sketch_fp8_workspace_bytes(t.params, batch, x_dtype, y_dtype)
+        n = t._ws[key] = sketch_fp8_workspace_bytes(t._params, batch, x_dtype, y_dtype)
     return n
 
 
@@ -292,18 +299,18 @@ def fp8_matmul(t, X, out=None, workspace=None, dtype=None, float32_sums=False):
     e4m3 matrix cores (twice as fast; include/sketch_fp8.h states the error)
     unless float32_sums is true.  `out` may share memory with X (of up to
     FP8_TOKENS rows a copy is made), not with the weight or with encoded rows."""
-    if t.block_rows != 128 or t.count is not None:
+    if t._block_rows != 128 or t._count is not None:
         raise ValueError("t must be one weight, encoded with block_rows=128")
     rows = isinstance(X, Fp8Tables)
     if rows:
         _need(X.block_rows == 1 and X.count is None, "encoded rows must have block_rows=1")
-    shape, device = X.shape, t.device
+    shape, device = X.shape, t._device
     if X.device != device:
         raise ValueError("X and the weight are on different devices")
     squeeze = len(shape) == 1
     batch = 1 if squeeze else shape[0]
-    if len(shape) > 2 or shape[-1] != t.N:
-        raise ValueError("X must have %d columns, got shape %s" % (t.N, tuple(shape)))
+    if len(shape) > 2 or shape[-1] != t._N:
+        raise ValueError("X must have %d columns, got shape %s" % (t._N, tuple(shape)))
     if rows:
         xdt, at = FP8_ROWS, X._at
     else:
@@ -311,7 +318,7 @@ def fp8_matmul(t, X, out=None, workspace=None, dtype=None, float32_sums=False):
         if out is not None and batch <= FP8_TOKENS and _shared(x, out):
             x = x.clone()
         at = x.data_ptr()
-    shape = (t.M,) if squeeze else (batch, t.M)
+    shape = (t._M,) if squeeze else (batch, t._M)
     if dtype is None:
         dtype = torch.float32 if out is None else out.dtype
     with _On(device) as stream:
@@ -348,13 +355,14 @@ class MoE:
               "gate and up must be [E, I, H], down [E, H, I], the router [E, H]")
         self._tensors = _aligned(router), gate, up, down
         self._topk, self._renorm = int(topk), bool(renorm)
-        self.params = MoEParams(H, I, E, self._topk, int(self._renorm), dtype_code(router))
-        self._fixed = (ctypes.byref(self.params), self.router.data_ptr(), gate._at, up._at, down._at)
+        self._params = MoEParams(H, I, E, self._topk, int(self._renorm), dtype_code(router))
+        self._fixed = (ctypes.byref(self._params), self.router.data_ptr(), gate._at, up._at, down._at)
         self._H, self._dtype, self._device = H, router.dtype, router.device
-        sketch_moe_workspace_bytes(self.params, 0)   # checks the sizes
+        sketch_moe_workspace_bytes(self._params, 0)   # checks the sizes
         self._ws = {}
 
-    # a layer's values may be changed in place, its tensors and sizes not
+    # a layer's values may be changed in place, its tensors and sizes not (`params` is a copy)
+    params = property(lambda self: MoEParams.from_buffer_copy(self._params))
     router = property(lambda self: self._tensors[0])
     gate = property(lambda self: self._tensors[1])
     up = property(lambda self: self._tensors[2])
@@ -365,7 +373,7 @@ class MoE:
     def _workspace_bytes(self, tokens):
         n = self._ws.get(tokens)
         if n is None:
-            n = self._ws[tokens] = max(sketch_moe_workspace_bytes(self.params, tokens), 16)
+            n = self._ws[tokens] = max(sketch_moe_workspace_bytes(self._params, tokens), 16)
         return n
 
     def workspace_for(self, tokens):
