@@ -6,8 +6,6 @@
 // fragment be read without bank conflicts.  A fragment is 16 rows x 128
 // columns: lane l holds row l % 16 and the columns 16c..16c+15 and
 // 64+16c..64+16c+15, c = l / 16, the same ones in both operands.
-#include <utility>
-
 #include "fp8.h"
 
 namespace sketch {
@@ -329,9 +327,8 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 // two workgroups to a CU: for fewer tiles than the big kernel needs.  EXACT is as
 // above.  The loads of the next step go out first: between the MFMAs, as above,
 // they came too late for a step this short (4096 x 4096 at 2048 tokens 49 -> 53
-// us).  Loads two steps ahead, and widening between the MFMAs, changed nothing
-// (11008 x 4096 at 512 tokens in float32: 66, 68 and 66 us).  K is split over blockIdx.y when the
-// tiles alone leave compute units idle; the parts are float32, rows padded to 4
+// us).  Loads two steps ahead, and widening between the MFMAs, changed nothing.
+// K is split over blockIdx.y when the tiles alone leave compute units idle; the parts are float32, rows padded to 4
 // outputs, and fp8_add_kernel adds them in their order.
 // ---------------------------------------------------------------------------
 template <int FA, int FB> constexpr uint32_t mid_stage() { return (32 * FA + 32 * FB) * 128; }
@@ -478,41 +475,54 @@ struct GemmPlan {
     uint32_t splits;
 };
 
-constexpr int kSplitTo = 2;
+// What a product takes in us, by a model of the kernels: a block of 128 columns
+// takes a tile a time of its own, more where two workgroups share a compute
+// unit; tiles of the big kernel go in rounds over the units, each as long as two
+// blocks more to begin and end, the smaller ones follow one another, half a
+// round lost at the end; parts cost the launch that adds them and their way to
+// memory and back.  The figures are fitted to every kernel and split timed on
+// 512 products (58 x 20935 to 128256 x 2048, 17 to 70000 tokens): what the model
+// takes is 1.2% slower than the fastest one on average, at worst 20%; on 163
+// others that the fit has not seen 1.7%, at worst 30%.  (Tiles of 256 tokens
+// wherever they make 3/4 of a round, and parts by one figure for all kinds of
+// tiles, as simpler rules, took 10% more than the fastest on average, and
+// 28672 x 8192 in float32 at 17 tokens 112 us, now 59, 128256 x 2048 129 us, now 55.)
+struct TileCost {
+    int fa, fb;         // outputs and tokens of a tile, in units of 32
+    double one, two;    // us per block: a workgroup alone on its compute unit, or one of two
+};
+constexpr TileCost kCost[2][3] = {   // [exact]
+    {{4, 4, 0.83, 1.05}, {3, 4, 0.67, 0.85}, {4, 2, 0.56, 0.77}},
+    {{4, 4, 1.07, 1.70}, {3, 4, 0.92, 1.36}, {4, 2, 0.68, 1.04}}};
+constexpr TileCost kBigCost[2][3] = {{{8, 8, 1.50, 0}, {7, 8, 1.15, 0}, {6, 8, 1.01, 0}},
+                                     {{4, 8, 1.55, 0}, {3, 8, 1.24, 0}, {3, 8, 1.24, 0}}};
+constexpr int64_t kMaxSplits = 16, kNarrowTokens = 192;   // most tokens that tiles of 64 were timed with
 
 GemmPlan gemm_plan(int64_t M, int64_t T, uint32_t kb, bool exact) {
     const int64_t ncu = compute_units();
-    // rounds of the big kernel's tiles over the compute units, in units of 32 outputs
-    int64_t best = 0;
-    int big = 0;
-    for (int f : {8, 7, 6, 4, 3}) {
-        if ((f < 6) != exact) continue;
-        const int64_t tiles = (M + 32 * f - 1) / (32 * f) * ((T + 255) / 256), cost = (tiles + ncu - 1) / ncu * f;
-        if (tiles >= ncu * 3 / 4 && (big == 0 || cost < best)) best = cost, big = f;
-    }
-    if (big) return {true, big, 8, 1};
-    // K split over idle compute units, up to about two workgroups to each, into
-    // the number of parts that should take least: a block of 128 columns takes a
-    // workgroup about 0.75 us, adding the parts a launch (6 us with its gaps) and
-    // their way to memory and back (4096 x 1024 at 200 tokens: 14.8 us in 2
-    // parts, 11.7 us in one; 4096 x 4096 at 256: 25.5 us in 8, 23.7 us in 4, 35 us
-    // in one).
-    const int fb = T <= 64 ? 2 : 4;
-    auto plan = [&](int fa) {
-        const int64_t tiles = (M + 32 * fa - 1) / (32 * fa) * ((T + 32 * fb - 1) / (32 * fb));
-        const int64_t most = tiles >= ncu ? 1 : kSplitTo * ncu / tiles;
-        int64_t splits = 1;
-        double least = 0.75 * kb;
-        for (int64_t n = 2; n <= most && n <= kb / 4; ++n) {
-            const double us = 0.75 * double((kb + n - 1) / n) + 6.0 + 1e-6 * double(n * M * T);
-            if (us < least) least = us, splits = n;
-        }
-        const int64_t rounds = (tiles * splits + ncu - 1) / ncu;
-        return std::pair{GemmPlan{false, fa, fb, uint32_t(splits)}, double(rounds * fa) / double(splits)};
+    GemmPlan best{};
+    double least = 1e300;
+    auto consider = [&](const GemmPlan& g, double us) {
+        if (us < least) least = us, best = g;
     };
-    // 96 outputs to a tile where these take fewer rounds (11008 x 4096, 256 tokens: 37 us with 128, 34 us)
-    const auto four = plan(4), three = plan(3);
-    return fb == 4 && three.second < four.second ? three.first : four.first;
+    auto tiles_of = [&](const TileCost& c) { return (M + 32 * c.fa - 1) / (32 * c.fa) * ((T + 32 * c.fb - 1) / (32 * c.fb)); };
+    for (const TileCost& c : kBigCost[exact])
+        consider({true, c.fa, c.fb, 1}, (exact ? 3.9 : 5.8) + double((tiles_of(c) + ncu - 1) / ncu) * double(kb + 2) * c.one);
+    for (const TileCost& c : kCost[exact]) {
+        if (c.fb == 2 && T > kNarrowTokens) continue;
+        const int64_t tiles = tiles_of(c);
+        for (int64_t n = 1; n <= kMaxSplits; ++n) {
+            if (n > 1 && (2 * n > int64_t(kb) || tiles * n > 4 * ncu || T > 65535)) break;   // T: a grid's second dimension
+            const int64_t w = tiles * n, slots = 2 * ncu;
+            const double steps = double(kb) / double(n) + 0.5, rounds = double(w) / double(slots);
+            double us = 4.8 + steps * (w <= ncu     ? c.one
+                                       : w <= slots ? c.two
+                                                    : c.two * 0.5 * (rounds + double((w + slots - 1) / slots)));
+            if (n > 1) us += 1.3 + 1.5e-6 * double(n) * double(T) * double(M);
+            consider({false, c.fa, c.fb, uint32_t(n)}, us);
+        }
+    }
+    return best;
 }
 
 void launch_big(const GemmArgs& a, int fa, unsigned grid, hipStream_t st) {
@@ -568,9 +578,8 @@ sketch_status launch_fp8_gemm(const Fp8Product& p, void* ws, hipStream_t st) {
     if (p.exact)
         return go(fp8_gemm_kernel<SKETCH_BF16, true, 4, 4>, fp8_gemm_kernel<SKETCH_BF16, true, 3, 4>,
                   fp8_gemm_kernel<SKETCH_BF16, true, 4, 2>, fp8_add_kernel<SKETCH_BF16>);
-    static_assert(SKETCH_FP8_EXACT_BATCH >= 64, "tiles of 64 tokens have float32 sums");
     return go(fp8_gemm_kernel<SKETCH_BF16, false, 4, 4>, fp8_gemm_kernel<SKETCH_BF16, false, 3, 4>,
-              fp8_gemm_kernel<SKETCH_BF16, true, 4, 2>, fp8_add_kernel<SKETCH_BF16>);
+              fp8_gemm_kernel<SKETCH_BF16, false, 4, 2>, fp8_add_kernel<SKETCH_BF16>);
 }
 
 }  // namespace sketch
