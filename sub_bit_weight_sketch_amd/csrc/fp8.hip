@@ -309,9 +309,11 @@ sketch_status launch_few(const Fp8Product& p, int x_dtype, int64_t N, hipStream_
         return p.T == 1 ? tokens(fp8_tokens_kernel<SKETCH_BF16, 1>) : tokens(fp8_tokens_kernel<SKETCH_BF16, 4>);
     if (x_dtype == SKETCH_F16)
         return p.T == 1 ? tokens(fp8_tokens_kernel<SKETCH_F16, 1>) : tokens(fp8_tokens_kernel<SKETCH_F16, 4>);
-    // 32 outputs to a workgroup halve the reads of X (16 rows, 5000 x 28672: 61 us with 16 outputs, 48 us with 32;
-    // 8192 x 28672 68 and 57); where those of 16 all have a compute unit to themselves (4096 x 28672: 38 and 48), or a
-    // wave has but one run (11008 x 4096: 17.7 and 18.7), 16 have the shorter way
+    // 32 outputs to a workgroup halve the reads of X.  They pay from 64 outputs per compute unit on (16 rows, 16384 x
+    // 4096: 20.5 us with 16 outputs, 19.1 us with 32; 28672 x 8192 61.6 and 56.1; 128256 x 1024 41.1 and 35.8; at 5 rows
+    // 28672 x 8192 48.8 and 50.2), and below where a wave has several runs (16 rows, 5000 x 28672 61 and 48; 8192 x
+    // 28672 68 and 57).  With one run (11008 x 4096: 15.2 and 17.0), or where those of 16 all have a compute unit to
+    // themselves (4096 x 28672: 38 and 48), 16 have the shorter way.
     const int64_t ncu = compute_units();
     const bool two = p.M >= 64 * ncu || (p.M > 16 * ncu && p.kb > kWaves * kRun);
     return two ? rows(fp8_rows_kernel<2>, 32) : rows(fp8_rows_kernel<1>, 16);
