@@ -117,9 +117,22 @@ struct Fp8Product {
     bool exact;    // float32 sums
 };
 
-// Products of many rows (fp8_gemm.hip): scratch (parts of a split of K), launch.
-size_t fp8_gemm_workspace(int64_t M, int64_t T, uint32_t kb, bool exact);
-sketch_status launch_fp8_gemm(const Fp8Product& p, void* ws, hipStream_t st);
+// Threads that one dimension of a grid holds.
+constexpr int64_t kMaxThreads = 0xFFFFFFFF;
+
+// Products of many rows (fp8_gemm.hip): which kernel one takes, and over how
+// many workgroups K is split.
+struct GemmPlan {
+    bool big;          // fp8_gemm_big_kernel, or fp8_gemm_kernel
+    int fa, fb;        // outputs and tokens of a tile, in units of 32
+    uint32_t splits;
+    int64_t tiles_o, tiles_t;
+    size_t workspace;  // the parts of a split
+};
+
+// SKETCH_EINVAL when there are more tiles than a grid holds.
+sketch_status fp8_gemm_plan(int64_t M, int64_t T, uint32_t kb, bool exact, GemmPlan* g);
+sketch_status launch_fp8_gemm(const Fp8Product& p, const GemmPlan& g, void* ws, hipStream_t st);
 
 sketch_status launch_fp8_encode(const sketch_fp8_params* p, const sketch_fp8_shape& s, const void* W,
                                 sketch_dtype dt, void* buf, int32_t* status, hipStream_t st);

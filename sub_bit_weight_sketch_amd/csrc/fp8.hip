@@ -63,8 +63,9 @@ template <int DT>
 __global__ __launch_bounds__(256) void fp8_encode_kernel(EncodeArgs a) {
     __shared__ uint32_t red[4];
     const int tid = threadIdx.x;
-    const int64_t cb = blockIdx.x % a.lds, rb = (blockIdx.x / a.lds) % a.row_blocks,
-                  mat = blockIdx.x / a.lds / a.row_blocks;
+    const int64_t id = int64_t(blockIdx.y) * gridDim.x + blockIdx.x;
+    const int64_t cb = id % a.lds, rb = (id / a.lds) % a.row_blocks, mat = id / a.lds / a.row_blocks;
+    if (mat >= a.count) return;
     uint8_t* codes = a.buf + mat * a.bytes;
     uint8_t* scale = codes + a.scales_offset + rb * a.lds + cb;
     if (cb >= a.col_blocks) {   // scale bytes that round a row of scales up to a dword
@@ -105,7 +106,7 @@ __global__ __launch_bounds__(256) void fp8_encode_kernel(EncodeArgs a) {
 // Encoder of 1 x 128 blocks: 16 lanes per block, one block each.
 template <int DT>
 __global__ __launch_bounds__(256) void fp8_encode_rows_kernel(EncodeArgs a) {
-    const uint64_t id = uint64_t(blockIdx.x) * 16 + (threadIdx.x >> 4);   // (matrix, row, column block)
+    const uint64_t id = (uint64_t(blockIdx.y) * gridDim.x + blockIdx.x) * 16 + (threadIdx.x >> 4);   // (matrix, row, column block)
     const uint32_t lds = uint32_t(a.lds);
     const uint64_t grow = id / lds;
     const int64_t cb = int64_t(id - grow * lds), mat = int64_t(grow / uint64_t(a.M)), row = int64_t(grow) - mat * a.M;
@@ -334,6 +335,36 @@ bool y_type(int y_dtype, int64_t batch, int* type, bool* exact) {
     return valid_dtype(*type);
 }
 
+// What one product does and needs.
+struct ProductPlan {
+    sketch_fp8_shape w, x;   // the weight, the encoded rows
+    int ydt;
+    bool exact, encode;      // float32 sums; rows encoded by a launch of their own
+    GemmPlan gemm;           // more than 16 rows
+    size_t workspace;
+};
+
+// Checks the parameters (the rules of sketch_fp8_workspace_bytes) and fills the plan.
+sketch_status product_plan(const sketch_fp8_params* p, int64_t batch, int x_dtype, int y_dtype, ProductPlan* plan) {
+    sketch_status rc = fp8_shape(p, &plan->w);
+    if (rc != SKETCH_OK) return rc;
+    const bool rows = x_dtype == SKETCH_FP8_ROWS;
+    if (batch < 0 || p->block_rows != 128 || p->count > 1 || (!rows && !valid_dtype(x_dtype)) ||
+        !y_type(y_dtype, batch, &plan->ydt, &plan->exact))
+        return SKETCH_EINVAL;
+    const sketch_fp8_params xp{batch, p->N, 1, 1};
+    rc = fp8_shape(&xp, &plan->x);
+    if (rc != SKETCH_OK) return rc;
+    plan->workspace = 0;
+    if (batch == 0 || p->M == 0) return SKETCH_OK;
+    plan->encode = !rows && batch > kTokens;
+    if (plan->encode) plan->workspace += plan->x.bytes;
+    if (batch <= 16) return SKETCH_OK;
+    rc = fp8_gemm_plan(p->M, batch, uint32_t(plan->w.col_blocks), plan->exact, &plan->gemm);
+    plan->workspace += plan->gemm.workspace;
+    return rc;
+}
+
 }  // namespace
 
 sketch_status fp8_shape(const sketch_fp8_params* p, sketch_fp8_shape* s) {
@@ -354,10 +385,13 @@ sketch_status launch_fp8_encode(const sketch_fp8_params* p, const sketch_fp8_sha
     EncodeArgs a{W, static_cast<uint8_t*>(buf), status, p->M, p->N, s.ld, s.lds, s.row_blocks, s.col_blocks,
                  p->count > 1 ? p->count : 1, s.scales_offset, s.bytes};
     const bool rows = p->block_rows == 1;
-    const int64_t blocks = a.lds * a.row_blocks * a.count, grid = rows ? (blocks + 15) / 16 : blocks;
-    if (grid > 0x7FFFFFFF) return SKETCH_EINVAL;
+    const int64_t blocks = a.lds * a.row_blocks * a.count, groups = rows ? (blocks + 15) / 16 : blocks;
+    constexpr int64_t kLine = kMaxThreads / 256;
+    const int64_t lines = (groups + kLine - 1) / kLine;
+    if (lines > 65535) return SKETCH_EINVAL;
+    const dim3 grid(unsigned(lines > 1 ? kLine : groups), unsigned(lines));
     auto go = [&](auto kernel) {
-        kernel<<<unsigned(grid), 256, 0, st>>>(a);
+        kernel<<<grid, 256, 0, st>>>(a);
         return launch_status();
     };
     if (dt == SKETCH_F32) return rows ? go(fp8_encode_rows_kernel<SKETCH_F32>) : go(fp8_encode_kernel<SKETCH_F32>);
@@ -390,64 +424,47 @@ sketch_status sketch_fp8_encode(const sketch_fp8_params* p, const void* W, sketc
 
 sketch_status sketch_fp8_workspace_bytes(const sketch_fp8_params* p, int64_t batch, int x_dtype, int y_dtype,
                                          size_t* bytes) {
-    sketch_fp8_shape s, xs;
-    sketch_status rc = fp8_shape(p, &s);
+    ProductPlan plan;
+    const sketch_status rc = product_plan(p, batch, x_dtype, y_dtype, &plan);
     if (rc != SKETCH_OK) return rc;
-    int ydt;
-    bool exact;
-    if (!bytes || batch < 0 || p->block_rows != 128 || p->count > 1 || (!valid_dtype(x_dtype) && x_dtype != SKETCH_FP8_ROWS) ||
-        !y_type(y_dtype, batch, &ydt, &exact))
-        return SKETCH_EINVAL;
-    const sketch_fp8_params xp{batch, p->N, 1, 1};
-    rc = fp8_shape(&xp, &xs);
-    if (rc != SKETCH_OK) return rc;
-    *bytes = 0;
-    if (batch == 0 || p->M == 0) return SKETCH_OK;
-    if (x_dtype != SKETCH_FP8_ROWS && batch > kTokens) *bytes += xs.bytes;
-    if (batch > 16) *bytes += fp8_gemm_workspace(p->M, batch, uint32_t(s.col_blocks), exact);
+    if (!bytes) return SKETCH_EINVAL;
+    *bytes = plan.workspace;
     return SKETCH_OK;
 }
 
 sketch_status sketch_fp8_matmul(const sketch_fp8_params* p, const void* buf, const void* X, int x_dtype,
                                 int64_t batch, void* Y, int y_dtype, void* workspace,
                                 size_t workspace_bytes, void* stream) {
-    size_t need = 0;
-    sketch_status rc = sketch_fp8_workspace_bytes(p, batch, x_dtype, y_dtype, &need);
+    ProductPlan plan;
+    sketch_status rc = product_plan(p, batch, x_dtype, y_dtype, &plan);
     if (rc != SKETCH_OK) return rc;
     if (batch == 0 || p->M == 0) return SKETCH_OK;
+    const size_t need = plan.workspace;
     if (!buf || !X || !Y || !aligned16(buf) || !aligned16(X) || !aligned16(Y)) return SKETCH_EINVAL;
     if (need > 0) {
         if (!workspace || !aligned16(workspace)) return SKETCH_EINVAL;
         if (workspace_bytes < need) return SKETCH_ESMALL;
     }
-    // grids of the encoding and of the tiles, before either is launched
-    const int64_t kbs = (p->N + 127) / 128;
-    if (batch * ((kbs + 3) / 4) / 4 > 0x7FFFFFF0 || (p->M / 128 + 1) * (batch / 64 + 1) > 0x7FFFFFFF) return SKETCH_EINVAL;
+    // workgroups that are done store Y while others still read
+    const sketch_fp8_shape &s = plan.w, &xs = plan.x;
+    const Range ry{Y, size_t(batch) * size_t(p->M) * elem_bytes(plan.ydt)}, rw{buf, s.bytes}, rs{workspace, need},
+        rx{X, x_dtype == SKETCH_FP8_ROWS ? xs.bytes : size_t(batch) * size_t(p->N) * elem_bytes(x_dtype)};
+    if (overlap(ry, rw) || overlap(ry, rs) || (!plan.encode && overlap(ry, rx)) || overlap(rs, rw) || overlap(rs, rx))
+        return SKETCH_EINVAL;
     const hipStream_t st = static_cast<hipStream_t>(stream);
-    sketch_fp8_shape s, xs;
-    const sketch_fp8_params xp{batch, p->N, 1, 1};
-    (void)fp8_shape(p, &s);
-    (void)fp8_shape(&xp, &xs);
     const uint8_t *w8 = static_cast<const uint8_t*>(buf), *x8 = static_cast<const uint8_t*>(X);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    const bool rows = x_dtype == SKETCH_FP8_ROWS, encode = !rows && batch > kTokens;
-    Fp8Product a{w8, w8 + s.scales_offset, x8, x8 + xs.scales_offset, Y, p->M, batch, s.ld, s.lds,
-                 uint32_t(s.col_blocks), 0, true};
-    (void)y_type(y_dtype, batch, &a.ydt, &a.exact);
-    // workgroups that are done store Y while others still read
-    const Range ry{Y, size_t(batch) * size_t(p->M) * elem_bytes(a.ydt)}, rw{buf, s.bytes}, rs{workspace, need},
-        rx{X, rows ? xs.bytes : size_t(batch) * size_t(p->N) * elem_bytes(x_dtype)};
-    if (overlap(ry, rw) || overlap(ry, rs) || (!encode && overlap(ry, rx)) || overlap(rs, rw) || overlap(rs, rx))
-        return SKETCH_EINVAL;
-    if (encode) {
+    if (plan.encode) {
+        const sketch_fp8_params xp{batch, p->N, 1, 1};
         rc = launch_fp8_encode(&xp, xs, X, sketch_dtype(x_dtype), ws, nullptr, st);
         if (rc != SKETCH_OK) return rc;
-        a.x = ws;
-        a.xs = ws + xs.scales_offset;
+        x8 = ws;
         ws += xs.bytes;
     }
-    if (batch > 16) return launch_fp8_gemm(a, ws, st);
-    return launch_few(a, encode ? SKETCH_FP8_ROWS : x_dtype, p->N, st);
+    const Fp8Product a{w8, w8 + s.scales_offset, x8, x8 + xs.scales_offset, Y, p->M, batch, s.ld, s.lds,
+                       uint32_t(s.col_blocks), plan.ydt, plan.exact};
+    if (batch > 16) return launch_fp8_gemm(a, plan.gemm, ws, st);
+    return launch_few(a, plan.encode ? SKETCH_FP8_ROWS : x_dtype, p->N, st);
 }
 
 }  // extern "C"

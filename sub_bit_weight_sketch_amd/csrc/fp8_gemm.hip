@@ -468,13 +468,6 @@ __global__ __launch_bounds__(256) void fp8_add_kernel(GemmArgs a) {
     store4<YD>(a.p.Y, t * a.p.M + m, sum, m, a.p.M, a.p.M % 4 == 0);
 }
 
-// Which kernel a product takes, and over how many workgroups K is split.
-struct GemmPlan {
-    bool big;          // fp8_gemm_big_kernel, or fp8_gemm_kernel
-    int fa, fb;        // outputs and tokens of a tile, in units of 32
-    uint32_t splits;
-};
-
 // What a product takes in us, by a model of the kernels: a block of 128 columns
 // takes a tile a time of its own, more where two workgroups share a compute
 // unit; tiles of the big kernel go in rounds over the units, each as long as two
@@ -498,7 +491,7 @@ constexpr TileCost kBigCost[2][3] = {{{8, 8, 1.50, 0}, {7, 8, 1.15, 0}, {6, 8, 1
                                      {{4, 8, 1.55, 0}, {3, 8, 1.24, 0}, {3, 8, 1.24, 0}}};
 constexpr int64_t kMaxSplits = 16, kNarrowTokens = 192;   // most tokens that tiles of 64 were timed with
 
-GemmPlan gemm_plan(int64_t M, int64_t T, uint32_t kb, bool exact) {
+GemmPlan choose(int64_t M, int64_t T, uint32_t kb, bool exact) {
     const int64_t ncu = compute_units();
     GemmPlan best{};
     double least = 1e300;
@@ -507,7 +500,7 @@ GemmPlan gemm_plan(int64_t M, int64_t T, uint32_t kb, bool exact) {
     };
     auto tiles_of = [&](const TileCost& c) { return (M + 32 * c.fa - 1) / (32 * c.fa) * ((T + 32 * c.fb - 1) / (32 * c.fb)); };
     for (const TileCost& c : kBigCost[exact])
-        consider({true, c.fa, c.fb, 1}, (exact ? 3.9 : 5.8) + double((tiles_of(c) + ncu - 1) / ncu) * double(kb + 2) * c.one);
+        consider({true, c.fa, c.fb, 1, 0, 0, 0}, (exact ? 3.9 : 5.8) + double((tiles_of(c) + ncu - 1) / ncu) * double(kb + 2) * c.one);
     for (const TileCost& c : kCost[exact]) {
         if (c.fb == 2 && T > kNarrowTokens) continue;
         const int64_t tiles = tiles_of(c);
@@ -519,7 +512,7 @@ GemmPlan gemm_plan(int64_t M, int64_t T, uint32_t kb, bool exact) {
                                        : w <= slots ? c.two
                                                     : c.two * 0.5 * (rounds + double((w + slots - 1) / slots)));
             if (n > 1) us += 1.3 + 1.5e-6 * double(n) * double(T) * double(M);
-            consider({false, c.fa, c.fb, uint32_t(n)}, us);
+            consider({false, c.fa, c.fb, uint32_t(n), 0, 0, 0}, us);
         }
     }
     return best;
@@ -541,17 +534,18 @@ void launch_big(const GemmArgs& a, int fa, unsigned grid, hipStream_t st) {
 
 }  // namespace
 
-size_t fp8_gemm_workspace(int64_t M, int64_t T, uint32_t kb, bool exact) {
-    const GemmPlan g = gemm_plan(M, T, kb, exact);
-    return g.splits > 1 ? align256(size_t(g.splits) * size_t((M + 3) / 4 * 4) * size_t(T) * 4) : 0;
+sketch_status fp8_gemm_plan(int64_t M, int64_t T, uint32_t kb, bool exact, GemmPlan* g) {
+    *g = choose(M, T, kb, exact);
+    const int64_t rows = 32 * g->fa, cols = 32 * g->fb;
+    g->tiles_o = (M + rows - 1) / rows;
+    g->tiles_t = (T + cols - 1) / cols;
+    g->workspace = g->splits > 1 ? align256(size_t(g->splits) * size_t((M + 3) / 4 * 4) * size_t(T) * 4) : 0;
+    return g->tiles_o * g->tiles_t > kMaxThreads / (g->big ? 512 : 256) ? SKETCH_EINVAL : SKETCH_OK;
 }
 
-sketch_status launch_fp8_gemm(const Fp8Product& p, void* ws, hipStream_t st) {
-    const GemmPlan g = gemm_plan(p.M, p.T, p.kb, p.exact);
-    const int64_t rows = 32 * g.fa, cols = 32 * g.fb;
-    GemmArgs a{p, uint32_t((p.M + rows - 1) / rows), uint32_t((p.T + cols - 1) / cols), g.splits, static_cast<float*>(ws)};
-    const int64_t tiles = int64_t(a.tiles_o) * a.tiles_t;
-    if (tiles > 0x7FFFFFFF) return SKETCH_EINVAL;
+sketch_status launch_fp8_gemm(const Fp8Product& p, const GemmPlan& g, void* ws, hipStream_t st) {
+    const GemmArgs a{p, uint32_t(g.tiles_o), uint32_t(g.tiles_t), g.splits, static_cast<float*>(ws)};
+    const int64_t tiles = g.tiles_o * g.tiles_t;
     if (g.big) {
         launch_big(a, g.fa, unsigned(tiles), st);
         return launch_status();
