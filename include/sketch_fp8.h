@@ -138,7 +138,9 @@ sketch_status sketch_fp8_matmul(const sketch_fp8_params* p, const void* buf, con
  * G, U, D are encoded weights (block_rows 128), one buffer each with
  * count = E: the layouts of {I, H, 128, E} twice and of {H, I, 128, E}.  x and
  * h are not rounded to 8 bits: float32 sums of exact products with x in its
- * own precision and h in float32.
+ * own precision and h in float32.  They go to the matrix cores as up to three
+ * parts of 8 bits, of which those below 2^-126 may count as zero: float32 values
+ * below 2^-110 lose their last bits (1e-5 of them at 2^-116, 1e-4 at 2^-120).
  */
 typedef struct {
     int64_t H, I;          /* hidden size, expert size */
