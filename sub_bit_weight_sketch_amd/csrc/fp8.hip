@@ -327,7 +327,7 @@ bool valid_dtype(int d) { return d == SKETCH_F32 || d == SKETCH_BF16 || d == SKE
 // cores' sums (up to 5e-5); that to binary16 (2.1e-4) does not, and up to
 // SKETCH_FP8_EXACT_BATCH rows the product is bound by its bytes and gains
 // nothing to speak of (11008 x 4096 at 64 rows 23.1 us either way; 28672 x 8192
-// at 2048 rows 364 us, with float32 sums 760 us).
+// at 2048 rows 364 us, with float32 sums 740 us).
 bool y_type(int y_dtype, int64_t batch, int* type, bool* exact) {
     const bool asked = y_dtype == (SKETCH_BF16 | SKETCH_FP8_F32_SUMS);
     *type = asked ? int(SKETCH_BF16) : y_dtype;
