@@ -10,7 +10,9 @@ The C ABI (``include/sketch.h``) has the same names:
 ``sketch_matmul_group``, ``sketch_decode``, ``sketch_decode_hashed``,
 ``sketch_block_importance``, ``sketch_alloc_plan``, ``sketch_status_str``.
 The 8-bit floating-point linears and the mixture-of-experts layer
-(``include/sketch_fp8.h``) are bound in ``fp8.py`` and re-exported here.
+(``include/sketch_fp8.h``) are bound in ``fp8.py``, the 8-bit integer linears and
+their products grouped by expert (``include/sketch_int8.h``) in ``int8.py``; both
+are re-exported here.
 
 High-level use::
 
@@ -446,3 +448,10 @@ from .fp8 import (FP8_EXACT_BATCH, FP8_EXPORTS, FP8_F32_SUMS, FP8_ROWS, FP8_TOKE
                   MOE_MAX_TOKENS, MOE_MAX_TOPK, Fp8Params, Fp8Shape, Fp8Tables, MoE, MoEParams, fp8_encode, fp8_matmul, fp8_tables,
                   fp8_workspace_for, moe, sketch_fp8_encode, sketch_fp8_layout, sketch_fp8_matmul,
                   sketch_fp8_workspace_bytes, sketch_moe, sketch_moe_workspace_bytes)
+
+# 8-bit integer linears and their products grouped by expert
+from .int8 import (INT8_EXPORTS, INT8_MAX_EXPERTS, INT8_MAX_M, INT8_MAX_N, INT8_ROWS, INT8_TOKENS, Int8Groups,  # noqa: E402
+                   Int8Params, Int8Shape, Int8Tables, int8_encode, int8_group_workspace_for, int8_matmul,
+                   int8_matmul_group, int8_swiglu, int8_tables, int8_workspace_for, sketch_int8_encode,
+                   sketch_int8_group_workspace_bytes, sketch_int8_layout, sketch_int8_matmul, sketch_int8_matmul_group,
+                   sketch_int8_swiglu, sketch_int8_workspace_bytes)

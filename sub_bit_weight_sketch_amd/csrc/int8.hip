@@ -1,0 +1,527 @@
+// int8.hip -- matrices held as 8-bit integers with a float32 scale for each
+// row: their encoders, and the products Y = X8 * W8^T of few rows, for one weight
+// or for a stack of them with the rows grouped by expert.
+#include "int8.h"
+
+namespace sketch {
+namespace {
+
+// ---------------------------------------------------------------------------
+// Rounding.  A code is the integer next to 127 x / amax, ties to even, of the
+// exact quotient.  In b significant bits such a quotient is either the middle of
+// two integers or at least 2^-(b + 8) of its size away from it: with x and amax
+// integers X, A < 2^b (times a power of two) it differs from k + 1/2 by a multiple
+// of 1 / (2 A).  So a quotient known well enough is rounded right once it is
+// first brought to a grid that holds every middle and is finer than that distance.
+// 16-bit types (b <= 11): the float32 product x * (127 / amax) is off by 2 steps
+// of its last place at most; the grid is 8 of them, middles are 16 or more away.
+// float32 (b = 24): in float64, on a grid of 2^-40 (middles: 2^-33 away, error
+// 2^-45).
+// ---------------------------------------------------------------------------
+constexpr float kTiny = 7.88860905e-31f;   // 2^-100: below it 127 / amax may pass float32's range
+constexpr double kGrid = 6144.0;           // 1.5 * 2^12: a float64 beside it has steps of 2^-40
+
+__device__ inline int code64(double x, double inv) {
+    const double q = __builtin_fma(x, inv, kGrid) - kGrid;
+    return int(__builtin_rint(q));
+}
+
+template <int DT>
+struct Rounder {   // 16-bit types
+    float pre, inv;
+    __device__ explicit Rounder(float amax) {
+        pre = amax < kTiny ? 18446744073709551616.0f : 1.0f;   // 2^64
+        inv = 127.0f / (amax * pre);
+    }
+    __device__ int code(float x) const {
+        const float q = x * pre * inv;
+        return int(__builtin_rintf(__uint_as_float((__float_as_uint(q) + 4u) & ~7u)));
+    }
+};
+
+template <>
+struct Rounder<SKETCH_F32> {
+    double inv;
+    __device__ explicit Rounder(float amax) : inv(127.0 / double(amax)) {}
+    __device__ int code(float x) const { return code64(double(x), inv); }
+};
+
+__device__ inline uint32_t pack4(const int (&q)[8], int at) {
+    return uint32_t(q[at] & 255) | uint32_t(q[at + 1] & 255) << 8 | uint32_t(q[at + 2] & 255) << 16 | uint32_t(q[at + 3]) << 24;
+}
+
+__device__ inline uint32_t max_bits(const float (&v)[8]) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(v[e]) & 0x7FFFFFFFu);
+    return m;
+}
+
+template <int DT>
+__device__ inline uint2 codes8(const float (&v)[8], const Rounder<DT>& r) {
+    int q[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) q[e] = r.code(v[e]);
+    return make_uint2(pack4(q, 0), pack4(q, 4));
+}
+
+// Maximum over L lanes of a workgroup's row: a wave, or all four of them.
+template <int L, typename T, typename Max>
+__device__ inline T row_max(T m, T* red, Max larger) {
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) m = larger(m, __shfl_xor(m, d));
+    if constexpr (L == 256) {
+        __syncthreads();   // the last one's readers are done
+        if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
+        __syncthreads();
+        m = larger(larger(red[0], red[1]), larger(red[2], red[3]));
+    }
+    return m;
+}
+
+struct EncodeArgs {
+    const void *a, *b;        // the matrix, or gate and up
+    int64_t lda, ldb;
+    uint8_t* buf;
+    int32_t* status;
+    int64_t M, N, ld, rows;   // rows of all matrices
+    size_t scales_offset, bytes;
+};
+
+// SwiGLU of 8 elements in float32.  exp(-g) by a product in two parts, so that
+// the error is that of a few roundings (h: under 6e-7 of its size); `rough` is set
+// where that does not hold: far negative gates, and values past float32's range.
+__device__ inline void swiglu8(const float (&g)[8], const float (&u)[8], float (&h)[8], bool& rough) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        constexpr float kLog2e = 1.44269502162933349609375f, kLog2eLow = 1.92596299112661746887e-8f;
+        const float t = -g[e] * kLog2e;
+        const float low = __builtin_fmaf(-g[e], kLog2e, -t) - g[e] * kLog2eLow;   // what t lacks
+        const float ex = __builtin_amdgcn_exp2f(t) * __builtin_fmaf(low, 0.693147182f, 1.0f);
+        h[e] = g[e] * __builtin_amdgcn_rcpf(1.0f + ex) * u[e];
+        rough |= !(g[e] > -80.0f && fabsf(g[e]) < 3.0e38f && fabsf(h[e]) < 3.0e38f);
+    }
+}
+
+__device__ inline double swiglu64(float g, float u) { return double(g) / (1.0 + exp(-double(g))) * double(u); }
+
+// One row to L lanes (a workgroup of 256 has 256 / L rows), 8 elements to a
+// lane at a time; kKept such chunks of a lane stay in registers between the
+// maximum and the rounding, what a longer row has more is read again.
+// HBM-bound.
+constexpr int kKept = 4;
+
+template <int DT, int L>
+__global__ __launch_bounds__(256) void int8_encode_kernel(EncodeArgs a) {
+    __shared__ uint32_t red[4];
+    const int at = threadIdx.x & (L - 1);
+    const int64_t row = (int64_t(blockIdx.y) * gridDim.x + blockIdx.x) * (256 / L) + threadIdx.x / L;
+    if (row >= a.rows) return;   // a whole wave, or the whole workgroup
+    const int64_t mat = row / a.M, m = row - mat * a.M;
+    constexpr int es = DT == SKETCH_F32 ? 4 : 2;
+    const char* W = static_cast<const char*>(a.a) + row * a.lda * es;
+    uint8_t* buf = a.buf + mat * a.bytes;
+    const int chunks = int(a.ld / 8);
+    float v[kKept][8];
+    uint32_t bits = 0;
+#pragma unroll
+    for (int i = 0; i < kKept; ++i) {
+        if (at + i * L < chunks) {
+            load_row8<DT>(W, 0, a.N, (at + i * L) * 8, v[i]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[i][e] = 0.0f;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kKept; ++i) bits = max(bits, max_bits(v[i]));
+    for (int c = at + kKept * L; c < chunks; c += L) {
+        float x[8];
+        load_row8<DT>(W, 0, a.N, int64_t(c) * 8, x);
+        bits = max(bits, max_bits(x));
+    }
+    bits = row_max<L>(bits, red, [](uint32_t x, uint32_t y) { return max(x, y); });
+    const bool bad = bits >= 0x7F800000u;
+    const float amax = bad || bits == 0 ? 1.0f : __uint_as_float(bits);
+    const Rounder<DT> r(amax);
+    uint8_t* codes = buf + m * a.ld;
+    auto put = [&](int c, const float (&x)[8]) {
+        *reinterpret_cast<uint2*>(codes + int64_t(c) * 8) = bad ? make_uint2(0, 0) : codes8<DT>(x, r);
+    };
+#pragma unroll
+    for (int i = 0; i < kKept; ++i)
+        if (at + i * L < chunks) put(at + i * L, v[i]);
+    for (int c = at + kKept * L; c < chunks; c += L) {
+        float x[8];
+        load_row8<DT>(W, 0, a.N, int64_t(c) * 8, x);
+        put(c, x);
+    }
+    if (at == 0) {
+        reinterpret_cast<float*>(buf + a.scales_offset)[m] = bad ? __builtin_nanf("") : bits == 0 ? 0.0f : amax / 127.0f;
+        if (a.status && bad) atomicOr(a.status, SKETCH_FLAG_WEIGHT_RANGE);
+    }
+}
+
+// The same of h = silu(gate) * up.  The float32 h decides the codes where it
+// is clear of the middle of two integers (1.2e-4 of a code; its error is under
+// 7.5e-5), float64 the others, one in 4000; the largest magnitude is that of float64
+// among the elements within 2e-6 of the largest in float32.  Rows that float32
+// cannot hold (rough, or tiny) are computed in float64 throughout.
+template <int DT, int L>
+__global__ __launch_bounds__(256) void int8_swiglu_kernel(EncodeArgs a) {
+    __shared__ uint32_t red[4];
+    __shared__ double red64[4];
+    const int at = threadIdx.x & (L - 1);
+    const int64_t row = (int64_t(blockIdx.y) * gridDim.x + blockIdx.x) * (256 / L) + threadIdx.x / L;
+    if (row >= a.rows) return;
+    constexpr int es = DT == SKETCH_F32 ? 4 : 2;
+    const char *G = static_cast<const char*>(a.a) + row * a.lda * es, *U = static_cast<const char*>(a.b) + row * a.ldb * es;
+    const int chunks = int(a.ld / 8);
+    auto load = [&](int c, float (&g)[8], float (&u)[8]) {   // past the row's end: zeros
+        load_row8<DT>(G, 0, a.N, int64_t(c) * 8, g);
+        load_row8<DT>(U, 0, a.N, int64_t(c) * 8, u);
+    };
+    bool rough = false;
+    uint32_t bits = 0;
+    for (int c = at; c < chunks; c += L) {
+        float g[8], u[8], h[8];
+        load(c, g, u);
+        swiglu8(g, u, h, rough);
+        bits = max(bits, max_bits(h));
+    }
+    if (rough) bits = 0x7FFFFFFFu;
+    auto umax = [](uint32_t x, uint32_t y) { return max(x, y); };
+    auto dmax = [](double x, double y) { return x > y || x != x ? x : y; };   // NaN wins
+    bits = row_max<L>(bits, red, umax);
+    const bool whole = bits >= 0x7F800000u || bits < __float_as_uint(kTiny);
+    const float near = whole ? 0.0f : __uint_as_float(bits) * (1.0f - 2e-6f);
+    double big = 0.0;
+    for (int c = at; c < chunks; c += L) {
+        float g[8], u[8], h[8] = {};
+        load(c, g, u);
+        if (!whole) swiglu8(g, u, h, rough);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (whole || fabsf(h[e]) >= near) big = dmax(fabs(swiglu64(g[e], u[e])), big);
+    }
+    big = row_max<L>(big, red64, dmax);
+    const float scale = float(big / 127.0);
+    const bool bad = !(fabs(big) <= 3.4028234663852886e38);   // NaN too
+    const double inv = bad || big == 0.0 ? 0.0 : 127.0 / big;
+    const float inv32 = float(inv);
+    uint8_t* codes = a.buf + row * a.ld;
+    for (int c = at; c < chunks; c += L) {
+        float g[8], u[8], h[8] = {};
+        load(c, g, u);
+        if (!whole) swiglu8(g, u, h, rough);
+        int q[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float v = h[e] * inv32, near_int = __builtin_rintf(v);
+            q[e] = int(near_int);
+            if (whole || fabsf(v - near_int) > 0.5f - 1.2e-4f) q[e] = bad ? 0 : code64(swiglu64(g[e], u[e]), inv);
+        }
+        *reinterpret_cast<uint2*>(codes + int64_t(c) * 8) = make_uint2(pack4(q, 0), pack4(q, 4));
+    }
+    if (at == 0) {
+        reinterpret_cast<float*>(a.buf + a.scales_offset)[row] = bad ? __builtin_nanf("") : scale;
+        if (a.status && bad) atomicOr(a.status, SKETCH_FLAG_WEIGHT_RANGE);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Product of up to 16 terms at a time: 16 outputs to a workgroup, whose 8
+// waves share out the columns in runs of 4 blocks of 128.  A fragment is 16 rows
+// x 128 columns, one row to a lane: lane l holds row l % 16 and the columns
+// 16c..16c+15 and 64+16c..64+16c+15, c = l / 16, the same ones of outputs (A)
+// and terms (B).  D: term l % 16, outputs 4c..4c+3.
+// ---------------------------------------------------------------------------
+constexpr int kWaves = 8;
+constexpr int kRun = 4;
+
+struct Frag {
+    i32x4 lo, hi;
+    __device__ inline void load(const int8_t* row, uint32_t block, int c) {
+        const int8_t* at = row + size_t(block) * 128 + 16 * c;
+        lo = *reinterpret_cast<const i32x4*>(at);
+        hi = *reinterpret_cast<const i32x4*>(at + 64);
+    }
+};
+
+__device__ inline i32x4 multiply(const Frag& a, const Frag& b, i32x4 acc) {
+    acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(a.lo, b.lo, acc, 0, 0, 0);
+    return __builtin_amdgcn_mfma_i32_16x16x64_i8(a.hi, b.hi, acc, 0, 0, 0);
+}
+
+__device__ inline void store_y(const Int8Product& p, int64_t t, int64_t m, float v) {
+    const int64_t e = t * p.M + m;
+    if (p.ydt == SKETCH_F32)
+        store1_val<SKETCH_F32>(p.Y, e, v);
+    else if (p.ydt == SKETCH_BF16)
+        store1_val<SKETCH_BF16>(p.Y, e, v);
+    else
+        store1_val<SKETCH_F16>(p.Y, e, v);
+}
+
+template <bool GROUP>
+__global__ __launch_bounds__(kWaves * 64) void int8_rows_kernel(Int8Product p) {
+    __shared__ int part[kWaves][16][17];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int r = lane & 15, c = lane >> 4;
+    const int64_t tiles_o = (p.M + 15) / 16;
+    const int64_t id = int64_t(blockIdx.y) * gridDim.x + blockIdx.x, tile = id / tiles_o, m0 = (id - tile * tiles_o) * 16;
+    Terms t{0, int(tile * 16), int(min(int64_t(16), p.T - tile * 16))};
+    if (GROUP ? !find_terms<16>(p, int(tile), t) : t.n <= 0) return;
+    const int8_t* w = p.w + size_t(t.expert) * p.w_bytes;
+    const int8_t* wrow = w + min(m0 + r, p.M - 1) * p.ld;
+    const int64_t term = t.first + min(r, t.n - 1);
+    const int64_t row = GROUP ? term_row(p, term) : term;
+    const int8_t* xrow = p.x + (row < 0 ? 0 : row) * p.ld;
+    i32x4 acc = {0, 0, 0, 0};
+    for (uint32_t k = wave * kRun; k < p.kb; k += kWaves * kRun) {
+        Frag a[kRun], b[kRun];
+#pragma unroll
+        for (int u = 0; u < kRun; ++u) {
+            a[u].load(wrow, min(k + u, p.kb - 1), c);
+            b[u].load(xrow, min(k + u, p.kb - 1), c);
+        }
+#pragma unroll
+        for (int u = 0; u < kRun; ++u)
+            if (k + u < p.kb) acc = multiply(a[u], b[u], acc);
+    }
+#pragma unroll
+    for (int v = 0; v < 4; ++v) part[wave][r][4 * c + v] = acc[v];
+    __syncthreads();
+    const int m = tid & 15, n = tid >> 4;
+    if (n >= t.n || m0 + m >= p.M) return;
+    int sum = 0;
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) sum += part[i][n][m];
+    const int64_t from = GROUP ? term_row(p, t.first + n) : t.first + n;
+    const float sx = from < 0 ? __builtin_nanf("") : p.xs[from];
+    store_y(p, t.first + n, m0 + m, int8_value(sum, sx, reinterpret_cast<const float*>(w + p.w_scales)[m0 + m]));
+}
+
+bool valid_dtype(int d) { return d == SKETCH_F32 || d == SKETCH_BF16 || d == SKETCH_F16; }
+
+// A grid of `groups` workgroups of `threads` threads, over two dimensions where
+// one does not hold them; false past that.
+bool grid_of(int64_t groups, int threads, dim3* grid) {
+    const int64_t line = kMaxThreads / threads, lines = (groups + line - 1) / line;
+    if (lines > 65535) return false;
+    *grid = dim3(unsigned(lines > 1 ? line : groups), unsigned(lines));
+    return true;
+}
+
+sketch_status launch_encode8(const EncodeArgs& a, int dt, bool swiglu, hipStream_t st) {
+    dim3 grid;
+    // a wave to a row up to 2048 columns, which it keeps
+    const bool narrow = a.ld <= 64 * 8 * kKept;
+    if (!grid_of(narrow ? (a.rows + 3) / 4 : a.rows, 256, &grid)) return SKETCH_EINVAL;
+    auto go = [&](auto one, auto all) {
+        if (narrow)
+            one<<<grid, 256, 0, st>>>(a);
+        else
+            all<<<grid, 256, 0, st>>>(a);
+        return launch_status();
+    };
+    if (swiglu) {
+        if (dt == SKETCH_F32) return go(int8_swiglu_kernel<SKETCH_F32, 64>, int8_swiglu_kernel<SKETCH_F32, 256>);
+        if (dt == SKETCH_BF16) return go(int8_swiglu_kernel<SKETCH_BF16, 64>, int8_swiglu_kernel<SKETCH_BF16, 256>);
+        return go(int8_swiglu_kernel<SKETCH_F16, 64>, int8_swiglu_kernel<SKETCH_F16, 256>);
+    }
+    if (dt == SKETCH_F32) return go(int8_encode_kernel<SKETCH_F32, 64>, int8_encode_kernel<SKETCH_F32, 256>);
+    if (dt == SKETCH_BF16) return go(int8_encode_kernel<SKETCH_BF16, 64>, int8_encode_kernel<SKETCH_BF16, 256>);
+    return go(int8_encode_kernel<SKETCH_F16, 64>, int8_encode_kernel<SKETCH_F16, 256>);
+}
+
+int64_t matrices(const sketch_int8_params* p) { return p->count > 1 ? p->count : 1; }
+
+sketch_status launch_int8_encode(const sketch_int8_params* p, const sketch_int8_shape& s, const void* W, int dt,
+                                 int64_t ldw, void* buf, int32_t* status, hipStream_t st) {
+    return launch_encode8({W, nullptr, ldw, 0, static_cast<uint8_t*>(buf), status, p->M, p->N, s.ld,
+                           p->M * matrices(p), s.scales_offset, s.bytes}, dt, false, st);
+}
+
+constexpr int64_t kMaxElements = int64_t(1) << 60;   // whose bytes an int64 counts
+
+// Bytes from the first element of rows `ld` elements apart to behind the last.
+size_t extent(int64_t rows, int64_t N, int64_t ld, int dtype) {
+    return rows > 0 ? (size_t(rows - 1) * size_t(ld) + size_t(N)) * elem_bytes(dtype) : 0;
+}
+
+bool aligned_to_element(const void* p, int dtype) { return (reinterpret_cast<uintptr_t>(p) & (elem_bytes(dtype) - 1)) == 0; }
+
+// What one product does and needs.
+struct Plan {
+    sketch_int8_shape w, x;   // one weight, the encoded rows
+    bool encode;              // rows encoded by a launch of their own
+    size_t workspace;
+};
+
+// Checks the parameters and fills the plan.
+sketch_status make_plan(const sketch_int8_params* p, int64_t terms, int64_t x_rows, int x_dtype, int y_dtype,
+                        bool group, Plan* plan) {
+    sketch_status rc = int8_shape(p, &plan->w);
+    if (rc != SKETCH_OK) return rc;
+    const bool rows = x_dtype == SKETCH_INT8_ROWS;
+    if (terms < 0 || terms > SKETCH_INT8_MAX_M || (!rows && !valid_dtype(x_dtype)) || !valid_dtype(y_dtype) ||
+        matrices(p) > (group ? SKETCH_INT8_MAX_EXPERTS : 1))
+        return SKETCH_EINVAL;
+    const sketch_int8_params xp{x_rows, p->N, 1};
+    rc = int8_shape(&xp, &plan->x);
+    if (rc != SKETCH_OK) return rc;
+    plan->workspace = 0;
+    plan->encode = false;
+    if (terms == 0 || p->M == 0) return SKETCH_OK;
+    plan->encode = !rows;
+    if (plan->encode) plan->workspace += plan->x.bytes;
+    return SKETCH_OK;
+}
+
+sketch_status launch_product(const Int8Product& a, bool group, hipStream_t st) {
+    const int64_t tiles = (a.T + 15) / 16 + (group ? min(a.T, int64_t(a.experts)) : 0);
+    dim3 grid;
+    if (!grid_of((a.M + 15) / 16 * tiles, kWaves * 64, &grid)) return SKETCH_EINVAL;
+    if (group)
+        int8_rows_kernel<true><<<grid, kWaves * 64, 0, st>>>(a);
+    else
+        int8_rows_kernel<false><<<grid, kWaves * 64, 0, st>>>(a);
+    return launch_status();
+}
+
+sketch_status product(const sketch_int8_params* p, const void* buf, const void* X, int x_dtype, int64_t x_rows,
+                      int64_t terms, const sketch_int8_groups* g, void* Y, int y_dtype, void* workspace,
+                      size_t workspace_bytes, void* stream) {
+    Plan plan;
+    sketch_status rc = make_plan(p, terms, x_rows, x_dtype, y_dtype, g != nullptr, &plan);
+    if (rc != SKETCH_OK) return rc;
+    const bool index = g && g->rows;
+    if (g && ((g->counts_bits != 32 && g->counts_bits != 64) || (index && g->rows_bits != 32 && g->rows_bits != 64)))
+        return SKETCH_EINVAL;
+    if (terms == 0 || p->M == 0) return SKETCH_OK;
+    if (!buf || !X || !Y || !aligned16(buf) || !aligned16(X) || !aligned16(Y)) return SKETCH_EINVAL;
+    if (g && (x_rows < (index ? 1 : terms) || !g->counts ||
+              (reinterpret_cast<uintptr_t>(g->counts) & (g->counts_bits / 8 - 1)) ||
+              (index && (reinterpret_cast<uintptr_t>(g->rows) & (g->rows_bits / 8 - 1)))))
+        return SKETCH_EINVAL;
+    const size_t need = plan.workspace;
+    if (need > 0) {
+        if (!workspace || !aligned16(workspace)) return SKETCH_EINVAL;
+        if (workspace_bytes < need) return SKETCH_ESMALL;
+    }
+    // workgroups that are done store Y while others still read
+    const int64_t count = matrices(p);
+    const Range ry{Y, size_t(terms) * size_t(p->M) * elem_bytes(y_dtype)}, rw{buf, size_t(count) * plan.w.bytes},
+        rs{workspace, need}, rx{X, x_dtype == SKETCH_INT8_ROWS ? plan.x.bytes : extent(x_rows, p->N, p->N, x_dtype)},
+        rcounts{g ? g->counts : nullptr, g ? size_t(count) * size_t(g->counts_bits / 8) : 0},
+        rindex{index ? g->rows : nullptr, index ? size_t(terms) * size_t(g->rows_bits / 8) : 0};
+    if ((!plan.encode && overlap(ry, rx)) || overlap(rs, ry) || overlap(rs, rx)) return SKETCH_EINVAL;
+    for (const Range& r : {rw, rcounts, rindex})
+        if (overlap(ry, r) || overlap(rs, r)) return SKETCH_EINVAL;
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    const int8_t *w8 = static_cast<const int8_t*>(buf), *x8 = static_cast<const int8_t*>(X);
+    if (plan.encode) {
+        const sketch_int8_params xp{x_rows, p->N, 1};
+        rc = launch_int8_encode(&xp, plan.x, X, x_dtype, p->N, workspace, nullptr, st);
+        if (rc != SKETCH_OK) return rc;
+        x8 = static_cast<const int8_t*>(workspace);
+    }
+    Int8Product a{};
+    a.w = w8, a.w_bytes = plan.w.bytes, a.w_scales = plan.w.scales_offset;
+    a.x = x8, a.xs = reinterpret_cast<const float*>(x8 + plan.x.scales_offset), a.x_rows = x_rows;
+    a.Y = Y, a.M = p->M, a.T = terms, a.ld = plan.w.ld, a.kb = uint32_t(plan.w.ld / 128), a.ydt = y_dtype;
+    a.experts = int(count);
+    if (g) a.counts = g->counts, a.rows = g->rows, a.counts64 = g->counts_bits == 64, a.rows64 = g->rows_bits == 64;
+    return launch_product(a, g != nullptr, st);
+}
+
+}  // namespace
+
+sketch_status int8_shape(const sketch_int8_params* p, sketch_int8_shape* s) {
+    if (!p || p->M < 0 || p->M > SKETCH_INT8_MAX_M || p->N < 1 || p->N > SKETCH_INT8_MAX_N) return SKETCH_EINVAL;
+    if (p->count < 0 || p->count > SKETCH_INT8_MAX_COUNT) return SKETCH_EINVAL;
+    s->ld = (p->N + 127) / 128 * 128;
+    s->scales_offset = align256(size_t(p->M) * size_t(s->ld));
+    s->bytes = align256(s->scales_offset + size_t(p->M) * 4);
+    return SKETCH_OK;
+}
+
+}  // namespace sketch
+
+using namespace sketch;
+
+extern "C" {
+
+sketch_status sketch_int8_layout(const sketch_int8_params* p, sketch_int8_shape* shape) {
+    return shape ? int8_shape(p, shape) : SKETCH_EINVAL;
+}
+
+sketch_status sketch_int8_encode(const sketch_int8_params* p, const void* W, sketch_dtype w_dtype, int64_t ldw,
+                                 void* buf, int32_t* status_dev, void* stream) {
+    sketch_int8_shape s;
+    const sketch_status rc = int8_shape(p, &s);
+    if (rc != SKETCH_OK) return rc;
+    if (!valid_dtype(w_dtype) || ldw < p->N || (reinterpret_cast<uintptr_t>(status_dev) & 3u))
+        return SKETCH_EINVAL;
+    if (p->M == 0) return SKETCH_OK;
+    if (!W || !buf || !aligned_to_element(W, w_dtype) || !aligned16(buf)) return SKETCH_EINVAL;
+    const int64_t count = matrices(p);
+    if (ldw > kMaxElements / (count * p->M)) return SKETCH_EINVAL;
+    if (overlap({W, extent(count * p->M, p->N, ldw, w_dtype)}, {buf, size_t(count) * s.bytes})) return SKETCH_EINVAL;
+    return launch_int8_encode(p, s, W, w_dtype, ldw, buf, status_dev, static_cast<hipStream_t>(stream));
+}
+
+sketch_status sketch_int8_swiglu(const sketch_int8_params* p, const void* gate, int64_t ld_gate, const void* up,
+                                 int64_t ld_up, sketch_dtype dtype, void* buf, int32_t* status_dev, void* stream) {
+    sketch_int8_shape s;
+    const sketch_status rc = int8_shape(p, &s);
+    if (rc != SKETCH_OK) return rc;
+    if (!valid_dtype(dtype) || p->count > 1 || (reinterpret_cast<uintptr_t>(status_dev) & 3u)) return SKETCH_EINVAL;
+    if (ld_gate < p->N || ld_up < p->N) return SKETCH_EINVAL;
+    if (p->M == 0) return SKETCH_OK;
+    if (max(ld_gate, ld_up) > kMaxElements / p->M) return SKETCH_EINVAL;
+    if (!buf || !aligned16(buf)) return SKETCH_EINVAL;
+    for (const void* q : {gate, up})
+        if (!q || !aligned_to_element(q, dtype)) return SKETCH_EINVAL;
+    const Range out{buf, s.bytes};
+    if (overlap({gate, extent(p->M, p->N, ld_gate, dtype)}, out) || overlap({up, extent(p->M, p->N, ld_up, dtype)}, out))
+        return SKETCH_EINVAL;
+    return launch_encode8({gate, up, ld_gate, ld_up, static_cast<uint8_t*>(buf), status_dev, p->M, p->N, s.ld, p->M,
+                           s.scales_offset, s.bytes}, dtype, true, static_cast<hipStream_t>(stream));
+}
+
+sketch_status sketch_int8_workspace_bytes(const sketch_int8_params* p, int64_t batch, int x_dtype, int y_dtype,
+                                          size_t* bytes) {
+    Plan plan;
+    const sketch_status rc = make_plan(p, batch, batch, x_dtype, y_dtype, false, &plan);
+    if (rc != SKETCH_OK) return rc;
+    if (!bytes) return SKETCH_EINVAL;
+    *bytes = plan.workspace;
+    return SKETCH_OK;
+}
+
+sketch_status sketch_int8_matmul(const sketch_int8_params* p, const void* buf, const void* X, int x_dtype,
+                                 int64_t batch, void* Y, int y_dtype, void* workspace, size_t workspace_bytes,
+                                 void* stream) {
+    return product(p, buf, X, x_dtype, batch, batch, nullptr, Y, y_dtype, workspace, workspace_bytes, stream);
+}
+
+sketch_status sketch_int8_group_workspace_bytes(const sketch_int8_params* p, int64_t terms, int64_t x_rows,
+                                                int x_dtype, int y_dtype, size_t* bytes) {
+    Plan plan;
+    const sketch_status rc = make_plan(p, terms, x_rows, x_dtype, y_dtype, true, &plan);
+    if (rc != SKETCH_OK) return rc;
+    if (!bytes) return SKETCH_EINVAL;
+    *bytes = plan.workspace;
+    return SKETCH_OK;
+}
+
+sketch_status sketch_int8_matmul_group(const sketch_int8_params* p, const void* buf, const void* X, int x_dtype,
+                                       int64_t x_rows, const sketch_int8_groups* g, void* Y, int y_dtype,
+                                       void* workspace, size_t workspace_bytes, void* stream) {
+    if (!g) return SKETCH_EINVAL;
+    return product(p, buf, X, x_dtype, x_rows, g->terms, g, Y, y_dtype, workspace, workspace_bytes, stream);
+}
+
+}  // extern "C"
