@@ -356,6 +356,8 @@ bool aligned_to_element(const void* p, int dtype) { return (reinterpret_cast<uin
 struct Plan {
     sketch_int8_shape w, x;   // one weight, the encoded rows
     bool encode;              // rows encoded by a launch of their own
+    bool many;                // the kernels of int8_gemm.hip
+    Int8Plan gemm;
     size_t workspace;
 };
 
@@ -372,11 +374,16 @@ sketch_status make_plan(const sketch_int8_params* p, int64_t terms, int64_t x_ro
     rc = int8_shape(&xp, &plan->x);
     if (rc != SKETCH_OK) return rc;
     plan->workspace = 0;
-    plan->encode = false;
+    plan->encode = plan->many = false;
     if (terms == 0 || p->M == 0) return SKETCH_OK;
     plan->encode = !rows;
     if (plan->encode) plan->workspace += plan->x.bytes;
-    return SKETCH_OK;
+    plan->many = terms > 64;
+    if (!plan->many) return SKETCH_OK;
+    const bool near = x_rows * plan->x.ld <= int64_t(0xFFFFFFFF);
+    rc = int8_gemm_plan(p->M, terms, uint32_t(plan->w.ld / 128), int(matrices(p)), group, near, &plan->gemm);
+    plan->workspace += plan->gemm.workspace;
+    return rc;
 }
 
 sketch_status launch_product(const Int8Product& a, bool group, hipStream_t st) {
@@ -426,6 +433,7 @@ sketch_status product(const sketch_int8_params* p, const void* buf, const void* 
         rc = launch_int8_encode(&xp, plan.x, X, x_dtype, p->N, workspace, nullptr, st);
         if (rc != SKETCH_OK) return rc;
         x8 = static_cast<const int8_t*>(workspace);
+        workspace = static_cast<char*>(workspace) + plan.x.bytes;
     }
     Int8Product a{};
     a.w = w8, a.w_bytes = plan.w.bytes, a.w_scales = plan.w.scales_offset;
@@ -433,6 +441,7 @@ sketch_status product(const sketch_int8_params* p, const void* buf, const void* 
     a.Y = Y, a.M = p->M, a.T = terms, a.ld = plan.w.ld, a.kb = uint32_t(plan.w.ld / 128), a.ydt = y_dtype;
     a.experts = int(count);
     if (g) a.counts = g->counts, a.rows = g->rows, a.counts64 = g->counts_bits == 64, a.rows64 = g->rows_bits == 64;
+    if (plan.many) return launch_int8_gemm(a, plan.gemm, workspace, st);
     return launch_product(a, g != nullptr, st);
 }
 
