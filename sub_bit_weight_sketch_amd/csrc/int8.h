@@ -49,43 +49,54 @@ __device__ inline int expert_terms(const Int8Product& p, int e) {
     return int(c < 0 ? 0 : c > p.T ? p.T : c);
 }
 
-// Tile `tile` of the experts' terms cut into tiles of up to BT, or false past
-// the last one.  Every wave works it out for itself from the counts: 64 experts
-// at a time, two sums over the lanes.  T <= 2^24, so 64 counts of up to T fit an int.
-template <int BT>
-__device__ inline bool find_terms(const Int8Product& p, int tile, Terms& t) {
-    const int lane = threadIdx.x & 63, T = int(p.T);
-    int terms = 0, tiles = 0;
+// The terms of 64 experts, one to a lane, cut into tiles of up to BT.  T <= 2^24,
+// so 64 counts of up to T fit an int.
+struct ExpertTiles {
+    int begin, end;         // the lane's expert's terms
+    int tiles, upto;        // its tiles, and those of all experts up to it
+    int all_terms, all_tiles;
+
+    // of experts base .., behind `terms` terms and `before` tiles
+    template <int BT>
+    __device__ inline void count(const Int8Product& p, int base, int terms, int before) {
+        const int T = int(p.T), n = expert_terms(p, base + int(threadIdx.x & 63)), sum = wave_scan(n);
+        begin = min(terms + sum - n, T);
+        end = min(terms + sum, T);
+        tiles = (end - begin + BT - 1) / BT;
+        upto = before + wave_scan(tiles);
+        all_terms = __builtin_amdgcn_readlane(end, 63);
+        all_tiles = __builtin_amdgcn_readlane(upto, 63);
+    }
+
+    // whether `tile` is one of these, and which
+    template <int BT>
+    __device__ inline bool find(int base, int tile, Terms& t) const {
+        const uint64_t hit = __ballot(tile >= upto - tiles && tile < upto);
+        if (!hit) return false;
+        const int src = __builtin_ctzll(hit);
+        t.expert = base + src;
+        t.first = __builtin_amdgcn_readlane(begin, src) + (tile - __builtin_amdgcn_readlane(upto - tiles, src)) * BT;
+        t.n = min(BT, __builtin_amdgcn_readlane(end, src) - t.first);
+        return true;
+    }
+};
+
+// Tile `which(tiles)` of all `tiles` tiles of the experts' terms, or false where
+// that is none of them.  Every wave works it out for itself from the counts.
+template <int BT, typename Which>
+__device__ inline bool find_terms(const Int8Product& p, Which which, Terms& t) {
+    ExpertTiles x;
+    x.count<BT>(p, 0, 0, 0);
+    if (p.experts <= 64) return x.find<BT>(0, which(x.all_tiles), t);
+    for (int base = 64; base < p.experts; base += 64) x.count<BT>(p, base, x.all_terms, x.all_tiles);
+    const int tile = which(x.all_tiles);
+    int terms = 0, before = 0;
     for (int base = 0; base < p.experts; base += 64) {
-        const int n = expert_terms(p, base + lane);
-        const int upto = wave_scan(n), begin = min(terms + upto - n, T), end = min(terms + upto, T);
-        const int own = (end - begin + BT - 1) / BT, last = tiles + wave_scan(own);
-        const uint64_t hit = __ballot(tile >= last - own && tile < last);
-        if (hit) {
-            const int src = __builtin_ctzll(hit);
-            t.expert = base + src;
-            t.first = __builtin_amdgcn_readlane(begin, src) + (tile - __builtin_amdgcn_readlane(last - own, src)) * BT;
-            t.n = min(BT, __builtin_amdgcn_readlane(end, src) - t.first);
-            return true;
-        }
-        terms = min(terms + __builtin_amdgcn_readlane(upto, 63), T);
-        tiles = __builtin_amdgcn_readlane(last, 63);
+        x.count<BT>(p, base, terms, before);
+        if (x.find<BT>(base, tile, t)) return true;
+        terms = x.all_terms, before = x.all_tiles;
     }
     return false;
-}
-
-// Tiles of up to BT terms that the experts have.
-template <int BT>
-__device__ inline int count_tiles(const Int8Product& p) {
-    const int lane = threadIdx.x & 63, T = int(p.T);
-    int terms = 0, tiles = 0;
-    for (int base = 0; base < p.experts; base += 64) {
-        const int n = expert_terms(p, base + lane);
-        const int upto = wave_scan(n), begin = min(terms + upto - n, T), end = min(terms + upto, T);
-        tiles += __builtin_amdgcn_readlane(wave_scan((end - begin + BT - 1) / BT), 63);
-        terms = min(terms + __builtin_amdgcn_readlane(upto, 63), T);
-    }
-    return tiles;
 }
 
 // Row of X of a term, or -1 where it lies outside.
@@ -95,22 +106,34 @@ __device__ inline int64_t term_row(const Int8Product& p, int64_t term) {
     return r >= 0 && r < p.x_rows ? r : -1;
 }
 
-// What an exact sum stands for: rounded to float32, then by the scales.
-__device__ inline float int8_value(int sum, float sx, float sw) { return float(sum) * sx * sw; }
+// What an exact sum stands for: rounded to float32, then by the scales.  The
+// empty asm keeps the last product's rounding: without it the compiler may join it
+// with a conversion to binary16 that follows, and round once.
+__device__ inline float int8_value(int sum, float sx, float sw) {
+    float v = float(sum) * sx * sw;
+    asm("" : "+v"(v));
+    return v;
+}
 
-// Products of many rows (int8_gemm.hip): which kernel one takes, and over how
-// many workgroups K is split.
+// Which kernel a product takes, and over how many workgroups K is split.
+enum Int8Kind {
+    kInt8Rows1,   // int8_rows_kernel (int8.hip), 16 outputs to 8 waves
+    kInt8Rows2,   // the same, 32 outputs to 4 waves
+    kInt8Mid,     // int8_gemm_kernel (int8_gemm.hip)
+    kInt8Big      // int8_gemm_big_kernel
+};
+
 struct Int8Plan {
-    bool big;          // int8_gemm_big_kernel, or int8_gemm_kernel
+    Int8Kind kind;
     int fa, fb;        // outputs and terms of a tile, in units of 32
     uint32_t splits;
     int64_t tiles_o, tiles_t;
     size_t workspace;  // the parts of a split
 };
 
-// near: row * ld of every row of X fits 32 bits, or its rows are the terms in
-// order.  SKETCH_EINVAL when there are more tiles than a grid holds.
-sketch_status int8_gemm_plan(int64_t M, int64_t T, uint32_t kb, int experts, bool group, bool near, Int8Plan* g);
+// near: the place of every row of X in bytes fits 32 bits.  SKETCH_EINVAL when
+// there are more tiles than a grid holds.
+sketch_status int8_plan(int64_t M, int64_t T, uint32_t kb, int experts, bool group, bool near, Int8Plan* g);
 sketch_status launch_int8_gemm(const Int8Product& p, const Int8Plan& g, void* ws, hipStream_t st);
 
 sketch_status int8_shape(const sketch_int8_params* p, sketch_int8_shape* s);

@@ -2,6 +2,7 @@
 // row: their encoders, and the products Y = X8 * W8^T of few rows, for one weight
 // or for a stack of them with the rows grouped by expert.
 #include "int8.h"
+#include "tile.h"
 
 namespace sketch {
 namespace {
@@ -79,6 +80,11 @@ __device__ inline T row_max(T m, T* red, Max larger) {
     return m;
 }
 
+// Scale of a row from the bits of its largest magnitude.
+__device__ inline float row_scale(uint32_t bits) {
+    return bits >= 0x7F800000u ? __builtin_nanf("") : __uint_as_float(bits) / 127.0f;
+}
+
 struct EncodeArgs {
     const void *a, *b;        // the matrix, or gate and up
     int64_t lda, ldb;
@@ -88,10 +94,12 @@ struct EncodeArgs {
     size_t scales_offset, bytes;
 };
 
-// SwiGLU of 8 elements in float32.  exp(-g) by a product in two parts, so that
-// the error is that of a few roundings (h: under 6e-7 of its size); `rough` is set
-// where that does not hold: far negative gates, and values past float32's range.
-__device__ inline void swiglu8(const float (&g)[8], const float (&u)[8], float (&h)[8], bool& rough) {
+// SwiGLU of 8 elements in float32, and the least gate.  exp(-g) is a product in two
+// parts, so that the error is that of a few roundings (h: under 6e-7 of its size) for
+// gates from kLeastGate on; infinities and NaN show in h.
+constexpr float kLeastGate = -80.0f;
+
+__device__ inline void swiglu8(const float (&g)[8], const float (&u)[8], float (&h)[8], float& least) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         constexpr float kLog2e = 1.44269502162933349609375f, kLog2eLow = 1.92596299112661746887e-8f;
@@ -99,7 +107,7 @@ __device__ inline void swiglu8(const float (&g)[8], const float (&u)[8], float (
         const float low = __builtin_fmaf(-g[e], kLog2e, -t) - g[e] * kLog2eLow;   // what t lacks
         const float ex = __builtin_amdgcn_exp2f(t) * __builtin_fmaf(low, 0.693147182f, 1.0f);
         h[e] = g[e] * __builtin_amdgcn_rcpf(1.0f + ex) * u[e];
-        rough |= !(g[e] > -80.0f && fabsf(g[e]) < 3.0e38f && fabsf(h[e]) < 3.0e38f);
+        least = fminf(least, g[e]);
     }
 }
 
@@ -157,17 +165,19 @@ __global__ __launch_bounds__(256) void int8_encode_kernel(EncodeArgs a) {
         put(c, x);
     }
     if (at == 0) {
-        reinterpret_cast<float*>(buf + a.scales_offset)[m] = bad ? __builtin_nanf("") : bits == 0 ? 0.0f : amax / 127.0f;
+        reinterpret_cast<float*>(buf + a.scales_offset)[m] = row_scale(bits);
         if (a.status && bad) atomicOr(a.status, SKETCH_FLAG_WEIGHT_RANGE);
     }
 }
 
-// The same of h = silu(gate) * up.  The float32 h decides the codes where it
-// is clear of the middle of two integers (1.2e-4 of a code; its error is under
-// 7.5e-5), float64 the others, one in 4000; the largest magnitude is that of float64
-// among the elements within 2e-6 of the largest in float32.  Rows that float32
-// cannot hold (rough, or tiny) are computed in float64 throughout.
-template <int DT, int L>
+// The same of h = silu(gate) * up, K chunks of h kept.  The float32 h decides the
+// codes where it is clear of the middle of two integers (by 1.2e-4 of a code; its
+// error is under 7.6e-5), float64 the others, one in 4000, for which gate and up are
+// read again; the largest magnitude is that of float64 among the elements within 2e-6
+// of the largest in float32.  Rows that float32 cannot hold (a gate below
+// kLeastGate, values past its range, or tiny ones throughout) are computed in float64.
+// HBM-bound beside the arithmetic, some 35 instructions an element.
+template <int DT, int L, int K>
 __global__ __launch_bounds__(256) void int8_swiglu_kernel(EncodeArgs a) {
     __shared__ uint32_t red[4];
     __shared__ double red64[4];
@@ -181,64 +191,114 @@ __global__ __launch_bounds__(256) void int8_swiglu_kernel(EncodeArgs a) {
         load_row8<DT>(G, 0, a.N, int64_t(c) * 8, g);
         load_row8<DT>(U, 0, a.N, int64_t(c) * 8, u);
     };
-    bool rough = false;
-    uint32_t bits = 0;
-    for (int c = at; c < chunks; c += L) {
-        float g[8], u[8], h[8];
-        load(c, g, u);
-        swiglu8(g, u, h, rough);
-        bits = max(bits, max_bits(h));
-    }
-    if (rough) bits = 0x7FFFFFFFu;
+    auto precise = [&](int c, int e) { return swiglu64(load_elem<DT>(G, c * 8 + e), load_elem<DT>(U, c * 8 + e)); };
     auto umax = [](uint32_t x, uint32_t y) { return max(x, y); };
     auto dmax = [](double x, double y) { return x > y || x != x ? x : y; };   // NaN wins
+    uint8_t* codes = a.buf + row * a.ld;
+    float h[K][8], least = 0.0f;
+    uint32_t bits = 0;
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+        if (at + i * L < chunks) {
+            float g[8], u[8];
+            load(at + i * L, g, u);
+            swiglu8(g, u, h[i], least);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) h[i][e] = 0.0f;
+        }
+        bits = max(bits, max_bits(h[i]));
+    }
+    for (int c = at + K * L; c < chunks; c += L) {
+        float g[8], u[8], x[8];
+        load(c, g, u);
+        swiglu8(g, u, x, least);
+        bits = max(bits, max_bits(x));
+    }
+    if (least < kLeastGate) bits = 0x7FFFFFFFu;
     bits = row_max<L>(bits, red, umax);
     const bool whole = bits >= 0x7F800000u || bits < __float_as_uint(kTiny);
-    const float near = whole ? 0.0f : __uint_as_float(bits) * (1.0f - 2e-6f);
     double big = 0.0;
-    for (int c = at; c < chunks; c += L) {
-        float g[8], u[8], h[8] = {};
-        load(c, g, u);
-        if (!whole) swiglu8(g, u, h, rough);
+    auto larger = [&](int c, const float (&x)[8]) {
+        const float near = __uint_as_float(bits) * (1.0f - 2e-6f);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-            if (whole || fabsf(h[e]) >= near) big = dmax(fabs(swiglu64(g[e], u[e])), big);
+            if (fabsf(x[e]) >= near) big = dmax(fabs(precise(c, e)), big);
+    };
+    if (whole) {
+        for (int c = at; c < chunks; c += L) {
+            float g[8], u[8];
+            load(c, g, u);
+            for (int e = 0; e < 8; ++e) big = dmax(fabs(swiglu64(g[e], u[e])), big);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < K; ++i)
+            if (at + i * L < chunks) larger(at + i * L, h[i]);
+        for (int c = at + K * L; c < chunks; c += L) {
+            float g[8], u[8], x[8];
+            load(c, g, u);
+            swiglu8(g, u, x, least);
+            larger(c, x);
+        }
     }
     big = row_max<L>(big, red64, dmax);
-    const float scale = float(big / 127.0);
-    const bool bad = !(fabs(big) <= 3.4028234663852886e38);   // NaN too
-    const double inv = bad || big == 0.0 ? 0.0 : 127.0 / big;
-    const float inv32 = float(inv);
-    uint8_t* codes = a.buf + row * a.ld;
-    for (int c = at; c < chunks; c += L) {
-        float g[8], u[8], h[8] = {};
-        load(c, g, u);
-        if (!whole) swiglu8(g, u, h, rough);
+    const bool bad = !(big <= 3.4028234663852886e38);   // NaN too
+    const double per = bad || big == 0.0 ? 1.0 : big;
+    auto code = [&](double x) { return bad ? 0 : int(__builtin_rint(x * 127.0 / per)); };
+    const float inv = float(127.0 / per);
+    auto put = [&](int c, const float (&x)[8]) {
         int q[8];
+        uint32_t unsure = 0;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const float v = h[e] * inv32, near_int = __builtin_rintf(v);
-            q[e] = int(near_int);
-            if (whole || fabsf(v - near_int) > 0.5f - 1.2e-4f) q[e] = bad ? 0 : code64(swiglu64(g[e], u[e]), inv);
+            const float v = x[e] * inv, integer = __builtin_rintf(v);
+            q[e] = int(integer);
+            unsure |= fabsf(v - integer) > 0.5f - 1.2e-4f ? 1u << e : 0u;
+        }
+        if (unsure) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (unsure >> e & 1) q[e] = code(precise(c, e));
         }
         *reinterpret_cast<uint2*>(codes + int64_t(c) * 8) = make_uint2(pack4(q, 0), pack4(q, 4));
+    };
+    if (whole) {
+        for (int c = at; c < chunks; c += L) {
+            float g[8], u[8];
+            int q[8];
+            load(c, g, u);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) q[e] = code(swiglu64(g[e], u[e]));
+            *reinterpret_cast<uint2*>(codes + int64_t(c) * 8) = make_uint2(pack4(q, 0), pack4(q, 4));
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < K; ++i)
+            if (at + i * L < chunks) put(at + i * L, h[i]);
+        for (int c = at + K * L; c < chunks; c += L) {
+            float g[8], u[8], x[8];
+            load(c, g, u);
+            swiglu8(g, u, x, least);
+            put(c, x);
+        }
     }
     if (at == 0) {
-        reinterpret_cast<float*>(a.buf + a.scales_offset)[row] = bad ? __builtin_nanf("") : scale;
+        reinterpret_cast<float*>(a.buf + a.scales_offset)[row] = bad ? __builtin_nanf("") : float(big / 127.0);
         if (a.status && bad) atomicOr(a.status, SKETCH_FLAG_WEIGHT_RANGE);
     }
 }
 
 // ---------------------------------------------------------------------------
-// Product of up to 16 terms at a time: 16 outputs to a workgroup, whose 8
-// waves share out the columns in runs of 4 blocks of 128.  A fragment is 16 rows
-// x 128 columns, one row to a lane: lane l holds row l % 16 and the columns
-// 16c..16c+15 and 64+16c..64+16c+15, c = l / 16, the same ones of outputs (A)
-// and terms (B).  D: term l % 16, outputs 4c..4c+3.
+// Product of up to 16 TT terms at a time, bound by the codes of W coming from
+// memory: 16 RT outputs to a workgroup, whose waves share out the columns in runs
+// of RUN blocks of 128, all loads of a run in flight, both operands straight to
+// registers.  A fragment is 16 rows x 128 columns, one row to a lane: lane l
+// holds row l % 16 and the columns 16c..16c+15 and 64+16c..64+16c+15, c = l / 16,
+// the same ones of outputs (A) and terms (B), so that a pair of loads covers 128
+// contiguous bytes of a row.  D: term l % 16, outputs 4c..4c+3.  The waves' sums meet
+// in LDS, 16 terms at a time.
 // ---------------------------------------------------------------------------
-constexpr int kWaves = 8;
-constexpr int kRun = 4;
-
 struct Frag {
     i32x4 lo, hi;
     __device__ inline void load(const int8_t* row, uint32_t block, int c) {
@@ -253,53 +313,191 @@ __device__ inline i32x4 multiply(const Frag& a, const Frag& b, i32x4 acc) {
     return __builtin_amdgcn_mfma_i32_16x16x64_i8(a.hi, b.hi, acc, 0, 0, 0);
 }
 
-__device__ inline void store_y(const Int8Product& p, int64_t t, int64_t m, float v) {
-    const int64_t e = t * p.M + m;
-    if (p.ydt == SKETCH_F32)
-        store1_val<SKETCH_F32>(p.Y, e, v);
-    else if (p.ydt == SKETCH_BF16)
-        store1_val<SKETCH_BF16>(p.Y, e, v);
-    else
-        store1_val<SKETCH_F16>(p.Y, e, v);
-}
-
-template <bool GROUP>
-__global__ __launch_bounds__(kWaves * 64) void int8_rows_kernel(Int8Product p) {
-    __shared__ int part[kWaves][16][17];
+template <bool GROUP, int WAVES, int RT, int TT, int RUN>
+__global__ __launch_bounds__(WAVES * 64) void int8_rows_kernel(Int8Product p) {
+    __shared__ __attribute__((aligned(16))) int part[TT > 1 ? 2 : 1][WAVES][16][RT * 16 + 4];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r = lane & 15, c = lane >> 4;
-    const int64_t tiles_o = (p.M + 15) / 16;
-    const int64_t id = int64_t(blockIdx.y) * gridDim.x + blockIdx.x, tile = id / tiles_o, m0 = (id - tile * tiles_o) * 16;
-    Terms t{0, int(tile * 16), int(min(int64_t(16), p.T - tile * 16))};
-    if (GROUP ? !find_terms<16>(p, int(tile), t) : t.n <= 0) return;
+    const int64_t tiles_o = (p.M + RT * 16 - 1) / (RT * 16);
+    const int64_t id = int64_t(blockIdx.y) * gridDim.x + blockIdx.x, tile = id / tiles_o, m0 = (id - tile * tiles_o) * (RT * 16);
+    Terms t{0, int(tile * (16 * TT)), int(min(int64_t(16 * TT), p.T - tile * (16 * TT)))};
+    if (GROUP ? !find_terms<16 * TT>(p, [&](int) { return int(tile); }, t) : t.n <= 0) return;
     const int8_t* w = p.w + size_t(t.expert) * p.w_bytes;
-    const int8_t* wrow = w + min(m0 + r, p.M - 1) * p.ld;
-    const int64_t term = t.first + min(r, t.n - 1);
-    const int64_t row = GROUP ? term_row(p, term) : term;
-    const int8_t* xrow = p.x + (row < 0 ? 0 : row) * p.ld;
-    i32x4 acc = {0, 0, 0, 0};
-    for (uint32_t k = wave * kRun; k < p.kb; k += kWaves * kRun) {
-        Frag a[kRun], b[kRun];
+    const int8_t *wrow[RT], *xrow[TT];
 #pragma unroll
-        for (int u = 0; u < kRun; ++u) {
-            a[u].load(wrow, min(k + u, p.kb - 1), c);
-            b[u].load(xrow, min(k + u, p.kb - 1), c);
+    for (int i = 0; i < RT; ++i) wrow[i] = w + min(m0 + i * 16 + r, p.M - 1) * p.ld;
+#pragma unroll
+    for (int j = 0; j < TT; ++j) {
+        const int64_t term = t.first + min(j * 16 + r, t.n - 1);
+        xrow[j] = p.x + (GROUP ? max(term_row(p, term), int64_t(0)) : term) * p.ld;
+    }
+    i32x4 acc[RT][TT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int j = 0; j < TT; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+    for (uint32_t k = wave * RUN; k < p.kb; k += WAVES * RUN) {
+        Frag a[RUN][RT], b[RUN][TT];
+#pragma unroll
+        for (int u = 0; u < RUN; ++u) {   // blocks past the last are read as the last and not used
+            const uint32_t block = min(k + u, p.kb - 1);
+#pragma unroll
+            for (int i = 0; i < RT; ++i) a[u][i].load(wrow[i], block, c);
+#pragma unroll
+            for (int j = 0; j < TT; ++j) b[u][j].load(xrow[j], block, c);
         }
+        asm volatile("" ::: "memory");   // all loads of the run before its first use
 #pragma unroll
-        for (int u = 0; u < kRun; ++u)
-            if (k + u < p.kb) acc = multiply(a[u], b[u], acc);
+        for (int u = 0; u < RUN; ++u) {
+            if (k + u >= p.kb) break;
+#pragma unroll
+            for (int i = 0; i < RT; ++i)
+#pragma unroll
+                for (int j = 0; j < TT; ++j) acc[i][j] = multiply(a[u][i], b[u][j], acc[i][j]);
+        }
+    }
+    // 16 terms x 16 RT outputs, 4 outputs to a thread
+    constexpr int kAcross = RT * 4;
+    const int m = tid % kAcross * 4, n = tid / kAcross;
+    const bool stores = n < 16 && m0 + m < p.M, vec = p.M % 4 == 0;
+    f32x4 sw = {0, 0, 0, 0};
+    if (stores) sw = *reinterpret_cast<const f32x4*>(reinterpret_cast<const char*>(w) + p.w_scales + (m0 + m) * 4);
+#pragma unroll
+    for (int j = 0; j < TT; ++j) {
+        int (&mine)[WAVES][16][RT * 16 + 4] = part[j & 1];
+#pragma unroll
+        for (int i = 0; i < RT; ++i) *reinterpret_cast<i32x4*>(&mine[wave][r][i * 16 + 4 * c]) = acc[i][j];
+        __syncthreads();
+        if (!stores || j * 16 + n >= t.n) continue;
+        i32x4 sum = *reinterpret_cast<const i32x4*>(&mine[0][n][m]);
+#pragma unroll
+        for (int i = 1; i < WAVES; ++i) sum += *reinterpret_cast<const i32x4*>(&mine[i][n][m]);
+        const int64_t term = t.first + j * 16 + n, row = GROUP ? term_row(p, term) : term;
+        const float sx = row < 0 ? __builtin_nanf("") : p.xs[row];
+        f32x4 v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = int8_value(sum[i], sx, sw[i]);
+        const int64_t at = term * p.M + m0 + m;
+        if (p.ydt == SKETCH_F32)
+            store4<SKETCH_F32>(p.Y, at, v, m0 + m, p.M, vec);
+        else if (p.ydt == SKETCH_BF16)
+            store4<SKETCH_BF16>(p.Y, at, v, m0 + m, p.M, vec);
+        else
+            store4<SKETCH_F16>(p.Y, at, v, m0 + m, p.M, vec);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Product of up to NP rows of X (p.x, of dtype XD), encoded by every workgroup for
+// itself, which saves the launch that would encode them first: 16 outputs to a
+// workgroup, whose 8 waves share out the columns in runs of 4 blocks, as above.  The
+// loads of W go out first; while they are on their way the workgroup encodes X
+// into LDS, two chunks of 8 columns of each row to a thread from registers, what a
+// longer row has more read again.
+// ---------------------------------------------------------------------------
+constexpr uint32_t kTokenCodes = 32768;   // bytes of codes that LDS holds, with 64 more for each row
+constexpr int kTokens = SKETCH_INT8_TOKENS;
+
+template <int XD, int NP>
+__global__ __launch_bounds__(512) void int8_tokens_kernel(Int8Product p, int64_t N) {
+    extern __shared__ __attribute__((aligned(16))) uint8_t codes[];   // [NP][ld + 64]
+    __shared__ uint32_t red[8][NP];
+    __shared__ __attribute__((aligned(16))) int part[8][16][20];
+    constexpr int RUN = 4;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int r = lane & 15, c = lane >> 4, T = int(p.T), pitch = int(p.ld) + 64, chunks = int(p.ld / 8);
+    const int64_t m0 = int64_t(blockIdx.x) * 16;
+    const int8_t* wrow = p.w + min(m0 + r, p.M - 1) * p.ld;
+    const uint32_t k0 = wave * RUN;
+    Frag a[RUN];
+#pragma unroll
+    for (int u = 0; u < RUN; ++u) a[u].load(wrow, min(k0 + u, p.kb - 1), c);
+    asm volatile("" ::: "memory");   // on their way before X is asked for
+
+    constexpr int es = XD == SKETCH_F32 ? 4 : 2;
+    auto row_of = [&](int n) { return static_cast<const char*>(static_cast<const void*>(p.x)) + int64_t(min(n, T - 1)) * N * es; };
+    float v[NP][2][8];
+    uint32_t bits[NP];
+#pragma unroll
+    for (int n = 0; n < NP; ++n) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (tid + i * 512 < chunks) {
+                load_row8<XD>(row_of(n), 0, N, (tid + i * 512) * 8, v[n][i]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[n][i][e] = 0.0f;
+            }
+        }
     }
 #pragma unroll
-    for (int v = 0; v < 4; ++v) part[wave][r][4 * c + v] = acc[v];
+    for (int n = 0; n < NP; ++n) {
+        bits[n] = max(max_bits(v[n][0]), max_bits(v[n][1]));
+        for (int q = tid + 1024; q < chunks; q += 512) {
+            float x[8];
+            load_row8<XD>(row_of(n), 0, N, int64_t(q) * 8, x);
+            bits[n] = max(bits[n], max_bits(x));
+        }
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) bits[n] = max(bits[n], uint32_t(__shfl_xor(int(bits[n]), d)));
+        if (lane == 0) red[wave][n] = bits[n];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < NP; ++n) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) bits[n] = max(bits[n], red[i][n]);
+        if (n >= T) break;
+        const bool bad = bits[n] >= 0x7F800000u;
+        const Rounder<XD> round(bad || bits[n] == 0 ? 1.0f : __uint_as_float(bits[n]));
+        auto put = [&](int q, const float (&x)[8]) {
+            *reinterpret_cast<uint2*>(codes + n * pitch + q * 8) = bad ? make_uint2(0, 0) : codes8<XD>(x, round);
+        };
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (tid + i * 512 < chunks) put(tid + i * 512, v[n][i]);
+        for (int q = tid + 1024; q < chunks; q += 512) {
+            float x[8];
+            load_row8<XD>(row_of(n), 0, N, int64_t(q) * 8, x);
+            put(q, x);
+        }
+    }
+    __syncthreads();
+
+    i32x4 acc = {0, 0, 0, 0};
+    const int8_t* xrow = reinterpret_cast<const int8_t*>(codes) + min(r, T - 1) * pitch;   // terms past the last are not stored
+    for (uint32_t k = k0; k < p.kb; k += 8 * RUN) {
+        if (k != k0) {
+#pragma unroll
+            for (int u = 0; u < RUN; ++u) a[u].load(wrow, min(k + u, p.kb - 1), c);
+        }
+#pragma unroll
+        for (int u = 0; u < RUN; ++u) {
+            if (k + u >= p.kb) break;
+            Frag b;
+            b.load(xrow, k + u, c);
+            acc = multiply(a[u], b, acc);
+        }
+    }
+    *reinterpret_cast<i32x4*>(&part[wave][r][4 * c]) = acc;
     __syncthreads();
     const int m = tid & 15, n = tid >> 4;
-    if (n >= t.n || m0 + m >= p.M) return;
+    if (n >= T || m0 + m >= p.M) return;
     int sum = 0;
 #pragma unroll
-    for (int i = 0; i < kWaves; ++i) sum += part[i][n][m];
-    const int64_t from = GROUP ? term_row(p, t.first + n) : t.first + n;
-    const float sx = from < 0 ? __builtin_nanf("") : p.xs[from];
-    store_y(p, t.first + n, m0 + m, int8_value(sum, sx, reinterpret_cast<const float*>(w + p.w_scales)[m0 + m]));
+    for (int i = 0; i < 8; ++i) sum += part[i][n][m];
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = max(top, red[i][NP > 1 ? n : 0]);
+    const float sx = row_scale(top);
+    const float y = int8_value(sum, sx, reinterpret_cast<const float*>(reinterpret_cast<const char*>(p.w) + p.w_scales)[m0 + m]);
+    const int64_t at = n * p.M + m0 + m;
+    if (p.ydt == SKETCH_F32)
+        store1_val<SKETCH_F32>(p.Y, at, y);
+    else if (p.ydt == SKETCH_BF16)
+        store1_val<SKETCH_BF16>(p.Y, at, y);
+    else
+        store1_val<SKETCH_F16>(p.Y, at, y);
 }
 
 bool valid_dtype(int d) { return d == SKETCH_F32 || d == SKETCH_BF16 || d == SKETCH_F16; }
@@ -315,8 +513,9 @@ bool grid_of(int64_t groups, int threads, dim3* grid) {
 
 sketch_status launch_encode8(const EncodeArgs& a, int dt, bool swiglu, hipStream_t st) {
     dim3 grid;
-    // a wave to a row up to 2048 columns, which it keeps
-    const bool narrow = a.ld <= 64 * 8 * kKept;
+    // a wave to a row of up to 2048 columns, which it keeps, where there are rows for all compute units; a workgroup
+    // to a row otherwise
+    const bool narrow = a.ld <= 64 * 8 * kKept && a.rows >= 4 * int64_t(compute_units());
     if (!grid_of(narrow ? (a.rows + 3) / 4 : a.rows, 256, &grid)) return SKETCH_EINVAL;
     auto go = [&](auto one, auto all) {
         if (narrow)
@@ -326,9 +525,9 @@ sketch_status launch_encode8(const EncodeArgs& a, int dt, bool swiglu, hipStream
         return launch_status();
     };
     if (swiglu) {
-        if (dt == SKETCH_F32) return go(int8_swiglu_kernel<SKETCH_F32, 64>, int8_swiglu_kernel<SKETCH_F32, 256>);
-        if (dt == SKETCH_BF16) return go(int8_swiglu_kernel<SKETCH_BF16, 64>, int8_swiglu_kernel<SKETCH_BF16, 256>);
-        return go(int8_swiglu_kernel<SKETCH_F16, 64>, int8_swiglu_kernel<SKETCH_F16, 256>);
+        if (dt == SKETCH_F32) return go(int8_swiglu_kernel<SKETCH_F32, 64, 4>, int8_swiglu_kernel<SKETCH_F32, 256, 6>);
+        if (dt == SKETCH_BF16) return go(int8_swiglu_kernel<SKETCH_BF16, 64, 4>, int8_swiglu_kernel<SKETCH_BF16, 256, 6>);
+        return go(int8_swiglu_kernel<SKETCH_F16, 64, 4>, int8_swiglu_kernel<SKETCH_F16, 256, 6>);
     }
     if (dt == SKETCH_F32) return go(int8_encode_kernel<SKETCH_F32, 64>, int8_encode_kernel<SKETCH_F32, 256>);
     if (dt == SKETCH_BF16) return go(int8_encode_kernel<SKETCH_BF16, 64>, int8_encode_kernel<SKETCH_BF16, 256>);
@@ -356,10 +555,18 @@ bool aligned_to_element(const void* p, int dtype) { return (reinterpret_cast<uin
 struct Plan {
     sketch_int8_shape w, x;   // one weight, the encoded rows
     bool encode;              // rows encoded by a launch of their own
-    bool many;                // the kernels of int8_gemm.hip
     Int8Plan gemm;
     size_t workspace;
 };
+
+// Whether a product of raw rows encodes them in its own workgroups.  One row
+// always gains (11008 x 4096: 11.7 us, 14.2 with a launch of its own; 28672 x 8192
+// 45.1 and 45.3).  2 to 4 rows need registers that leave a compute unit one workgroup,
+// and gain where each has one only (4096 x 4096, 4 rows: 10.2 and 12.6 us; 11008 x
+// 4096 22.9 and 14.6).
+bool encodes_itself(int64_t M, int64_t rows, int64_t ld) {
+    return rows <= kTokens && rows * ld <= int64_t(kTokenCodes) && (rows == 1 || M <= 16 * int64_t(compute_units()));
+}
 
 // Checks the parameters and fills the plan.
 sketch_status make_plan(const sketch_int8_params* p, int64_t terms, int64_t x_rows, int x_dtype, int y_dtype,
@@ -374,27 +581,37 @@ sketch_status make_plan(const sketch_int8_params* p, int64_t terms, int64_t x_ro
     rc = int8_shape(&xp, &plan->x);
     if (rc != SKETCH_OK) return rc;
     plan->workspace = 0;
-    plan->encode = plan->many = false;
+    plan->encode = false;
     if (terms == 0 || p->M == 0) return SKETCH_OK;
-    plan->encode = !rows;
+    plan->encode = !rows && (group || !encodes_itself(p->M, terms, plan->x.ld));
     if (plan->encode) plan->workspace += plan->x.bytes;
-    plan->many = terms > 64;
-    if (!plan->many) return SKETCH_OK;
+    if (!plan->encode && !rows) return SKETCH_OK;   // encoded by the product's own workgroups
     const bool near = x_rows * plan->x.ld <= int64_t(0xFFFFFFFF);
-    rc = int8_gemm_plan(p->M, terms, uint32_t(plan->w.ld / 128), int(matrices(p)), group, near, &plan->gemm);
+    rc = int8_plan(p->M, terms, uint32_t(plan->w.ld / 128), int(matrices(p)), group, near, &plan->gemm);
     plan->workspace += plan->gemm.workspace;
     return rc;
 }
 
-sketch_status launch_product(const Int8Product& a, bool group, hipStream_t st) {
-    const int64_t tiles = (a.T + 15) / 16 + (group ? min(a.T, int64_t(a.experts)) : 0);
+template <int WAVES, int RT, int TT, int RUN>
+sketch_status launch_rows(const Int8Product& a, hipStream_t st) {
+    const int64_t tiles = (a.T + 16 * TT - 1) / (16 * TT) + (a.counts ? min(a.T, int64_t(a.experts)) : 0);
     dim3 grid;
-    if (!grid_of((a.M + 15) / 16 * tiles, kWaves * 64, &grid)) return SKETCH_EINVAL;
-    if (group)
-        int8_rows_kernel<true><<<grid, kWaves * 64, 0, st>>>(a);
+    if (!grid_of((a.M + RT * 16 - 1) / (RT * 16) * tiles, WAVES * 64, &grid)) return SKETCH_EINVAL;
+    if (a.counts)
+        int8_rows_kernel<true, WAVES, RT, TT, RUN><<<grid, WAVES * 64, 0, st>>>(a);
     else
-        int8_rows_kernel<false><<<grid, kWaves * 64, 0, st>>>(a);
+        int8_rows_kernel<false, WAVES, RT, TT, RUN><<<grid, WAVES * 64, 0, st>>>(a);
     return launch_status();
+}
+
+template <int NP>
+sketch_status launch_tokens(const Int8Product& a, int x_dtype, int64_t N, hipStream_t st) {
+    auto go = [&](auto kernel) {
+        kernel<<<unsigned((a.M + 15) / 16), 512, unsigned(a.T * (a.ld + 64)), st>>>(a, N);
+        return launch_status();
+    };
+    if (x_dtype == SKETCH_F32) return go(int8_tokens_kernel<SKETCH_F32, NP>);
+    return x_dtype == SKETCH_BF16 ? go(int8_tokens_kernel<SKETCH_BF16, NP>) : go(int8_tokens_kernel<SKETCH_F16, NP>);
 }
 
 sketch_status product(const sketch_int8_params* p, const void* buf, const void* X, int x_dtype, int64_t x_rows,
@@ -423,7 +640,7 @@ sketch_status product(const sketch_int8_params* p, const void* buf, const void* 
         rs{workspace, need}, rx{X, x_dtype == SKETCH_INT8_ROWS ? plan.x.bytes : extent(x_rows, p->N, p->N, x_dtype)},
         rcounts{g ? g->counts : nullptr, g ? size_t(count) * size_t(g->counts_bits / 8) : 0},
         rindex{index ? g->rows : nullptr, index ? size_t(terms) * size_t(g->rows_bits / 8) : 0};
-    if ((!plan.encode && overlap(ry, rx)) || overlap(rs, ry) || overlap(rs, rx)) return SKETCH_EINVAL;
+    if (((!plan.encode || (!g && terms <= kTokens)) && overlap(ry, rx)) || overlap(rs, ry) || overlap(rs, rx)) return SKETCH_EINVAL;
     for (const Range& r : {rw, rcounts, rindex})
         if (overlap(ry, r) || overlap(rs, r)) return SKETCH_EINVAL;
     const hipStream_t st = static_cast<hipStream_t>(stream);
@@ -441,8 +658,11 @@ sketch_status product(const sketch_int8_params* p, const void* buf, const void* 
     a.Y = Y, a.M = p->M, a.T = terms, a.ld = plan.w.ld, a.kb = uint32_t(plan.w.ld / 128), a.ydt = y_dtype;
     a.experts = int(count);
     if (g) a.counts = g->counts, a.rows = g->rows, a.counts64 = g->counts_bits == 64, a.rows64 = g->rows_bits == 64;
-    if (plan.many) return launch_int8_gemm(a, plan.gemm, workspace, st);
-    return launch_product(a, g != nullptr, st);
+    if (!plan.encode && x_dtype != SKETCH_INT8_ROWS)
+        return terms == 1 ? launch_tokens<1>(a, x_dtype, p->N, st) : launch_tokens<kTokens>(a, x_dtype, p->N, st);
+    if (plan.gemm.kind == kInt8Rows1) return launch_rows<8, 1, 1, 4>(a, st);
+    if (plan.gemm.kind == kInt8Rows2) return launch_rows<4, 2, 1, 4>(a, st);
+    return launch_int8_gemm(a, plan.gemm, workspace, st);
 }
 
 }  // namespace

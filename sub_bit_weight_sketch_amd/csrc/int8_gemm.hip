@@ -7,6 +7,10 @@
 // fragment be read without bank conflicts.  A fragment is 16 rows x 128
 // columns: lane l holds row l % 16 and the columns 16c..16c+15 and
 // 64+16c..64+16c+15, c = l / 16, the same ones in both operands.
+#include <math.h>
+
+#include <type_traits>
+
 #include "int8.h"
 #include "tile.h"
 
@@ -28,29 +32,103 @@ __device__ inline void dma16_at(const int8_t* at, uint32_t lds) {
 // Tile of a workgroup: its first output and its terms; false where it has none.
 template <int ROWS, int BT, bool GROUP>
 __device__ inline bool my_tile(const GemmArgs& a, int64_t& o0, Terms& t) {
-    uint32_t to, tt, n = gridDim.x, tiles_t = a.tiles_t;
+    uint32_t to = 0, tt;
     if constexpr (GROUP) {
-        tiles_t = uint32_t(count_tiles<BT>(a.p));
-        n = tiles_t * a.tiles_o;
-        if (blockIdx.x >= n) return false;
+        const bool any = find_terms<BT>(a.p, [&](int tiles) {
+            const uint32_t n = uint32_t(tiles) * a.tiles_o;
+            if (blockIdx.x >= n) return -1;
+            spread_tile(blockIdx.x, a.tiles_o, uint32_t(tiles), n, to, tt);
+            return int(tt);
+        }, t);
+        o0 = int64_t(to) * ROWS;
+        return any;
     }
-    spread_tile(blockIdx.x, a.tiles_o, tiles_t, n, to, tt);
+    spread_tile(blockIdx.x, a.tiles_o, a.tiles_t, gridDim.x, to, tt);
     o0 = int64_t(to) * ROWS;
-    if constexpr (GROUP) return find_terms<BT>(a.p, int(tt), t);
     t.expert = 0;
     t.first = int(tt) * BT;
     t.n = int(min(int64_t(BT), a.p.T - t.first));
     return true;
 }
 
-__device__ inline float term_scale(const Int8Product& p, bool group, int64_t term) {
-    const int64_t row = group ? term_row(p, term) : term;
+// The scales of a tile: thread i loads that of output i, or of term i - ROWS, well
+// before the sums are there; they meet in LDS behind the waves' parts.
+template <int ROWS, int BT, bool GROUP>
+__device__ inline float tile_scale(const Int8Product& p, const Terms& t, int64_t o0) {
+    const int i = threadIdx.x;
+    if (i < ROWS) {
+        const char* w = reinterpret_cast<const char*>(p.w) + size_t(t.expert) * p.w_bytes;
+        return reinterpret_cast<const float*>(w + p.w_scales)[min(o0 + i, p.M - 1)];
+    }
+    const int64_t term = t.first + min(i - ROWS, t.n - 1), row = GROUP ? term_row(p, term) : term;
     return row < 0 ? __builtin_nanf("") : p.xs[row];
 }
 
 __device__ inline f32x4 values(i32x4 sum, float sx, f32x4 sw) {
     return f32x4{int8_value(sum[0], sx, sw[0]), int8_value(sum[1], sx, sw[1]), int8_value(sum[2], sx, sw[2]),
                  int8_value(sum[3], sx, sw[3])};
+}
+
+// The scaled sums of a wave's tile to Y: 16 FA outputs from o0 + wm on, strips of
+// 16 terms, SPREAD apart, from wt on.  They go through the wave's own part of
+// LDS (`mine`, JC strips at a time), so that a row's outputs leave in pieces of
+// 16 bytes side by side, or of 4 or 2 where M leaves rows no better aligned
+// (8 experts of 15486 x 523, 3784 terms, M = 2 mod 4: 143 us with stores from
+// registers).
+template <int YD, int FA> constexpr uint32_t out_pitch() { return FA * 16 * (YD == SKETCH_F32 ? 4 : 2) + 16; }
+template <int YD, int FA, int JC> constexpr uint32_t out_bytes() { return JC * 16 * out_pitch<YD, FA>(); }
+
+template <int YD, int FA, int FB, int SPREAD, int JC>
+__device__ inline void store_tile(const Int8Product& p, const Terms& t, const i32x4 (&acc)[FA][FB], int64_t o0, int wm,
+                                  int wt, const float* scales, int rows, unsigned char* mine) {
+    constexpr int es = YD == SKETCH_F32 ? 4 : 2;
+    constexpr uint32_t pitch = out_pitch<YD, FA>();
+    const int lane = threadIdx.x & 63, r = lane & 15, c = lane >> 4;
+    f32x4 so[FA];
+#pragma unroll
+    for (int i = 0; i < FA; ++i) so[i] = *reinterpret_cast<const f32x4*>(scales + wm + i * 16 + 4 * c);
+    float sx[FB];
+#pragma unroll
+    for (int j = 0; j < FB; ++j) sx[j] = scales[rows + j * SPREAD + wt + r];
+    const int left = int(min(p.M - o0 - wm, int64_t(FA * 16)));   // outputs that there are
+    if (left <= 0) return;
+    unsigned char* Y = static_cast<unsigned char*>(p.Y) + (int64_t(t.first) * p.M + o0 + wm) * es;
+    auto rows_out = [&](int j0, auto unit) {
+        typedef decltype(unit) U;
+        constexpr int per = FA * 16 * es / sizeof(U);
+#pragma unroll 4
+        for (int q = lane; q < JC * 16 * per; q += 64) {
+            const int row = q / per, at = q % per, n = (j0 + row / 16) * SPREAD + wt + row % 16;
+            if (n < t.n && at * int(sizeof(U)) < left * es)
+                *reinterpret_cast<U*>(Y + int64_t(n) * p.M * es + at * sizeof(U)) =
+                    *reinterpret_cast<const U*>(mine + row * pitch + at * sizeof(U));
+        }
+    };
+#pragma unroll
+    for (int j0 = 0; j0 < FB; j0 += JC) {
+        if (j0 * SPREAD + wt >= t.n) break;
+#pragma unroll
+        for (int j = j0; j < j0 + JC; ++j)
+#pragma unroll
+            for (int i = 0; i < FA; ++i) {
+                const f32x4 v = values(acc[i][j], sx[j], so[i]);
+                unsigned char* at = mine + ((j - j0) * 16 + r) * pitch + (i * 16 + 4 * c) * es;
+                if constexpr (YD == SKETCH_F32)
+                    *reinterpret_cast<f32x4*>(at) = v;
+                else
+                    *reinterpret_cast<uint2*>(at) = make_uint2(pack2<YD>(v[0], v[1]), pack2<YD>(v[2], v[3]));
+            }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        if (p.M * es % 16 == 0)
+            rows_out(j0, u32x4());
+        else if (p.M * es % 4 == 0)
+            rows_out(j0, uint32_t());
+        else
+            rows_out(j0, uint16_t());
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -75,7 +153,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
     const Int8Product& p = a.p;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int r = lane & 15, c = lane >> 4, group = wave >> 2, w4 = wave & 3, wm = group * FA * 16, wt = w4 * 64;
+    const int r = lane & 15, c = lane >> 4, group = wave >> 2, w4 = wave & 3, wm = group * FA * 16, wt = w4 * 16;
     constexpr int kRows = 32 * FA;
     constexpr int kTurns = (2 * FA + 3) / 4;   // loads of 8 rows that a wave has of its group's 16 FA rows of W
     int64_t o0;
@@ -97,6 +175,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
         if (gather) row = uint32_t(max(term_row(p, t.first + int(row)), int64_t(0)));   // x_rows * ld < 2^32 (the plan)
         xoff[i] = row * ld + piece;
     }
+    const float scale = tile_scale<kRows, 512 - kRows, GROUP>(p, t, o0);
     const uint32_t lds0 = lds_address(lds), lx = lds0 + 32768 + w4 * 1024;
     uint32_t lw[kTurns];
 #pragma unroll
@@ -109,152 +188,140 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     for (int i = 0; i < FA; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
-    i32x4 af[FA][2], bf[4][2];
     const unsigned char* frag = lds + r * 128 + ((c ^ (r & 7)) << 4);
     const unsigned char* frag2 = lds + r * 128 + (((c + 4) ^ (r & 7)) << 4);
-
-    auto read_step = [&](uint32_t k) {
-        const uint32_t st = (k & 1) * kBigStage;
-        const unsigned char *f1 = frag + st + wm * 128, *f2 = frag2 + st + wm * 128;
-        const unsigned char *g1 = frag + st + 32768 + wt * 128, *g2 = frag2 + st + 32768 + wt * 128;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            bf[j][0] = *reinterpret_cast<const i32x4*>(g1 + j * 2048);
-            bf[j][1] = *reinterpret_cast<const i32x4*>(g2 + j * 2048);
-        }
-#pragma unroll
-        for (int i = 0; i < FA; ++i) {
-            af[i][0] = *reinterpret_cast<const i32x4*>(f1 + i * 2048);
-            af[i][1] = *reinterpret_cast<const i32x4*>(f2 + i * 2048);
-        }
-    };
-    // the step's MFMAs, with between(n) among them, n < 2 FA
-    auto compute = [&](auto between) {
-        __builtin_amdgcn_s_setprio(1);
-#pragma unroll
-        for (int n = 0; n < 2 * FA; ++n) {
-            const int i = n >> 1, h = n & 1;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(af[i][h], bf[j][h], acc[i][j], 0, 0, 0);
-            __builtin_amdgcn_sched_barrier(0);
-            between(n);
-            __builtin_amdgcn_sched_barrier(0);
-        }
-        __builtin_amdgcn_s_setprio(0);
-    };
-
     const uint32_t last = p.kb - 1;
-    constexpr int kLoads = 8 + kTurns;   // of a wave of group 1
-#pragma unroll
-    for (uint32_t k = 0; k < 2; ++k) {
-#pragma unroll
-        for (int i = 0; i < kTurns; ++i) load_w(min(k, last), k, i);
-        if (group == 1) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) load_x(min(k, last), k, i);
-        }
-    }
-    wait_loads();
-    barrier();
-    if (group == 0) {
-        for (uint32_t k = 0; k < p.kb; ++k) {
-            read_step(k);
-            wait_lds();
-            barrier();
-            compute([&](int n) {
-                if (n % 2 == 0 && n / 2 < kTurns) load_w(min(k + 2, last), k & 1, n / 2);
-            });
-            asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kTurns) : "memory");   // step k + 1 is here
-            barrier();
-        }
-        barrier();
-    } else {
-        barrier();
-        for (uint32_t k = 0; k < p.kb; ++k) {
-            read_step(k);
-            wait_lds();
-            wait_loads();   // step k + 1 is here
-            barrier();
-            compute([&](int n) {
-#pragma unroll
-                for (int i = n * kLoads / (2 * FA); i < (n + 1) * kLoads / (2 * FA); ++i) {
-                    if (i < 8)
-                        load_x(min(k + 2, last), k & 1, i);
-                    else
-                        load_w(min(k + 2, last), k & 1, i - 8);
-                }
-            });
-            barrier();
-        }
-    }
-    wait_loads();
 
-    const float* sw = reinterpret_cast<const float*>(reinterpret_cast<const char*>(p.w) + size_t(t.expert) * p.w_bytes + p.w_scales);
-    f32x4 so[FA];
-    const int64_t m_last = (p.M - 1) & ~int64_t(3);
+    // the products of the first NJ strips of 64 terms
+    auto run = [&](auto strips) {
+        constexpr int NJ = decltype(strips)::value;
+        i32x4 af[FA][2], bf[NJ][2];
+        auto read_step = [&](uint32_t k) {
+            const uint32_t st = (k & 1) * kBigStage;
+            const unsigned char *f1 = frag + st + wm * 128, *f2 = frag2 + st + wm * 128;
+            const unsigned char *g1 = frag + st + 32768 + wt * 128, *g2 = frag2 + st + 32768 + wt * 128;
 #pragma unroll
-    for (int i = 0; i < FA; ++i) so[i] = *reinterpret_cast<const f32x4*>(sw + min(o0 + wm + i * 16 + 4 * c, m_last));
-    float sx[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) sx[j] = term_scale(p, GROUP, t.first + min(wt + j * 16 + r, t.n - 1));
-    // 16-bit rows go out through LDS, 256 contiguous bytes of a term's row and
-    // more at a time, where their pieces are aligned
-    if (YD != SKETCH_F32 && p.M % 8 == 0) {
-        constexpr uint32_t kRow = FA * 32;   // bytes of a term's outputs in the wave's tile
-        unsigned char* mine = lds + wave * (64 * kRow);
-        barrier();   // every wave is done reading its fragments
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
+            for (int j = 0; j < NJ; ++j) {
+                bf[j][0] = *reinterpret_cast<const i32x4*>(g1 + j * 8192);
+                bf[j][1] = *reinterpret_cast<const i32x4*>(g2 + j * 8192);
+            }
 #pragma unroll
             for (int i = 0; i < FA; ++i) {
-                const f32x4 v = values(acc[i][j], sx[j], so[i]);
-                *reinterpret_cast<uint2*>(mine + (j * 16 + r) * kRow + i * 32 + c * 8) =
-                    make_uint2(pack2<YD>(v[0], v[1]), pack2<YD>(v[2], v[3]));
+                af[i][0] = *reinterpret_cast<const i32x4*>(f1 + i * 2048);
+                af[i][1] = *reinterpret_cast<const i32x4*>(f2 + i * 2048);
             }
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        uint16_t* Y = static_cast<uint16_t*>(p.Y) + int64_t(t.first + wt) * p.M + o0 + wm;
-        const int64_t left = p.M - o0 - wm;
+        };
+        // the step's MFMAs, with between(n) among them, n < 2 FA
+        auto compute = [&](auto between) {
+            __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-        for (uint32_t n = 0; n < 64 * kRow / 1024; ++n) {
-            const uint32_t at = n * 1024 + lane * 16, row = at / kRow, m = at % kRow / 2;
-            if (wt + int(row) < t.n && int64_t(m) < left)
-                *reinterpret_cast<u32x4*>(Y + int64_t(row) * p.M + m) = *reinterpret_cast<const u32x4*>(mine + at);
+            for (int n = 0; n < 2 * FA; ++n) {
+                const int i = n >> 1, h = n & 1;
+#pragma unroll
+                for (int j = 0; j < NJ; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(af[i][h], bf[j][h], acc[i][j], 0, 0, 0);
+                __builtin_amdgcn_sched_barrier(0);
+                between(n);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            __builtin_amdgcn_s_setprio(0);
+        };
+        constexpr int kLoads = 2 * NJ + kTurns;   // of a wave of group 1
+#pragma unroll
+        for (uint32_t k = 0; k < 2; ++k) {
+#pragma unroll
+            for (int i = 0; i < kTurns; ++i) load_w(min(k, last), k, i);
+            if (group == 1) {
+#pragma unroll
+                for (int i = 0; i < 2 * NJ; ++i) load_x(min(k, last), k, i);
+            }
         }
-        return;
-    }
-    const bool vec = p.M % 4 == 0;
+        wait_loads();
+        barrier();
+        if (group == 0) {
+            for (uint32_t k = 0; k < p.kb; ++k) {
+                read_step(k);
+                wait_lds();
+                barrier();
+                compute([&](int n) {
+                    if (n % 2 == 0 && n / 2 < kTurns) load_w(min(k + 2, last), k & 1, n / 2);
+                });
+                asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kTurns) : "memory");   // step k + 1 is here
+                barrier();
+            }
+            barrier();
+        } else {
+            barrier();
+            for (uint32_t k = 0; k < p.kb; ++k) {
+                read_step(k);
+                wait_lds();
+                wait_loads();   // step k + 1 is here
+                barrier();
+                compute([&](int n) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int n = wt + j * 16 + r;
-        if (n >= t.n) continue;
-#pragma unroll
-        for (int i = 0; i < FA; ++i) {
-            const int64_t m = o0 + wm + i * 16 + 4 * c;
-            store4<YD>(p.Y, int64_t(t.first + n) * p.M + m, values(acc[i][j], sx[j], so[i]), m, p.M, vec);
+                    for (int i = n * kLoads / (2 * FA); i < (n + 1) * kLoads / (2 * FA); ++i) {
+                        if (i < 2 * NJ)
+                            load_x(min(k + 2, last), k & 1, i);
+                        else
+                            load_w(min(k + 2, last), k & 1, i - 2 * NJ);
+                    }
+                });
+                barrier();
+            }
         }
-    }
+        wait_loads();
+    };
+    if (t.n > 192)
+        run(std::integral_constant<int, 4>());
+    else if (t.n > 128)
+        run(std::integral_constant<int, 3>());
+    else if (t.n > 64)
+        run(std::integral_constant<int, 2>());
+    else
+        run(std::integral_constant<int, 1>());
+
+    barrier();   // every wave is done reading its fragments
+    constexpr int JC = YD == SKETCH_F32 ? 1 : 2;
+    constexpr uint32_t parts = 8 * out_bytes<YD, FA, JC>();
+    static_assert(parts + 2048 <= kBigLds, "the waves' parts of LDS and the scales");
+    float* scales = reinterpret_cast<float*>(lds + parts);
+    scales[tid] = scale;
+    __syncthreads();
+    store_tile<YD, FA, 4, 64, JC>(p, t, acc, o0, wm, wt, scales, kRows, lds + wave * out_bytes<YD, FA, JC>());
 }
 
 // ---------------------------------------------------------------------------
-// 32 FA outputs x 32 FB terms, 4 waves of 16 FA x 16 FB, two workgroups to a CU:
-// for fewer tiles than the big kernel needs.  The loads of the next step go out
-// first.  K is split over blockIdx.y when the tiles alone leave compute units
+// 32 FA outputs x up to 128 terms, 4 waves of 16 FA x 64, two workgroups to a CU,
+// which share its LDS: for fewer terms than the big kernel needs, down to those
+// whose time is the way of W from memory.  A wave's terms are strips of 16, 32
+// apart, so that a tile of few terms leaves out whole strips, with their loads, and
+// has LDS for more steps in flight instead.
+// K is split over blockIdx.y when the tiles alone leave compute units
 // idle; the parts are the 32-bit sums, rows padded to 4 outputs, and
 // int8_add_kernel adds them.
 // ---------------------------------------------------------------------------
-template <int FA, int FB> constexpr uint32_t mid_stage() { return (32 * FA + 32 * FB) * 128; }
-template <int FA, int FB> constexpr uint32_t mid_lds() { return 2 * mid_stage<FA, FB>(); }
+constexpr uint32_t mid_lds(int groups) { return 163840 / groups / 1024 * 1024; }   // of one of so many workgroups to a CU
 
-template <int YD, int FA, int FB, bool GROUP>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void int8_gemm_kernel(GemmArgs a) {
-    static_assert(FA <= 4 && FB <= 4, "a wave loads FA times 8 rows of W and FB times 8 of X");
+// Steps of 32 NJ rows of X and of 32 FA rows of W that LDS holds: up to 4 of
+// both, or one more of W, which comes from further away, where that fits.
+template <int FA, int NJ, int WGS> constexpr int mid_steps_x() {
+    return (FA + NJ) * 4 * 4096 <= int(mid_lds(WGS)) ? 4 : int(mid_lds(WGS)) / ((FA + NJ) * 4096);
+}
+template <int FA, int NJ, int WGS> constexpr int mid_steps_w() {
+    constexpr int x = mid_steps_x<FA, NJ, WGS>();
+    return x < 4 && (x * NJ + (x + 1) * FA) * 4096 <= int(mid_lds(WGS)) ? x + 1 : x;
+}
+
+template <int N>
+__device__ inline void wait_until() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory"); }
+
+template <int YD, int FA, int FB, int WGS, bool GROUP>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(WGS, WGS))) void int8_gemm_kernel(GemmArgs a) {
     constexpr int kRows = 32 * FA;
     extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
     const Int8Product& p = a.p;
-    constexpr uint32_t stage = mid_stage<FA, FB>();
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int r = lane & 15, c = lane >> 4, wm = (wave >> 1) * 16 * FA, wt = (wave & 1) * 16 * FB;
+    const int r = lane & 15, c = lane >> 4, wm = (wave >> 1) * 16 * FA, wt = (wave & 1) * 16;
     int64_t o0;
     Terms t;
     if (!my_tile<kRows, 32 * FB, GROUP>(a, o0, t)) return;
@@ -277,61 +344,93 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
         else
             xoff[i] = uint32_t(row) * ld + piece;
     }
-    const uint32_t lds0 = lds_address(lds), lw = lds0 + wave * 1024, lx = lw + kRows * 128;
-    auto load_part = [&](uint32_t k, int i) {   // i < 4
-        const uint32_t st = ((k - kbeg) & 1) * stage;
-        if (i < FA) dma16(wbase + size_t(k) * 128, woff[i], lw + st + i * 4096);
-        if (i < FB) {
-            if constexpr (GROUP)
-                dma16_at(xat[i] + size_t(k) * 128, lx + st + i * 4096);
-            else
-                dma16(xbase + size_t(k) * 128, xoff[i], lx + st + i * 4096);
-        }
-    };
+    const float scale = tile_scale<kRows, 256 - kRows, GROUP>(p, t, o0);
+    const uint32_t lds0 = lds_address(lds) + wave * 1024;
+    const uint32_t frag = r * 128 + ((c ^ (r & 7)) << 4), frag2 = r * 128 + (((c + 4) ^ (r & 7)) << 4);
 
     i32x4 acc[FA][FB];
 #pragma unroll
     for (int i = 0; i < FA; ++i)
 #pragma unroll
         for (int j = 0; j < FB; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
-    const unsigned char* frag = lds + r * 128 + ((c ^ (r & 7)) << 4);
-    const unsigned char* frag2 = lds + r * 128 + (((c + 4) ^ (r & 7)) << 4);
 
-    if (kbeg < kend)
+    auto run = [&](auto strips) {
+        constexpr int NJ = decltype(strips)::value, SX = mid_steps_x<FA, NJ, WGS>(), SW = mid_steps_w<FA, NJ, WGS>();
+        static_assert(SX >= 2 && SX <= 4 && SW - SX <= 1 && (SW * FA + SX * NJ) * 4096 <= int(mid_lds(WGS)), "rings of steps");
+        constexpr uint32_t w_step = FA * 4096, x_step = NJ * 4096, x0 = SW * w_step;
+        auto next = [](uint32_t at, uint32_t step, uint32_t steps) { return at + step == steps * step ? 0 : at + step; };
+        uint32_t w_to = 0, x_to = 0, w_from = 0, x_from = 0;   // where the next step goes, and the current one lies
+        auto load_w = [&](uint32_t k) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) load_part(kbeg, i);
-    for (uint32_t k = kbeg; k < kend; ++k) {
-        wait_loads();
-        barrier();   // step k is here, and every wave is done with step k - 1
-        if (k + 1 < kend)
+            for (int i = 0; i < FA; ++i) dma16(wbase + size_t(k) * 128, woff[i], lds0 + w_to + i * 4096);
+            w_to = next(w_to, w_step, SW);
+        };
+        auto load_x = [&](uint32_t k) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) load_part(k + 1, i);
-        const uint32_t st = ((k - kbeg) & 1) * stage;
-        const unsigned char* f[2] = {frag + st + wm * 128, frag2 + st + wm * 128};
-        const unsigned char* g[2] = {frag + st + (kRows + wt) * 128, frag2 + st + (kRows + wt) * 128};
-        i32x4 af[FA][2], bf[FB][2];
+            for (int i = 0; i < NJ; ++i) {
+                if constexpr (GROUP)
+                    dma16_at(xat[i] + size_t(k) * 128, lds0 + x0 + x_to + i * 4096);
+                else
+                    dma16(xbase + size_t(k) * 128, xoff[i], lds0 + x0 + x_to + i * 4096);
+            }
+            x_to = next(x_to, x_step, SX);
+        };
+        // in the order of the steps, X of one before the W that goes out with it
+        if (SW > SX && kbeg < kend) load_w(kbeg);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-#pragma unroll
-            for (int j = 0; j < FB; ++j) bf[j][h] = *reinterpret_cast<const i32x4*>(g[h] + j * 2048);
-#pragma unroll
-            for (int i = 0; i < FA; ++i) af[i][h] = *reinterpret_cast<const i32x4*>(f[h] + i * 2048);
+        for (uint32_t n = 0; n < SX - 1; ++n) {
+            if (kbeg + n < kend) load_x(kbeg + n);
+            if (kbeg + n + (SW - SX) < kend) load_w(kbeg + n + (SW - SX));
         }
+        for (uint32_t k = kbeg; k < kend; ++k) {
+            // what follows X of this step may stay on its way: W of the step that went out with it, and later steps
+            constexpr int kAhead = SW > SX ? FA : 0;
+            if (SX > 3 && k + 2 < kend)
+                wait_until<2 * (FA + NJ)>();
+            else if (SX > 2 && k + 1 + (SW - SX) < kend)
+                wait_until<kAhead + FA + NJ>();
+            else if (SX == 2 && SW > SX && k + 1 < kend)
+                wait_until<kAhead>();
+            else
+                wait_loads();
+            barrier();   // step k is here, and every wave is done with step k - 1
+            if (k + SX - 1 < kend) load_x(k + SX - 1);
+            if (k + SW - 1 < kend) load_w(k + SW - 1);
+            const unsigned char *f = lds + w_from + wm * 128, *g = lds + x0 + x_from + wt * 128;
+            w_from = next(w_from, w_step, SW), x_from = next(x_from, x_step, SX);
+            i32x4 af[FA][2], bf[NJ][2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t at = h ? frag2 : frag;
 #pragma unroll
-            for (int i = 0; i < FA; ++i)
+                for (int j = 0; j < NJ; ++j) bf[j][h] = *reinterpret_cast<const i32x4*>(g + at + j * 4096);
 #pragma unroll
-                for (int j = 0; j < FB; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(af[i][h], bf[j][h], acc[i][j], 0, 0, 0);
-    }
+                for (int i = 0; i < FA; ++i) af[i][h] = *reinterpret_cast<const i32x4*>(f + at + i * 2048);
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int i = 0; i < FA; ++i)
+#pragma unroll
+                    for (int j = 0; j < NJ; ++j)
+                        acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(af[i][h], bf[j][h], acc[i][j], 0, 0, 0);
+        }
+    };
+    if (FB == 4 && t.n > 96)
+        run(std::integral_constant<int, FB>());
+    else if (FB == 4 && t.n > 64)
+        run(std::integral_constant<int, FB == 4 ? 3 : 1>());
+    else if (t.n > 32)
+        run(std::integral_constant<int, 2>());
+    else
+        run(std::integral_constant<int, 1>());
 
     if (!GROUP && a.splits > 1) {
         const int64_t ldy = (p.M + 3) / 4 * 4;
         int* part = a.parts + int64_t(blockIdx.y) * p.T * ldy;
 #pragma unroll
         for (int j = 0; j < FB; ++j) {
-            const int n = wt + j * 16 + r;
+            const int n = j * 32 + wt + r;
             if (n >= t.n) continue;
 #pragma unroll
             for (int i = 0; i < FA; ++i) {
@@ -341,23 +440,13 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
         }
         return;
     }
-    const float* sw = reinterpret_cast<const float*>(reinterpret_cast<const char*>(p.w) + size_t(t.expert) * p.w_bytes + p.w_scales);
-    const int64_t m_last = (p.M - 1) & ~int64_t(3);
-    f32x4 so[FA];
-#pragma unroll
-    for (int i = 0; i < FA; ++i) so[i] = *reinterpret_cast<const f32x4*>(sw + min(o0 + wm + i * 16 + 4 * c, m_last));
-    const bool vec = p.M % 4 == 0;
-#pragma unroll
-    for (int j = 0; j < FB; ++j) {
-        const int n = wt + j * 16 + r;
-        if (n >= t.n) continue;
-        const float sx = term_scale(p, GROUP, t.first + n);
-#pragma unroll
-        for (int i = 0; i < FA; ++i) {
-            const int64_t m = o0 + wm + i * 16 + 4 * c;
-            store4<YD>(p.Y, int64_t(t.first + n) * p.M + m, values(acc[i][j], sx, so[i]), m, p.M, vec);
-        }
-    }
+    barrier();   // every wave is done reading its fragments
+    constexpr uint32_t parts = 4 * out_bytes<YD, FA, FB>();
+    static_assert(parts + 1024 <= mid_lds(WGS) && kRows + 32 * FB <= 256, "the waves' parts of LDS and the scales");
+    float* scales = reinterpret_cast<float*>(lds + parts);
+    scales[tid] = scale;
+    __syncthreads();
+    store_tile<YD, FA, FB, 32, FB>(p, t, acc, o0, wm, wt, scales, kRows, lds + wave * out_bytes<YD, FA, FB>());
 }
 
 // Y from the parts, 4 outputs to a thread.
@@ -374,23 +463,110 @@ __global__ __launch_bounds__(256) void int8_add_kernel(GemmArgs a) {
     store4<YD>(p.Y, t * p.M + m, values(sum, p.xs[t], *reinterpret_cast<const f32x4*>(sw + m)), m, p.M, p.M % 4 == 0);
 }
 
+// What a product takes in us, by a model of the kernels: a sum of what one tile
+// takes by itself (its steps of 128 columns one after another), of the rounds that
+// the tiles make over the slots of the compute units, and of the work that they add up to
+// (tiles times steps, and strips of terms times steps); parts cost the launch
+// that adds them and their way to memory and back.  The figures are fitted to every
+// kernel and split, timed on 2000 products of one weight (64 x 64 to 28672 x
+// 16384, 2 to 2100 rows) and on 1500 grouped ones (4 to 128 experts, 1 to 24000 terms):
+// what the model takes is 2.8% and 3.2% slower than the fastest kernel on average,
+// at worst 45% and 57%, and the same on thirds of them that the fit had not seen.
+// One kernel of tiles of 128 x 128 in place of the set: 25% slower on average.
+struct TileCost {
+    int fa, fb, slots;   // outputs and terms of a tile in units of 32; workgroups that a compute unit holds
+    double call, step, round_step, round, tile_step, strip_step, strip, parts, part_bytes, byte;   // one weight
+    double g_call, g_step, g_round_step, g_round, g_tile_step, g_strip_step, g_strip;              // grouped
+};
+constexpr TileCost kCost[] = {
+    {1, 2, 4, 3.31, 0.148, 0.090, 0.0, 0.049, 0.012, 0.252, 2.27, 1.43, 0.0326, 4.71, 0.132, 0.085, 0.50, 0.039, 0.058, 0.063},
+    {2, 2, 4, 3.58, 0.159, 0.051, 0.067, 0.061, 0.033, 0.357, 2.17, 1.14, 0.0662, 4.75, 0.158, 0.101, 0.16, 0.201, 0.022, 0.154},
+    {2, 4, 2, 4.08, 0.146, 0.198, 0.0, 0.099, 0.035, 0.397, 2.03, 1.04, 0.0408, 0, 0, 0, 0, 0, 0, 0},
+    {4, 2, 2, 4.17, 0.193, 0.245, 0.0, 0.129, 0.029, 0.750, 2.08, 0.93, 0.0765, 5.30, 0.168, 0.0, 1.33, 0.478, 0.0, 0.324},
+    {4, 4, 2, 5.12, 0.186, 0.200, 0.0, 0.193, 0.049, 0.643, 1.32, 0.94, 0.0602, 5.91, 0.189, 0.099, 0.30, 0.442, 0.038, 0.699},
+    {8, 8, 1, 6.46, 0.748, 0.697, 3.68, 0.0, 0.143, 2.54, 0.0, 0.0, 0.0230, 5.62, 0.599, 0.749, 0.0, 0.289, 0.215, 3.56}};
+constexpr int64_t kMaxSplits = 16;
+constexpr double kFewPerExpert = 6;   // terms per expert up to which int8_rows_kernel was timed on groups
+
+// Tiles of up to BT terms that an expert of `mean` terms has on average, where the numbers of terms
+// fall off evenly (exponentially), as those of routed tokens about do.
+double tiles_per_expert(double mean, int64_t bt) { return (1 - exp(-mean)) / (1 - exp(-double(bt) / mean)); }
+
+Int8Plan choose_group(int64_t M, int64_t T, double kb, int experts, bool near) {
+    const double ncu = double(compute_units()), mean = double(T) / experts;
+    Int8Plan best{};
+    double least = 1e300;
+    auto consider = [&](const Int8Plan& g, double us) {
+        if (us < least) least = us, best = g;
+    };
+    for (const TileCost& c : kCost) {
+        const bool big = c.fa == 8;
+        if (c.g_call == 0 || (big && !near)) continue;
+        const double across = double((M + 32 * c.fa - 1) / (32 * c.fa)) * experts;
+        const double tiles = across * tiles_per_expert(mean, 32 * c.fb), strips = across * tiles_per_expert(mean, big ? 64 : 32);
+        const double rounds = fmax(tiles / ((big ? 1 : 2) * ncu), 1) - 1;   // of the rounds that the fit counts
+        consider({big ? kInt8Big : kInt8Mid, c.fa, c.fb, 1, 0, 0, 0},
+                 c.g_call + c.g_step * kb + rounds * (c.g_round_step * kb + c.g_round) +
+                     (c.g_tile_step * tiles + c.g_strip_step * strips) / ncu * kb + c.g_strip * strips / ncu);
+    }
+    if (mean <= kFewPerExpert) {
+        const double tiles = experts * tiles_per_expert(mean, 16) / ncu, one = double((M + 15) / 16) * tiles,
+                     two = double((M + 31) / 32) * tiles;
+        consider({kInt8Rows1, 0, 0, 1, 0, 0, 0}, 3.45 + 1.28 * ceil(kb / 32) + one * (2.31 * kb / 32 + 0.28));
+        consider({kInt8Rows2, 0, 0, 1, 0, 0, 0}, 3.67 + 1.33 * ceil(kb / 16) + two * (4.18 * kb / 32 + 0.155));
+    }
+    return best;
+}
+
+Int8Plan choose(int64_t M, int64_t T, uint32_t kb, bool near) {
+    const int64_t ncu = compute_units();
+    const double bytes = 128e-6 * double(M) * double(kb);
+    Int8Plan best{};
+    double least = 1e300;
+    auto consider = [&](const Int8Plan& g, double us) {
+        if (us < least) least = us, best = g;
+    };
+    for (const TileCost& c : kCost) {
+        const bool big = c.fa == 8;
+        if (big && (!near || T <= 64)) continue;
+        const int64_t across = (M + 32 * c.fa - 1) / (32 * c.fa), bt = 32 * c.fb, down = (T + bt - 1) / bt, strip = big ? 64 : 32;
+        for (int64_t n = 1; n <= kMaxSplits; ++n) {
+            if (n > 1 && (big || 2 * n > int64_t(kb) || across * down * n > 4 * ncu || T > 65535)) break;   // T: a grid's second dimension
+            const double tiles = double(across * down * n), strips = double(across * ((T + strip - 1) / strip) * n);
+            const double steps = ceil(double(kb) / double(n)), rounds = ceil(tiles / double((big ? 1 : 2) * ncu)) - 1;
+            double us = c.call + c.step * steps + rounds * (c.round_step * steps + c.round) +
+                        (c.tile_step * tiles + c.strip_step * strips) / double(ncu) * steps + c.strip * strips / double(ncu) + c.byte * bytes;
+            if (n > 1) us += c.parts + c.part_bytes * 1e-6 * double(n) * double(T) * double(M);
+            consider({big ? kInt8Big : kInt8Mid, c.fa, c.fb, uint32_t(n), 0, 0, 0}, us);
+        }
+    }
+    if (T <= 32) {
+        const double w = double((M + 15) / 16 * ((T + 15) / 16)) / double(ncu), x = fmax(0, w - 1), k = kb / 32.0,
+                     t = double(T < 16 ? T : 16) / 16;
+        consider({kInt8Rows1, 0, 0, 1, 0, 0, 0}, 2.94 + k * (2.40 + 1.34 * t) + x * (k * (2.74 + 0.56 * t) + 0.385) + (bytes > 60 ? 0.0114 * bytes : 0));
+    }
+    return best;
+}
+
 template <int YD, bool GROUP>
 sketch_status launch(const GemmArgs& a, const Int8Plan& g, hipStream_t st) {
     const int64_t tiles = g.tiles_o * g.tiles_t;
-    if (g.big) {
-        auto go = [&](auto kernel) { kernel<<<unsigned(tiles), 512, kBigLds, st>>>(a); };
-        g.fa == 8   ? go(int8_gemm_big_kernel<YD, 8, GROUP>)
-        : g.fa == 7 ? go(int8_gemm_big_kernel<YD, 7, GROUP>)
-                    : go(int8_gemm_big_kernel<YD, 6, GROUP>);
+    if (g.kind == kInt8Big) {
+        int8_gemm_big_kernel<YD, 8, GROUP><<<unsigned(tiles), 512, kBigLds, st>>>(a);
         return launch_status();
     }
     const dim3 grid(unsigned(tiles), g.splits);
-    if (g.fb == 2)
-        int8_gemm_kernel<YD, 4, 2, GROUP><<<grid, 256, mid_lds<4, 2>(), st>>>(a);
+    auto go = [&](auto kernel, int slots) { kernel<<<grid, 256, mid_lds(slots), st>>>(a); };
+    if (g.fa == 1)
+        go(int8_gemm_kernel<YD, 1, 2, 4, GROUP>, 4);
+    else if (g.fa == 2 && g.fb == 2)
+        go(int8_gemm_kernel<YD, 2, 2, 4, GROUP>, 4);
+    else if (g.fb == 2)
+        go(int8_gemm_kernel<YD, 4, 2, 2, GROUP>, 2);
     else if (g.fa == 4)
-        int8_gemm_kernel<YD, 4, 4, GROUP><<<grid, 256, mid_lds<4, 4>(), st>>>(a);
-    else
-        int8_gemm_kernel<YD, 3, 4, GROUP><<<grid, 256, mid_lds<3, 4>(), st>>>(a);
+        go(int8_gemm_kernel<YD, 4, 4, 2, GROUP>, 2);
+    else if constexpr (!GROUP)
+        go(int8_gemm_kernel<YD, 2, 4, 2, false>, 2);
     if (g.splits == 1) return launch_status();
     if (hipGetLastError() != hipSuccess) return SKETCH_EDEVICE;
     int8_add_kernel<YD><<<dim3(unsigned((a.p.M + 1023) / 1024), unsigned(a.p.T)), 256, 0, st>>>(a);
@@ -399,16 +575,14 @@ sketch_status launch(const GemmArgs& a, const Int8Plan& g, hipStream_t st) {
 
 }  // namespace
 
-sketch_status int8_gemm_plan(int64_t M, int64_t T, uint32_t kb, int experts, bool group, bool near, Int8Plan* g) {
-    *g = Int8Plan{};
-    const int64_t ncu = compute_units();
-    g->big = (M + 255) / 256 * ((T + 255) / 256) >= ncu / 2 && near;
-    g->fa = g->big ? 8 : 4, g->fb = g->big ? 8 : 4, g->splits = 1;
+sketch_status int8_plan(int64_t M, int64_t T, uint32_t kb, int experts, bool group, bool near, Int8Plan* g) {
+    *g = group ? choose_group(M, T, kb, experts, near) : choose(M, T, kb, near);
+    if (g->kind == kInt8Rows1 || g->kind == kInt8Rows2) return SKETCH_OK;   // their launch counts its own workgroups
     const int64_t rows = 32 * g->fa, cols = 32 * g->fb;
     g->tiles_o = (M + rows - 1) / rows;
     g->tiles_t = (T + cols - 1) / cols + (group ? min(T, int64_t(experts)) : 0);
     g->workspace = g->splits > 1 ? align256(size_t(g->splits) * size_t((M + 3) / 4 * 4) * size_t(T) * 4) : 0;
-    return g->tiles_o * g->tiles_t > kMaxThreads / (g->big ? 512 : 256) ? SKETCH_EINVAL : SKETCH_OK;
+    return g->tiles_o * g->tiles_t > kMaxThreads / (g->kind == kInt8Big ? 512 : 256) ? SKETCH_EINVAL : SKETCH_OK;
 }
 
 sketch_status launch_int8_gemm(const Int8Product& p, const Int8Plan& g, void* ws, hipStream_t st) {
