@@ -111,7 +111,7 @@ sketch_status sketch_int8_workspace_bytes(const sketch_int8_params* p, int64_t b
  * is with more than SKETCH_INT8_TOKENS rows that are not SKETCH_INT8_ROWS; any
  * other overlap of Y or the workspace with another buffer gives SKETCH_EINVAL.
  */
-#define SKETCH_INT8_TOKENS 4
+#define SKETCH_INT8_TOKENS 16
 sketch_status sketch_int8_matmul(const sketch_int8_params* p, const void* buf, const void* X, int x_dtype,
                                  int64_t batch, void* Y, int y_dtype, void* workspace, size_t workspace_bytes,
                                  void* stream);
@@ -144,9 +144,8 @@ sketch_status sketch_int8_group_workspace_bytes(const sketch_int8_params* p, int
  *            expert are left as they were.
  * The counts are read on the device, so routing needs no wait of the host.  A
  * term whose row lies outside 0..x_rows-1 gives a row of NaN.  terms == 0 or
- * M == 0 is a no-op.  Y may share memory with X where X is not SKETCH_INT8_ROWS
- * (it is encoded into the workspace first); any other overlap of Y or the
- * workspace with another buffer gives SKETCH_EINVAL.
+ * M == 0 is a no-op.  Overlap of Y or the workspace with another buffer gives
+ * SKETCH_EINVAL.
  */
 sketch_status sketch_int8_matmul_group(const sketch_int8_params* p, const void* buf, const void* X, int x_dtype,
                                        int64_t x_rows, const sketch_int8_groups* g, void* Y, int y_dtype,

@@ -1,6 +1,8 @@
 // int8.hip -- matrices held as 8-bit integers with a float32 scale for each
 // row: their encoders, and the products Y = X8 * W8^T of few rows, for one weight
 // or for a stack of them with the rows grouped by expert.
+#include <type_traits>
+
 #include "int8.h"
 #include "tile.h"
 
@@ -388,84 +390,99 @@ __global__ __launch_bounds__(WAVES * 64) void int8_rows_kernel(Int8Product p) {
 }
 
 // ---------------------------------------------------------------------------
-// Product of up to NP rows of X (p.x, of dtype XD), encoded by every workgroup for
+// The same for up to 16 rows of X (p.x, of dtype XD) that every workgroup encodes for
 // itself, which saves the launch that would encode them first: 16 outputs to a
-// workgroup, whose 8 waves share out the columns in runs of 4 blocks, as above.  The
-// loads of W go out first; while they are on their way the workgroup encodes X
-// into LDS, two chunks of 8 columns of each row to a thread from registers, what a
-// longer row has more read again.
+// workgroup of 8 waves.  The loads of W go out first; while they are on their way the
+// rows are encoded into LDS, a single one by the whole workgroup, several by a wave
+// each, 8 columns to a lane at a time; what a row has more than the lanes keep is read
+// again.
 // ---------------------------------------------------------------------------
 constexpr uint32_t kTokenCodes = 32768;   // bytes of codes that LDS holds, with 64 more for each row
-constexpr int kTokens = SKETCH_INT8_TOKENS;
 
-template <int XD, int NP>
+template <int XD, bool GROUP>
 __global__ __launch_bounds__(512) void int8_tokens_kernel(Int8Product p, int64_t N) {
-    extern __shared__ __attribute__((aligned(16))) uint8_t codes[];   // [NP][ld + 64]
-    __shared__ uint32_t red[8][NP];
+    extern __shared__ __attribute__((aligned(16))) uint8_t codes[];   // [min(16, T)][ld + 64]
+    __shared__ uint32_t red[16];
     __shared__ __attribute__((aligned(16))) int part[8][16][20];
-    constexpr int RUN = 4;
+    constexpr int RUN = 4, es = XD == SKETCH_F32 ? 4 : 2;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int r = lane & 15, c = lane >> 4, T = int(p.T), pitch = int(p.ld) + 64, chunks = int(p.ld / 8);
-    const int64_t m0 = int64_t(blockIdx.x) * 16;
-    const int8_t* wrow = p.w + min(m0 + r, p.M - 1) * p.ld;
+    const int r = lane & 15, c = lane >> 4, pitch = int(p.ld) + 64, chunks = int(p.ld / 8);
+    const int64_t tiles_o = (p.M + 15) / 16, tile = GROUP ? blockIdx.x / tiles_o : 0;
+    const int64_t m0 = (blockIdx.x - tile * tiles_o) * 16;
+    Terms t{0, 0, int(p.T)};
+    if (GROUP && !find_terms<16>(p, [&](int) { return int(tile); }, t)) return;
+    const int8_t* w = p.w + size_t(t.expert) * p.w_bytes;
+    const int8_t* wrow = w + min(m0 + r, p.M - 1) * p.ld;
     const uint32_t k0 = wave * RUN;
     Frag a[RUN];
 #pragma unroll
     for (int u = 0; u < RUN; ++u) a[u].load(wrow, min(k0 + u, p.kb - 1), c);
     asm volatile("" ::: "memory");   // on their way before X is asked for
 
-    constexpr int es = XD == SKETCH_F32 ? 4 : 2;
-    auto row_of = [&](int n) { return static_cast<const char*>(static_cast<const void*>(p.x)) + int64_t(min(n, T - 1)) * N * es; };
-    float v[NP][2][8];
-    uint32_t bits[NP];
+    auto row_at = [&](int n) {
+        const int64_t row = GROUP ? max(term_row(p, t.first + n), int64_t(0)) : n;
+        return reinterpret_cast<const char*>(p.x) + row * N * es;
+    };
+    // row n by `lanes` threads, `at` this one's place among them, KEPT chunks of a thread kept
+    auto encode = [&](int n, int at, auto lanes_c, auto kept_c, auto maximum) {
+        constexpr int LANES = decltype(lanes_c)::value, KEPT = decltype(kept_c)::value;
+        const char* x = row_at(n);
+        float v[KEPT][8];
+        uint32_t bits = 0;
 #pragma unroll
-    for (int n = 0; n < NP; ++n) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            if (tid + i * 512 < chunks) {
-                load_row8<XD>(row_of(n), 0, N, (tid + i * 512) * 8, v[n][i]);
+        for (int i = 0; i < KEPT; ++i) {
+            if (at + i * LANES < chunks) {
+                load_row8<XD>(x, 0, N, (at + i * LANES) * 8, v[i]);
             } else {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[n][i][e] = 0.0f;
+                for (int e = 0; e < 8; ++e) v[i][e] = 0.0f;
             }
         }
-    }
 #pragma unroll
-    for (int n = 0; n < NP; ++n) {
-        bits[n] = max(max_bits(v[n][0]), max_bits(v[n][1]));
-        for (int q = tid + 1024; q < chunks; q += 512) {
-            float x[8];
-            load_row8<XD>(row_of(n), 0, N, int64_t(q) * 8, x);
-            bits[n] = max(bits[n], max_bits(x));
+        for (int i = 0; i < KEPT; ++i) bits = max(bits, max_bits(v[i]));
+        for (int q = at + KEPT * LANES; q < chunks; q += LANES) {
+            float y[8];
+            load_row8<XD>(x, 0, N, int64_t(q) * 8, y);
+            bits = max(bits, max_bits(y));
         }
 #pragma unroll
-        for (int d = 1; d < 64; d <<= 1) bits[n] = max(bits[n], uint32_t(__shfl_xor(int(bits[n]), d)));
-        if (lane == 0) red[wave][n] = bits[n];
-    }
-    __syncthreads();
-#pragma unroll
-    for (int n = 0; n < NP; ++n) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) bits[n] = max(bits[n], red[i][n]);
-        if (n >= T) break;
-        const bool bad = bits[n] >= 0x7F800000u;
-        const Rounder<XD> round(bad || bits[n] == 0 ? 1.0f : __uint_as_float(bits[n]));
-        auto put = [&](int q, const float (&x)[8]) {
-            *reinterpret_cast<uint2*>(codes + n * pitch + q * 8) = bad ? make_uint2(0, 0) : codes8<XD>(x, round);
+        for (int d = 1; d < 64; d <<= 1) bits = max(bits, uint32_t(__shfl_xor(int(bits), d)));
+        bits = maximum(bits);
+        const bool bad = bits >= 0x7F800000u;
+        const Rounder<XD> round(bad || bits == 0 ? 1.0f : __uint_as_float(bits));
+        auto put = [&](int q, const float (&y)[8]) {
+            *reinterpret_cast<uint2*>(codes + n * pitch + q * 8) = bad ? make_uint2(0, 0) : codes8<XD>(y, round);
         };
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            if (tid + i * 512 < chunks) put(tid + i * 512, v[n][i]);
-        for (int q = tid + 1024; q < chunks; q += 512) {
-            float x[8];
-            load_row8<XD>(row_of(n), 0, N, int64_t(q) * 8, x);
-            put(q, x);
+        for (int i = 0; i < KEPT; ++i)
+            if (at + i * LANES < chunks) put(at + i * LANES, v[i]);
+        for (int q = at + KEPT * LANES; q < chunks; q += LANES) {
+            float y[8];
+            load_row8<XD>(x, 0, N, int64_t(q) * 8, y);
+            put(q, y);
+        }
+        return bits;
+    };
+    if (t.n == 1) {
+        const uint32_t bits = encode(0, tid, std::integral_constant<int, 512>(), std::integral_constant<int, 2>(), [&](uint32_t m) {
+            if (lane == 0) red[wave + 8] = m;
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) m = max(m, red[i + 8]);
+            return m;
+        });
+        if (tid == 0) red[0] = bits;
+    } else {
+        for (int n = wave; n < t.n; n += 8) {
+            const uint32_t bits =
+                encode(n, lane, std::integral_constant<int, 64>(), std::integral_constant<int, 4>(), [](uint32_t m) { return m; });
+            if (lane == 0) red[n] = bits;
         }
     }
     __syncthreads();
 
     i32x4 acc = {0, 0, 0, 0};
-    const int8_t* xrow = reinterpret_cast<const int8_t*>(codes) + min(r, T - 1) * pitch;   // terms past the last are not stored
+    const int8_t* xrow = reinterpret_cast<const int8_t*>(codes) + min(r, t.n - 1) * pitch;   // terms past the last are not stored
     for (uint32_t k = k0; k < p.kb; k += 8 * RUN) {
         if (k != k0) {
 #pragma unroll
@@ -482,16 +499,14 @@ __global__ __launch_bounds__(512) void int8_tokens_kernel(Int8Product p, int64_t
     *reinterpret_cast<i32x4*>(&part[wave][r][4 * c]) = acc;
     __syncthreads();
     const int m = tid & 15, n = tid >> 4;
-    if (n >= T || m0 + m >= p.M) return;
+    if (n >= t.n || m0 + m >= p.M) return;
     int sum = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) sum += part[i][n][m];
-    uint32_t top = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) top = max(top, red[i][NP > 1 ? n : 0]);
-    const float sx = row_scale(top);
-    const float y = int8_value(sum, sx, reinterpret_cast<const float*>(reinterpret_cast<const char*>(p.w) + p.w_scales)[m0 + m]);
-    const int64_t at = n * p.M + m0 + m;
+    const int64_t term = t.first + n;
+    const float sx = GROUP && term_row(p, term) < 0 ? __builtin_nanf("") : row_scale(red[n]);
+    const float y = int8_value(sum, sx, reinterpret_cast<const float*>(reinterpret_cast<const char*>(w) + p.w_scales)[m0 + m]);
+    const int64_t at = term * p.M + m0 + m;
     if (p.ydt == SKETCH_F32)
         store1_val<SKETCH_F32>(p.Y, at, y);
     else if (p.ydt == SKETCH_BF16)
@@ -559,13 +574,18 @@ struct Plan {
     size_t workspace;
 };
 
-// Whether a product of raw rows encodes them in its own workgroups.  One row
-// always gains (11008 x 4096: 11.7 us, 14.2 with a launch of its own; 28672 x 8192
-// 45.1 and 45.3).  2 to 4 rows need registers that leave a compute unit one workgroup,
-// and gain where each has one only (4096 x 4096, 4 rows: 10.2 and 12.6 us; 11008 x
-// 4096 22.9 and 14.6).
-bool encodes_itself(int64_t M, int64_t rows, int64_t ld) {
-    return rows <= kTokens && rows * ld <= int64_t(kTokenCodes) && (rows == 1 || M <= 16 * int64_t(compute_units()));
+// Whether the workgroups of a product encode its raw rows themselves.  A single
+// row always gains or is even (435 x 4149 5.8 us, 8.7 with a launch of its own; 28672 x
+// 8192 45.1 and 45.3).  Several, up to 16384 codes, do where a compute unit has one
+// workgroup at most: on the GPU they are 15% faster to 15% slower (256 x 512, 2 rows 5.1 and
+// 6.1 us; 4096 x 1024, 15 rows 7.4 and 6.9), but a launch takes the host 4.5 us, and
+// calls this small wait for it (16 rows of 256 x 512 among others 12.1 and 7.5 us).
+// With more workgroups the work that they repeat outweighs that (20447 x 692, 8 rows 20 and 10 us).
+bool encodes_itself(int64_t M, int64_t terms, int64_t ld, int experts, bool group) {
+    if (!group && terms > 16) return false;
+    const int64_t rows = min(terms, int64_t(16)), tiles = group ? (terms + 15) / 16 + min(terms, int64_t(experts)) : 1;
+    return rows * ld <= int64_t(rows == 1 ? kTokenCodes : kTokenCodes / 2) &&
+           (terms == 1 || (M + 15) / 16 * tiles <= int64_t(compute_units()));
 }
 
 // Checks the parameters and fills the plan.
@@ -583,7 +603,7 @@ sketch_status make_plan(const sketch_int8_params* p, int64_t terms, int64_t x_ro
     plan->workspace = 0;
     plan->encode = false;
     if (terms == 0 || p->M == 0) return SKETCH_OK;
-    plan->encode = !rows && (group || !encodes_itself(p->M, terms, plan->x.ld));
+    plan->encode = !rows && !encodes_itself(p->M, terms, plan->x.ld, int(matrices(p)), group);
     if (plan->encode) plan->workspace += plan->x.bytes;
     if (!plan->encode && !rows) return SKETCH_OK;   // encoded by the product's own workgroups
     const bool near = x_rows * plan->x.ld <= int64_t(0xFFFFFFFF);
@@ -604,14 +624,21 @@ sketch_status launch_rows(const Int8Product& a, hipStream_t st) {
     return launch_status();
 }
 
-template <int NP>
+int64_t token_groups(const Int8Product& a) {
+    return (a.M + 15) / 16 * (a.counts ? (a.T + 15) / 16 + min(a.T, int64_t(a.experts)) : 1);
+}
+
 sketch_status launch_tokens(const Int8Product& a, int x_dtype, int64_t N, hipStream_t st) {
     auto go = [&](auto kernel) {
-        kernel<<<unsigned((a.M + 15) / 16), 512, unsigned(a.T * (a.ld + 64)), st>>>(a, N);
+        kernel<<<unsigned(token_groups(a)), 512, unsigned(min(a.T, int64_t(16)) * (a.ld + 64)), st>>>(a, N);
         return launch_status();
     };
-    if (x_dtype == SKETCH_F32) return go(int8_tokens_kernel<SKETCH_F32, NP>);
-    return x_dtype == SKETCH_BF16 ? go(int8_tokens_kernel<SKETCH_BF16, NP>) : go(int8_tokens_kernel<SKETCH_F16, NP>);
+    if (a.counts) {
+        if (x_dtype == SKETCH_F32) return go(int8_tokens_kernel<SKETCH_F32, true>);
+        return x_dtype == SKETCH_BF16 ? go(int8_tokens_kernel<SKETCH_BF16, true>) : go(int8_tokens_kernel<SKETCH_F16, true>);
+    }
+    if (x_dtype == SKETCH_F32) return go(int8_tokens_kernel<SKETCH_F32, false>);
+    return x_dtype == SKETCH_BF16 ? go(int8_tokens_kernel<SKETCH_BF16, false>) : go(int8_tokens_kernel<SKETCH_F16, false>);
 }
 
 sketch_status product(const sketch_int8_params* p, const void* buf, const void* X, int x_dtype, int64_t x_rows,
@@ -640,7 +667,7 @@ sketch_status product(const sketch_int8_params* p, const void* buf, const void* 
         rs{workspace, need}, rx{X, x_dtype == SKETCH_INT8_ROWS ? plan.x.bytes : extent(x_rows, p->N, p->N, x_dtype)},
         rcounts{g ? g->counts : nullptr, g ? size_t(count) * size_t(g->counts_bits / 8) : 0},
         rindex{index ? g->rows : nullptr, index ? size_t(terms) * size_t(g->rows_bits / 8) : 0};
-    if (((!plan.encode || (!g && terms <= kTokens)) && overlap(ry, rx)) || overlap(rs, ry) || overlap(rs, rx)) return SKETCH_EINVAL;
+    if (((g || !plan.encode || terms <= SKETCH_INT8_TOKENS) && overlap(ry, rx)) || overlap(rs, ry) || overlap(rs, rx)) return SKETCH_EINVAL;
     for (const Range& r : {rw, rcounts, rindex})
         if (overlap(ry, r) || overlap(rs, r)) return SKETCH_EINVAL;
     const hipStream_t st = static_cast<hipStream_t>(stream);
@@ -659,7 +686,7 @@ sketch_status product(const sketch_int8_params* p, const void* buf, const void* 
     a.experts = int(count);
     if (g) a.counts = g->counts, a.rows = g->rows, a.counts64 = g->counts_bits == 64, a.rows64 = g->rows_bits == 64;
     if (!plan.encode && x_dtype != SKETCH_INT8_ROWS)
-        return terms == 1 ? launch_tokens<1>(a, x_dtype, p->N, st) : launch_tokens<kTokens>(a, x_dtype, p->N, st);
+        return launch_tokens(a, x_dtype, p->N, st);
     if (plan.gemm.kind == kInt8Rows1) return launch_rows<8, 1, 1, 4>(a, st);
     if (plan.gemm.kind == kInt8Rows2) return launch_rows<4, 2, 1, 4>(a, st);
     return launch_int8_gemm(a, plan.gemm, workspace, st);

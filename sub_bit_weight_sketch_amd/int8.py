@@ -16,7 +16,7 @@ from . import OK, SketchError, _check, _ptr, _stream_handle, dtype_code, lib, sk
 from .fp8 import _aligned, _given, _need, _On, _out, _shared
 
 INT8_ROWS = 4               # x_dtype of rows that an encoder wrote
-INT8_TOKENS = 4             # rows that a product may encode as it reads them
+INT8_TOKENS = 16            # rows that a product may encode as it reads them
 INT8_MAX_N, INT8_MAX_M, INT8_MAX_EXPERTS = 131071, 1 << 24, 512
 INT8_EXPORTS = ("sketch_int8_layout", "sketch_int8_encode", "sketch_int8_swiglu", "sketch_int8_workspace_bytes",
                 "sketch_int8_matmul", "sketch_int8_group_workspace_bytes", "sketch_int8_matmul_group")
@@ -131,23 +131,23 @@ class Int8Tables:
     def __init__(self, M, N, count=None, device="cuda", buf=None):
         if count is not None and count < 1:
             raise ValueError("an empty stack of matrices")
-        stack = 1 if count is None else int(count)
-        self._M, self._N, self._count = int(M), int(N), None if count is None else stack
-        self._params, self._ref, self._layout = _shape(self._M, self._N, stack)
-        n = stack * self._layout.bytes
+        self._M, self._N, self._count = int(M), int(N), None if count is None else int(count)
+        self._params, self._ref, self._layout = _shape(self._M, self._N, self._count or 1)
+        n = (self._count or 1) * self._layout.bytes
         if buf is None:
-            buf = torch.empty(n, dtype=torch.uint8, device=device)
+            self._codes = torch.empty(n, dtype=torch.int8, device=device)
         else:
             _need(buf.dtype == torch.uint8 and buf.is_contiguous() and buf.numel() >= n and buf.data_ptr() % 16 == 0,
                   "the buffer must be %d dense, 16-byte aligned bytes" % n)
-        self._buf, self._device, self._at = buf, buf.device, buf.data_ptr()
+            self._codes = buf.view(-1).view(torch.int8)
+        self._device, self._at = self._codes.device, self._codes.data_ptr()
         self._ws = {}
 
     M = property(lambda self: self._M)
     N = property(lambda self: self._N)
     count = property(lambda self: self._count)
     device = property(lambda self: self._device)
-    buf = property(lambda self: self._buf)
+    buf = property(lambda self: self._codes.view(torch.uint8))
     params = property(lambda self: Int8Params.from_buffer_copy(self._params))
     layout = property(lambda self: Int8Shape.from_buffer_copy(self._layout))
 
@@ -155,21 +155,20 @@ class Int8Tables:
     def shape(self):
         return ((self._M, self._N) if self._count is None else (self._count, self._M, self._N))
 
-    def _view(self, kind, shape, strides, at):
-        """A view as elements of `kind`, from byte `at` of each matrix on."""
-        size, n = kind.itemsize, (1 if self._count is None else self._count) * self._layout.bytes
-        flat = self._buf[:n].view(kind)
-        if self._count is not None:
-            shape, strides = (self._count,) + shape, (self._layout.bytes // size,) + strides
-        return flat.as_strided(shape, strides, flat.storage_offset() + at // size)
-
     def codes(self):
         """The codes as an int8 view (rows are padded: not contiguous unless N % 128 == 0)."""
-        return self._view(torch.int8, (self._M, self._N), (self._layout.ld, 1), 0)
+        s, at = self._layout, self._codes.storage_offset()
+        if self._count is None:
+            return self._codes.as_strided((self._M, self._N), (s.ld, 1), at)
+        return self._codes.as_strided((self._count, self._M, self._N), (s.bytes, s.ld, 1), at)
 
     def scales(self):
         """The scales, float32 [M] (a view)."""
-        return self._view(torch.float32, (self._M,), (1,), self._layout.scales_offset)
+        s = self._layout
+        at = self._codes.storage_offset() + s.scales_offset
+        if self._count is None:
+            return self._codes.as_strided((4 * self._M,), (1,), at).view(torch.float32)
+        return self._codes.as_strided((self._count, 4 * self._M), (s.bytes, 1), at).view(torch.float32)
 
 
 def _row_stride(x):
@@ -362,7 +361,7 @@ def int8_matmul_group(t, X, counts, rows=None, out=None, workspace=None, dtype=N
     the Int8Tables of encoded rows.  dtype: of Y, float32 (the default, or that
     of `out`), bfloat16 or float16.  Rows of Y behind the last term are left as
     they were (an `out` that is not given holds anything there).  `out` may share
-    memory with X, not with the weights or with encoded rows."""
+    memory with X (a copy is made), not with the weights or with encoded rows."""
     if t._count is None:
         raise ValueError("t must be a stack of weights")
     shape, device = X.shape, t._device
@@ -380,6 +379,8 @@ def int8_matmul_group(t, X, counts, rows=None, out=None, workspace=None, dtype=N
         Y = torch.empty((terms, t._M), dtype=dtype, device=device) if out is None else \
             _out(out, (terms, t._M), dtype, device)
         ydt = dtype_code(Y)
+        if xdt != INT8_ROWS and out is not None and _shared(x, out):
+            x = x.clone()
         if workspace is None:
             wsb = _group_workspace_bytes(t, terms, shape[0], xdt, ydt)
             workspace = torch.empty(wsb, dtype=torch.uint8, device=device) if wsb else None

@@ -224,6 +224,14 @@ def test_product_types(x, y, b):
     check_product(weight(130, 400, 3), randn((b, 400), b, 1.0, x).to(dev()), y)
 
 
+@pytest.mark.parametrize("x", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("M,N", [(48, 1), (100, 2047), (33, 2049), (40, 5000), (40, 8200), (17, 16500), (16, 40000)])
+@pytest.mark.parametrize("b", [1, 2, 3, 4, 7, 9, 16])
+def test_product_of_raw_rows(M, N, b, x):
+    """Rows that the product encodes itself: shorter and longer than its lanes keep, up to what LDS holds and beyond."""
+    check_product(weight(M, N, M + N), randn((b, N), b, 1.0, x).to(dev()), "f32")
+
+
 @pytest.mark.parametrize("M,N,b", [(4096, 4096, 1), (11008, 4096, 16), (4099, 5003, 77), (4096, 1024, 300), (1024, 8192, 700),
                                    (2000, 1408, 1000), (128, 20000, 40), (70001, 65, 3), (16, 131071, 18), (64, 131071, 1),
                                    (8192, 2048, 2049)])
@@ -288,7 +296,7 @@ def test_out_workspace_strides_vectors():
     assert e.value.code == sk.ESMALL
 
 
-@pytest.mark.parametrize("b", [1, 4, 5, 16, 40, 200])
+@pytest.mark.parametrize("b", [1, 4, 5, 16, 17, 40, 200])
 def test_out_may_be_x(b):
     w = weight(256, 256, 4)
     X = randn((b, 256), 6).to(dev())

@@ -146,8 +146,8 @@ def test_group_validates_before_launching():
         assert size(ref(q), terms, xr, xdt, ydt, ref(n)) == sk.EINVAL
     assert size(ref(p), 4, 4, sk.BF16, sk.F32, None) == sk.EINVAL
     assert size(ref(p), 0, 4, sk.BF16, sk.F32, ref(n)) == sk.OK and n.value == 0
-    need = sk.sketch_int8_group_workspace_bytes(p, 12, 5, sk.BF16, sk.F32)
-    base = dict(w=1 << 20, x=1 << 24, xdt=sk.BF16, xr=5, terms=12, counts=1 << 25, cb=32, rows=1 << 26, rb=32, y=1 << 28,
+    need = sk.sketch_int8_group_workspace_bytes(p, 600, 5, sk.BF16, sk.F32)
+    base = dict(w=1 << 20, x=1 << 24, xdt=sk.BF16, xr=5, terms=600, counts=1 << 25, cb=32, rows=1 << 26, rb=32, y=1 << 28,
                 ydt=sk.F32, ws=1 << 32, wsb=need)
 
     def go(**change):
@@ -161,7 +161,7 @@ def test_group_validates_before_launching():
                 dict(rows=(1 << 26) + 2), dict(cb=64, counts=(1 << 25) + 4), dict(rb=64, rows=(1 << 26) + 4), dict(cb=16),
                 dict(rb=16), dict(rows=None), dict(xr=0), dict(xdt=3), dict(ydt=4), dict(terms=-1),
                 dict(y=1 << 20), dict(y=1 << 25), dict(y=1 << 26), dict(ws=1 << 20), dict(ws=1 << 24), dict(ws=1 << 25),
-                dict(ws=1 << 26), dict(ws=1 << 28), dict(xdt=sk.INT8_ROWS, y=1 << 24)):
+                dict(ws=1 << 26), dict(ws=1 << 28), dict(y=1 << 24), dict(xdt=sk.INT8_ROWS, y=1 << 24)):
         assert go(**bad) == sk.EINVAL, bad
     assert go(wsb=need - 1) == sk.ESMALL
     assert go(terms=0, w=None, x=None, y=None, counts=None, rows=None, ws=None) == sk.OK
