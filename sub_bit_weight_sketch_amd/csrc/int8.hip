@@ -582,7 +582,7 @@ struct Plan {
 // calls this small wait for it (16 rows of 256 x 512 among others 12.1 and 7.5 us).
 // With more workgroups the work that they repeat outweighs that (20447 x 692, 8 rows 20 and 10 us).
 bool encodes_itself(int64_t M, int64_t terms, int64_t ld, int experts, bool group) {
-    if (!group && terms > 16) return false;
+    if (terms > 16 * (group ? experts : 1)) return false;   // more than a tile of each
     const int64_t rows = min(terms, int64_t(16)), tiles = group ? (terms + 15) / 16 + min(terms, int64_t(experts)) : 1;
     return rows * ld <= int64_t(rows == 1 ? kTokenCodes : kTokenCodes / 2) &&
            (terms == 1 || (M + 15) / 16 * tiles <= int64_t(compute_units()));

@@ -114,6 +114,7 @@ def sketch_moe(p, router, gate, up, down, X, Y, ids, weights, workspace, stream=
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device   # a tensor on the GPU exists
 
 
 class _On:
@@ -126,7 +127,7 @@ class _On:
     def __enter__(self):
         if self.index is None:
             raise ValueError("tensors must be on a GPU")
-        if torch.cuda.current_device() != self.index:
+        if _current_device() != self.index:
             self.other = torch.cuda.device(self.index)
             self.other.__enter__()
         return _raw_stream(self.index)

@@ -171,21 +171,17 @@ class Int8Tables:
         return self._codes.as_strided((self._count, 4 * self._M), (s.bytes, 1), at).view(torch.float32)
 
 
-def _row_stride(x):
-    """Row stride of a tensor whose rows are dense and evenly apart, or None."""
-    if x.dim() == 3 and x.shape[0] > 1 and x.stride(0) != x.shape[1] * x.stride(1):
-        return None
-    if x.shape[-1] > 1 and x.stride(-1) != 1:
-        return None
-    if x.dim() == 2 and x.shape[0] <= 1:
-        return x.shape[1]
-    return x.stride(-2) if x.stride(-2) >= x.shape[-1] else None
-
-
 def _rows_of(x):
-    """(x or a copy of it, its row stride)"""
-    ld = _row_stride(x)
-    return (x, ld) if ld is not None else (x.contiguous(), x.shape[-1])
+    """(x, its row stride), or a copy where its rows are not dense and evenly apart."""
+    stride = x.stride()
+    if len(stride) == 2 and stride[1] == 1 and stride[0] >= x.shape[1]:
+        return x, stride[0]
+    rows, N = x.shape[-2:]
+    dense = N <= 1 or stride[-1] == 1
+    even = x.dim() == 2 or x.shape[0] <= 1 or stride[0] == rows * stride[1]
+    if dense and x.dim() == 2 and rows <= 1:
+        return x, N
+    return (x, stride[-2]) if dense and even and stride[-2] >= N else (x.contiguous(), N)
 
 
 def _flags(status, device):
@@ -230,16 +226,17 @@ def int8_swiglu(gate, up, status=None):
     in place): the activations between the products of an MLP.  Asynchronous; a
     row with a value that is NaN or infinite has the scale NaN, and ORs a flag
     into `status`, an int32 device tensor, when given."""
-    if gate.dim() != 2 or not gate.is_cuda or gate.shape != up.shape:
+    shape, device = gate.shape, gate.device
+    if len(shape) != 2 or not gate.is_cuda or shape != up.shape:
         raise ValueError("gate and up must be 2-D GPU tensors of one shape")
-    if gate.dtype != up.dtype or gate.device != up.device:
+    if gate.dtype != up.dtype or device != up.device:
         raise ValueError("gate and up must have one dtype and device")
-    _flags(status, gate.device)
+    _flags(status, device)
     dtype = dtype_code(gate)
     gate, ld_gate = _rows_of(gate)
     up, ld_up = _rows_of(up)
-    t = Int8Tables(gate.shape[0], gate.shape[1], None, gate.device)
-    with _On(gate.device) as stream:
+    t = Int8Tables(*shape, None, device)
+    with _On(device) as stream:
         rc = _int8_lib().sketch_int8_swiglu(t._ref, gate.data_ptr(), ld_gate, up.data_ptr(), ld_up, dtype, t._at,
                                             status.data_ptr() if status is not None else None, stream)
     if rc != OK:
