@@ -87,6 +87,54 @@ __device__ inline float row_scale(uint32_t bits) {
     return bits >= 0x7F800000u ? __builtin_nanf("") : __uint_as_float(bits) / 127.0f;
 }
 
+// K chunks of 8 columns of a row, L chunks apart, from chunk `at` on, zeros past
+// its end.  All loads go out before any is used (each in a branch of its own, as in
+// load_row8, they follow one another: 2048 rows of 8192 15.0 us, so 12.6); a chunk that
+// does not lie in the row as a whole is loaded from its last 8 columns and read
+// again by element.
+template <int DT, int K, int L>
+struct Chunks {
+    typedef uint32_t loose __attribute__((ext_vector_type(4), aligned(2)));
+    static constexpr int kWords = DT == SKETCH_F32 ? 2 : 1, es = DT == SKETCH_F32 ? 4 : 2;
+    loose raw[K][kWords];
+
+    __device__ inline void load(const char* x, int64_t N, int at) {
+        if (N < 8) return;
+#pragma unroll
+        for (int i = 0; i < K; ++i) {
+            if (i * L * 8 >= N) break;   // the whole row's
+            const loose* from = reinterpret_cast<const loose*>(x + min(int64_t(at + i * L) * 8, N - 8) * es);
+#pragma unroll
+            for (int u = 0; u < kWords; ++u) raw[i][u] = from[u];
+        }
+    }
+    __device__ inline void get(const char* x, int64_t N, int at, int i, float (&v)[8]) const {
+        if (i * L * 8 >= N) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+            return;
+        }
+        const int64_t c0 = int64_t(at + i * L) * 8;
+        if (c0 + 8 <= N) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const uint32_t h = (raw[i][0][e >> 1] >> ((e & 1) * 16)) & 0xFFFFu;
+                v[e] = DT == SKETCH_F32    ? __uint_as_float(raw[i][e / 4 % kWords][e & 3])
+                       : DT == SKETCH_BF16 ? bf16_bits_to_f32(h)
+                                           : f16_bits_to_f32(h);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+            if (c0 < N) {
+#pragma unroll
+                for (int e = 0; e < 7; ++e)
+                    if (c0 + e < N) v[e] = load_elem<DT>(x, c0 + e);
+            }
+        }
+    }
+};
+
 struct EncodeArgs {
     const void *a, *b;        // the matrix, or gate and up
     int64_t lda, ldb;
@@ -134,17 +182,13 @@ __global__ __launch_bounds__(256) void int8_encode_kernel(EncodeArgs a) {
     const int chunks = int(a.ld / 8);
     float v[kKept][8];
     uint32_t bits = 0;
+    Chunks<DT, kKept, L> x;
+    x.load(W, a.N, at);
 #pragma unroll
     for (int i = 0; i < kKept; ++i) {
-        if (at + i * L < chunks) {
-            load_row8<DT>(W, 0, a.N, (at + i * L) * 8, v[i]);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[i][e] = 0.0f;
-        }
+        x.get(W, a.N, at, i, v[i]);
+        bits = max(bits, max_bits(v[i]));
     }
-#pragma unroll
-    for (int i = 0; i < kKept; ++i) bits = max(bits, max_bits(v[i]));
     for (int c = at + kKept * L; c < chunks; c += L) {
         float x[8];
         load_row8<DT>(W, 0, a.N, int64_t(c) * 8, x);
@@ -199,16 +243,20 @@ __global__ __launch_bounds__(256) void int8_swiglu_kernel(EncodeArgs a) {
     uint8_t* codes = a.buf + row * a.ld;
     float h[K][8], least = 0.0f;
     uint32_t bits = 0;
+    Chunks<DT, K, L> gates, ups;
+    gates.load(G, a.N, at);
+    ups.load(U, a.N, at);
 #pragma unroll
     for (int i = 0; i < K; ++i) {
-        if (at + i * L < chunks) {
-            float g[8], u[8];
-            load(at + i * L, g, u);
-            swiglu8(g, u, h[i], least);
-        } else {
+        float g[8], u[8];
+        if (i * L >= chunks) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) h[i][e] = 0.0f;
+            continue;
         }
+        gates.get(G, a.N, at, i, g);
+        ups.get(U, a.N, at, i, u);
+        swiglu8(g, u, h[i], least);
         bits = max(bits, max_bits(h[i]));
     }
     for (int c = at + K * L; c < chunks; c += L) {
@@ -429,17 +477,13 @@ __global__ __launch_bounds__(512) void int8_tokens_kernel(Int8Product p, int64_t
         const char* x = row_at(n);
         float v[KEPT][8];
         uint32_t bits = 0;
+        Chunks<XD, KEPT, LANES> kept;
+        kept.load(x, N, at);
 #pragma unroll
         for (int i = 0; i < KEPT; ++i) {
-            if (at + i * LANES < chunks) {
-                load_row8<XD>(x, 0, N, (at + i * LANES) * 8, v[i]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[i][e] = 0.0f;
-            }
+            kept.get(x, N, at, i, v[i]);
+            bits = max(bits, max_bits(v[i]));
         }
-#pragma unroll
-        for (int i = 0; i < KEPT; ++i) bits = max(bits, max_bits(v[i]));
         for (int q = at + KEPT * LANES; q < chunks; q += LANES) {
             float y[8];
             load_row8<XD>(x, 0, N, int64_t(q) * 8, y);
