@@ -447,8 +447,8 @@ __global__ __launch_bounds__(WAVES * 64) void int8_rows_kernel(Int8Product p) {
 // ---------------------------------------------------------------------------
 constexpr uint32_t kTokenCodes = 32768;   // bytes of codes that LDS holds, with 64 more for each row
 
-template <int XD, bool GROUP>
-__global__ __launch_bounds__(512) void int8_tokens_kernel(Int8Product p, int64_t N) {
+template <int XD, bool GROUP, bool ONE>
+__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(ONE ? 6 : 4))) void int8_tokens_kernel(Int8Product p, int64_t N) {
     extern __shared__ __attribute__((aligned(16))) uint8_t codes[];   // [min(16, T)][ld + 64]
     __shared__ uint32_t red[16];
     __shared__ __attribute__((aligned(16))) int part[8][16][20];
@@ -465,6 +465,7 @@ __global__ __launch_bounds__(512) void int8_tokens_kernel(Int8Product p, int64_t
     Frag a[RUN];
 #pragma unroll
     for (int u = 0; u < RUN; ++u) a[u].load(wrow, min(k0 + u, p.kb - 1), c);
+    const float sw = reinterpret_cast<const float*>(reinterpret_cast<const char*>(w) + p.w_scales)[min(m0 + (tid & 15), p.M - 1)];
     asm volatile("" ::: "memory");   // on their way before X is asked for
 
     auto row_at = [&](int n) {
@@ -507,7 +508,7 @@ __global__ __launch_bounds__(512) void int8_tokens_kernel(Int8Product p, int64_t
         }
         return bits;
     };
-    if (t.n == 1) {
+    if (ONE || t.n == 1) {
         const uint32_t bits = encode(0, tid, std::integral_constant<int, 512>(), std::integral_constant<int, 2>(), [&](uint32_t m) {
             if (lane == 0) red[wave + 8] = m;
             __syncthreads();
@@ -516,10 +517,10 @@ __global__ __launch_bounds__(512) void int8_tokens_kernel(Int8Product p, int64_t
             return m;
         });
         if (tid == 0) red[0] = bits;
-    } else {
+    } else if constexpr (!ONE) {
         for (int n = wave; n < t.n; n += 8) {
             const uint32_t bits =
-                encode(n, lane, std::integral_constant<int, 64>(), std::integral_constant<int, 4>(), [](uint32_t m) { return m; });
+                encode(n, lane, std::integral_constant<int, 64>(), std::integral_constant<int, XD == SKETCH_F32 ? 2 : 4>(), [](uint32_t m) { return m; });
             if (lane == 0) red[n] = bits;
         }
     }
@@ -549,7 +550,7 @@ __global__ __launch_bounds__(512) void int8_tokens_kernel(Int8Product p, int64_t
     for (int i = 0; i < 8; ++i) sum += part[i][n][m];
     const int64_t term = t.first + n;
     const float sx = GROUP && term_row(p, term) < 0 ? __builtin_nanf("") : row_scale(red[n]);
-    const float y = int8_value(sum, sx, reinterpret_cast<const float*>(reinterpret_cast<const char*>(w) + p.w_scales)[m0 + m]);
+    const float y = int8_value(sum, sx, sw);
     const int64_t at = term * p.M + m0 + m;
     if (p.ydt == SKETCH_F32)
         store1_val<SKETCH_F32>(p.Y, at, y);
@@ -618,18 +619,20 @@ struct Plan {
     size_t workspace;
 };
 
-// Whether the workgroups of a product encode its raw rows themselves.  A single
-// row always gains or is even (435 x 4149 5.8 us, 8.7 with a launch of its own; 28672 x
-// 8192 45.1 and 45.3).  Several, up to 16384 codes, do where a compute unit has one
-// workgroup at most: on the GPU they are 15% faster to 15% slower (256 x 512, 2 rows 5.1 and
-// 6.1 us; 4096 x 1024, 15 rows 7.4 and 6.9), but a launch takes the host 4.5 us, and
-// calls this small wait for it (16 rows of 256 x 512 among others 12.1 and 7.5 us).
-// With more workgroups the work that they repeat outweighs that (20447 x 692, 8 rows 20 and 10 us).
+// Whether the workgroups of a product encode its raw rows themselves.  On the
+// GPU that is faster where they are few, or long enough to hide it: a single row of
+// 5179 x 3673 8.5 us, 11.1 with a launch of its own; 28672 x 8192 44 and 49; 28616 x 1385 19
+// and 12.  2 to 16 rows, up to 16384 codes, where a compute unit has one workgroup at most, are
+// 20% faster to 20% slower (1376 x 2048, 4 rows 5.7 and 7.1; 4096 x 4096, 2 rows 11.6 and
+// 9.5), with more workgroups much slower (14601 x 356, 4 rows 18 and 7.4).  But a launch takes the
+// host 4.5 us, and calls this small among others wait for it (16 rows of 256 x 512
+// 12.1 and 7.3 us), so the border lies where one launch takes what the host takes for two.
 bool encodes_itself(int64_t M, int64_t terms, int64_t ld, int experts, bool group) {
     if (terms > 16 * (group ? experts : 1)) return false;   // more than a tile of each
     const int64_t rows = min(terms, int64_t(16)), tiles = group ? (terms + 15) / 16 + min(terms, int64_t(experts)) : 1;
-    return rows * ld <= int64_t(rows == 1 ? kTokenCodes : kTokenCodes / 2) &&
-           (terms == 1 || (M + 15) / 16 * tiles <= int64_t(compute_units()));
+    const int64_t groups = (M + 15) / 16 * tiles, ncu = compute_units();
+    if (terms == 1) return ld <= int64_t(kTokenCodes) && (2 * groups <= 5 * ncu || ld * ncu >= 512 * groups);
+    return rows * ld <= int64_t(kTokenCodes / 2) && groups <= ncu;
 }
 
 // Checks the parameters and fills the plan.
@@ -677,12 +680,15 @@ sketch_status launch_tokens(const Int8Product& a, int x_dtype, int64_t N, hipStr
         kernel<<<unsigned(token_groups(a)), 512, unsigned(min(a.T, int64_t(16)) * (a.ld + 64)), st>>>(a, N);
         return launch_status();
     };
-    if (a.counts) {
-        if (x_dtype == SKETCH_F32) return go(int8_tokens_kernel<SKETCH_F32, true>);
-        return x_dtype == SKETCH_BF16 ? go(int8_tokens_kernel<SKETCH_BF16, true>) : go(int8_tokens_kernel<SKETCH_F16, true>);
-    }
-    if (x_dtype == SKETCH_F32) return go(int8_tokens_kernel<SKETCH_F32, false>);
-    return x_dtype == SKETCH_BF16 ? go(int8_tokens_kernel<SKETCH_BF16, false>) : go(int8_tokens_kernel<SKETCH_F16, false>);
+    auto all = [&](auto f32, auto bf16, auto f16) { return x_dtype == SKETCH_F32 ? go(f32) : x_dtype == SKETCH_BF16 ? go(bf16) : go(f16); };
+    if (a.counts)
+        return all(int8_tokens_kernel<SKETCH_F32, true, false>, int8_tokens_kernel<SKETCH_BF16, true, false>,
+                   int8_tokens_kernel<SKETCH_F16, true, false>);
+    if (a.T == 1)
+        return all(int8_tokens_kernel<SKETCH_F32, false, true>, int8_tokens_kernel<SKETCH_BF16, false, true>,
+                   int8_tokens_kernel<SKETCH_F16, false, true>);
+    return all(int8_tokens_kernel<SKETCH_F32, false, false>, int8_tokens_kernel<SKETCH_BF16, false, false>,
+               int8_tokens_kernel<SKETCH_F16, false, false>);
 }
 
 sketch_status product(const sketch_int8_params* p, const void* buf, const void* X, int x_dtype, int64_t x_rows,
