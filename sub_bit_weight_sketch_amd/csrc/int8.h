@@ -3,7 +3,7 @@
 #pragma once
 
 #include "../../include/sketch_int8.h"
-#include "fp8.h"
+#include "tile.h"
 
 namespace sketch {
 
@@ -135,6 +135,23 @@ struct Int8Plan {
 // there are more tiles than a grid holds.
 sketch_status int8_plan(int64_t M, int64_t T, uint32_t kb, int experts, bool group, bool near, Int8Plan* g);
 sketch_status launch_int8_gemm(const Int8Product& p, const Int8Plan& g, void* ws, hipStream_t st);
+
+// Four outputs of a row from m on, at any alignment of an element.
+template <int YD>
+__device__ inline void store4_any(void* Y, int64_t e, f32x4 v, int64_t m, int64_t M) {
+    typedef float loose4 __attribute__((ext_vector_type(4), aligned(4)));
+    typedef uint32_t loose2 __attribute__((ext_vector_type(2), aligned(2)));
+    if (m + 4 <= M) {
+        if constexpr (YD == SKETCH_F32)
+            *reinterpret_cast<loose4*>(static_cast<float*>(Y) + e) = v;
+        else
+            *reinterpret_cast<loose2*>(static_cast<uint16_t*>(Y) + e) = loose2{pack2<YD>(v[0], v[1]), pack2<YD>(v[2], v[3])};
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (m + i < M) store1_val<YD>(Y, e + i, v[i]);
+}
 
 sketch_status int8_shape(const sketch_int8_params* p, sketch_int8_shape* s);
 

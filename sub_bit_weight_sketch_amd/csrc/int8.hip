@@ -4,7 +4,6 @@
 #include <type_traits>
 
 #include "int8.h"
-#include "tile.h"
 
 namespace sketch {
 namespace {
@@ -409,7 +408,7 @@ __global__ __launch_bounds__(WAVES * 64) void int8_rows_kernel(Int8Product p) {
     // 16 terms x 16 RT outputs, 4 outputs to a thread
     constexpr int kAcross = RT * 4;
     const int m = tid % kAcross * 4, n = tid / kAcross;
-    const bool stores = n < 16 && m0 + m < p.M, vec = p.M % 4 == 0;
+    const bool stores = n < 16 && m0 + m < p.M;
     f32x4 sw = {0, 0, 0, 0};
     if (stores) sw = *reinterpret_cast<const f32x4*>(reinterpret_cast<const char*>(w) + p.w_scales + (m0 + m) * 4);
 #pragma unroll
@@ -429,11 +428,11 @@ __global__ __launch_bounds__(WAVES * 64) void int8_rows_kernel(Int8Product p) {
         for (int i = 0; i < 4; ++i) v[i] = int8_value(sum[i], sx, sw[i]);
         const int64_t at = term * p.M + m0 + m;
         if (p.ydt == SKETCH_F32)
-            store4<SKETCH_F32>(p.Y, at, v, m0 + m, p.M, vec);
+            store4_any<SKETCH_F32>(p.Y, at, v, m0 + m, p.M);
         else if (p.ydt == SKETCH_BF16)
-            store4<SKETCH_BF16>(p.Y, at, v, m0 + m, p.M, vec);
+            store4_any<SKETCH_BF16>(p.Y, at, v, m0 + m, p.M);
         else
-            store4<SKETCH_F16>(p.Y, at, v, m0 + m, p.M, vec);
+            store4_any<SKETCH_F16>(p.Y, at, v, m0 + m, p.M);
     }
 }
 

@@ -12,7 +12,6 @@
 #include <type_traits>
 
 #include "int8.h"
-#include "tile.h"
 
 namespace sketch {
 namespace {
@@ -72,9 +71,9 @@ __device__ inline f32x4 values(i32x4 sum, float sx, f32x4 sw) {
 // The scaled sums of a wave's tile to Y: 16 FA outputs from o0 + wm on, strips of
 // 16 terms, SPREAD apart, from wt on.  They go through the wave's own part of
 // LDS (`mine`, JC strips at a time), so that a row's outputs leave in pieces of
-// 16 bytes side by side, or of 4 or 2 where M leaves rows no better aligned
-// (8 experts of 15486 x 523, 3784 terms, M = 2 mod 4: 143 us with stores from
-// registers).
+// 16 bytes side by side, whatever M leaves of their alignment (8 experts of 15486 x
+// 523, 3784 terms: 143 us with stores from registers; 24825 x 133 at 1101 rows, M odd:
+// 40 us with stores by element, so 22).
 template <int YD, int FA> constexpr uint32_t out_pitch() { return FA * 16 * (YD == SKETCH_F32 ? 4 : 2) + 16; }
 template <int YD, int FA, int JC> constexpr uint32_t out_bytes() { return JC * 16 * out_pitch<YD, FA>(); }
 
@@ -93,15 +92,22 @@ __device__ inline void store_tile(const Int8Product& p, const Terms& t, const i3
     const int left = int(min(p.M - o0 - wm, int64_t(FA * 16)));   // outputs that there are
     if (left <= 0) return;
     unsigned char* Y = static_cast<unsigned char*>(p.Y) + (int64_t(t.first) * p.M + o0 + wm) * es;
-    auto rows_out = [&](int j0, auto unit) {
-        typedef decltype(unit) U;
-        constexpr int per = FA * 16 * es / sizeof(U);
+    // 16 bytes at a time, aligned to an element; by element where the row ends among them
+    typedef uint32_t loose __attribute__((ext_vector_type(4), aligned(2)));
+    typedef typename std::conditional<YD == SKETCH_F32, float, uint16_t>::type element;
+    constexpr int per = FA * es, kIn = 16 / es;
+    auto rows_out = [&](int j0) {
 #pragma unroll 4
         for (int q = lane; q < JC * 16 * per; q += 64) {
-            const int row = q / per, at = q % per, n = (j0 + row / 16) * SPREAD + wt + row % 16;
-            if (n < t.n && at * int(sizeof(U)) < left * es)
-                *reinterpret_cast<U*>(Y + int64_t(n) * p.M * es + at * sizeof(U)) =
-                    *reinterpret_cast<const U*>(mine + row * pitch + at * sizeof(U));
+            const int row = q / per, at = q % per * kIn, n = (j0 + row / 16) * SPREAD + wt + row % 16;
+            if (n >= t.n || at >= left) continue;
+            const element* from = reinterpret_cast<const element*>(mine + row * pitch) + at;
+            element* to = reinterpret_cast<element*>(Y) + int64_t(n) * p.M + at;
+            if (at + kIn <= left) {
+                *reinterpret_cast<loose*>(to) = *reinterpret_cast<const u32x4*>(from);
+            } else {
+                for (int e = 0; at + e < left; ++e) to[e] = from[e];
+            }
         }
     };
 #pragma unroll
@@ -120,12 +126,7 @@ __device__ inline void store_tile(const Int8Product& p, const Terms& t, const i3
             }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
-        if (p.M * es % 16 == 0)
-            rows_out(j0, u32x4());
-        else if (p.M * es % 4 == 0)
-            rows_out(j0, uint32_t());
-        else
-            rows_out(j0, uint16_t());
+        rows_out(j0);
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
     }
@@ -460,7 +461,7 @@ __global__ __launch_bounds__(256) void int8_add_kernel(GemmArgs a) {
 #pragma unroll 4
     for (uint32_t s = 1; s < a.splits; ++s) sum += *reinterpret_cast<const i32x4*>(part + s * p.T * ldy);
     const float* sw = reinterpret_cast<const float*>(reinterpret_cast<const char*>(p.w) + p.w_scales);
-    store4<YD>(p.Y, t * p.M + m, values(sum, p.xs[t], *reinterpret_cast<const f32x4*>(sw + m)), m, p.M, p.M % 4 == 0);
+    store4_any<YD>(p.Y, t * p.M + m, values(sum, p.xs[t], *reinterpret_cast<const f32x4*>(sw + m)), m, p.M);
 }
 
 // What a product takes in us, by a model of the kernels: a sum of what one tile
