@@ -133,7 +133,7 @@ struct Int8Plan {
 
 // near: the place of every row of X in bytes fits 32 bits.  SKETCH_EINVAL when
 // there are more tiles than a grid holds.
-sketch_status int8_plan(int64_t M, int64_t T, uint32_t kb, int experts, bool group, bool near, Int8Plan* g);
+sketch_status int8_plan(int64_t M, int64_t T, uint32_t kb, int ydt, int experts, bool group, bool near, Int8Plan* g);
 sketch_status launch_int8_gemm(const Int8Product& p, const Int8Plan& g, void* ws, hipStream_t st);
 
 // Four outputs of a row from m on, at any alignment of an element.

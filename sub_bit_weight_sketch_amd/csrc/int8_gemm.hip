@@ -466,67 +466,69 @@ __global__ __launch_bounds__(256) void int8_add_kernel(GemmArgs a) {
 
 // What a product takes in us, by a model of the kernels: a sum of what one tile
 // takes by itself (its steps of 128 columns one after another), of the rounds that
-// the tiles make over the slots of the compute units, and of the work that they add up to
-// (tiles times steps, and strips of terms times steps); parts cost the launch
-// that adds them and their way to memory and back.  The figures are fitted to every
-// kernel and split, timed on 2000 products of one weight (64 x 64 to 28672 x
-// 16384, 2 to 2100 rows) and on 1500 grouped ones (4 to 128 experts, 1 to 24000 terms):
-// what the model takes is 2.8% and 3.2% slower than the fastest kernel on average,
-// at worst 45% and 57%, and the same on thirds of them that the fit had not seen.
-// One kernel of tiles of 128 x 128 in place of the set: 25% slower on average.
+// the tiles make over the slots of the compute units, of the work that they add up to
+// (tiles times steps, and strips of terms times steps), and of the bytes of W and
+// Y in MB; parts cost the launch that adds them and their way to memory and back.  The
+// figures are fitted to every kernel and split, timed on two thirds of 2000 products of one weight
+// (64 x 64 to 28672 x 16384, 2 to 2100 rows) and of 1800 grouped ones (4 to 128 experts, 1 to
+// 24000 terms).  What the model takes is 2.6% and 3.0% slower than the fastest kernel
+// on average, at worst 45% and 43%; on the third that the fit has not seen 2.8% (61%) and 2.9%
+// (37%).  Tiles of 128 x 128, unsplit or split as is best, in place of the set: 28% and 16%.
 struct TileCost {
-    int fa, fb, slots;   // outputs and terms of a tile in units of 32; workgroups that a compute unit holds
-    double call, step, round_step, round, tile_step, strip_step, strip, parts, part_bytes, byte;   // one weight
-    double g_call, g_step, g_round_step, g_round, g_tile_step, g_strip_step, g_strip;              // grouped
+    int fa, fb;   // outputs and terms of a tile in units of 32
+    double call, step, round_step, round, tile_step, strip_step, strip, parts, part_mb, mb, out_mb;   // one weight
+    double g_call, g_step, g_round_step, g_round, g_strip_step, g_out_mb, g_mb;                      // grouped
 };
 constexpr TileCost kCost[] = {
-    {1, 2, 4, 3.31, 0.148, 0.090, 0.0, 0.049, 0.012, 0.252, 2.27, 1.43, 0.0326, 4.71, 0.132, 0.085, 0.50, 0.039, 0.058, 0.063},
-    {2, 2, 4, 3.58, 0.159, 0.051, 0.067, 0.061, 0.033, 0.357, 2.17, 1.14, 0.0662, 4.75, 0.158, 0.101, 0.16, 0.201, 0.022, 0.154},
-    {2, 4, 2, 4.08, 0.146, 0.198, 0.0, 0.099, 0.035, 0.397, 2.03, 1.04, 0.0408, 0, 0, 0, 0, 0, 0, 0},
-    {4, 2, 2, 4.17, 0.193, 0.245, 0.0, 0.129, 0.029, 0.750, 2.08, 0.93, 0.0765, 5.30, 0.168, 0.0, 1.33, 0.478, 0.0, 0.324},
-    {4, 4, 2, 5.12, 0.186, 0.200, 0.0, 0.193, 0.049, 0.643, 1.32, 0.94, 0.0602, 5.91, 0.189, 0.099, 0.30, 0.442, 0.038, 0.699},
-    {8, 8, 1, 6.46, 0.748, 0.697, 3.68, 0.0, 0.143, 2.54, 0.0, 0.0, 0.0230, 5.62, 0.599, 0.749, 0.0, 0.289, 0.215, 3.56}};
+    {1, 2, 3.22, 0.147, 0.092, 0.0, 0.045, 0.016, 0.218, 2.43, 1.44, 0.0325, 0.0, 4.47, 0.140, 0.084, 0.44, 0.064, 0.247, 0.0366},
+    {2, 2, 3.34, 0.161, 0.055, 0.10, 0.065, 0.032, 0.112, 2.49, 1.52, 0.0657, 0.139, 4.45, 0.178, 0.178, 0.06, 0.078, 0.213, 0.0626},
+    {2, 4, 3.75, 0.151, 0.211, 0.0, 0.094, 0.036, 0.160, 2.42, 1.45, 0.0417, 0.153, 0, 0, 0, 0, 0, 0, 0},
+    {4, 2, 3.80, 0.188, 0.235, 0.0, 0.122, 0.034, 0.215, 2.57, 1.38, 0.0796, 0.178, 4.84, 0.174, 0.180, 0.47, 0.136, 0.279, 0.0831},
+    {4, 4, 4.57, 0.182, 0.222, 0.0, 0.181, 0.055, 0.235, 1.98, 1.27, 0.0630, 0.115, 5.69, 0.172, 0.102, 1.02, 0.123, 0.233, 0.0920},
+    {8, 8, 5.84, 0.806, 0.836, 0.0, 0.0, 0.109, 1.03, 0.0, 0.0, 0.0320, 0.126, 6.21, 0.436, 0.492, 2.03, 0.263, 0.328, 0.0666}};
 constexpr int64_t kMaxSplits = 16;
-constexpr double kFewPerExpert = 6;   // terms per expert up to which int8_rows_kernel was timed on groups
+constexpr int64_t kFewRows = 32;      // rows up to which int8_rows_kernel was timed on one weight
+constexpr double kFewPerExpert = 6;   // and terms per expert on groups
 
-// Tiles of up to BT terms that an expert of `mean` terms has on average, where the numbers of terms
-// fall off evenly (exponentially), as those of routed tokens about do.
+// Tiles of up to bt terms that an expert of `mean` terms has on average, where the
+// numbers of terms fall off exponentially, as those of routed tokens about do.
 double tiles_per_expert(double mean, int64_t bt) { return (1 - exp(-mean)) / (1 - exp(-double(bt) / mean)); }
 
-Int8Plan choose_group(int64_t M, int64_t T, double kb, int experts, bool near) {
+struct Best {
+    Int8Plan plan{};
+    double us = 1e300;
+    void consider(const Int8Plan& p, double t) {
+        if (t < us) us = t, plan = p;
+    }
+};
+
+Int8Plan choose_group(int64_t M, int64_t T, double kb, int experts, double out_mb, bool near) {
     const double ncu = double(compute_units()), mean = double(T) / experts;
-    Int8Plan best{};
-    double least = 1e300;
-    auto consider = [&](const Int8Plan& g, double us) {
-        if (us < least) least = us, best = g;
-    };
+    const double mb = 128e-6 * double(M) * kb * experts * (1 - exp(-mean));   // of the experts that have terms
+    Best best;
     for (const TileCost& c : kCost) {
         const bool big = c.fa == 8;
         if (c.g_call == 0 || (big && !near)) continue;
         const double across = double((M + 32 * c.fa - 1) / (32 * c.fa)) * experts;
         const double tiles = across * tiles_per_expert(mean, 32 * c.fb), strips = across * tiles_per_expert(mean, big ? 64 : 32);
-        const double rounds = fmax(tiles / ((big ? 1 : 2) * ncu), 1) - 1;   // of the rounds that the fit counts
-        consider({big ? kInt8Big : kInt8Mid, c.fa, c.fb, 1, 0, 0, 0},
-                 c.g_call + c.g_step * kb + rounds * (c.g_round_step * kb + c.g_round) +
-                     (c.g_tile_step * tiles + c.g_strip_step * strips) / ncu * kb + c.g_strip * strips / ncu);
+        const double rounds = fmax(tiles / ((big ? 1 : 2) * ncu), 1) - 1;
+        best.consider({big ? kInt8Big : kInt8Mid, c.fa, c.fb, 1, 0, 0, 0},
+                      c.g_call + c.g_step * kb + rounds * (c.g_round_step * kb + c.g_round) + c.g_strip_step * strips / ncu * kb +
+                          c.g_out_mb * out_mb + c.g_mb * mb);
     }
     if (mean <= kFewPerExpert) {
         const double tiles = experts * tiles_per_expert(mean, 16) / ncu, one = double((M + 15) / 16) * tiles,
                      two = double((M + 31) / 32) * tiles;
-        consider({kInt8Rows1, 0, 0, 1, 0, 0, 0}, 3.45 + 1.28 * ceil(kb / 32) + one * (2.31 * kb / 32 + 0.28));
-        consider({kInt8Rows2, 0, 0, 1, 0, 0, 0}, 3.67 + 1.33 * ceil(kb / 16) + two * (4.18 * kb / 32 + 0.155));
+        best.consider({kInt8Rows1, 0, 0, 1, 0, 0, 0}, 2.25 + 2.44 * ceil(kb / 32) + one * (2.42 * kb / 32 + 0.154) + 3.12 * out_mb);
+        best.consider({kInt8Rows2, 0, 0, 1, 0, 0, 0}, 3.45 + 1.51 * ceil(kb / 16) + two * (4.21 * kb / 32 + 0.043) + 1.64 * out_mb);
     }
-    return best;
+    return best.plan;
 }
 
-Int8Plan choose(int64_t M, int64_t T, uint32_t kb, bool near) {
+Int8Plan choose(int64_t M, int64_t T, uint32_t kb, double out_mb, bool near) {
     const int64_t ncu = compute_units();
-    const double bytes = 128e-6 * double(M) * double(kb);
-    Int8Plan best{};
-    double least = 1e300;
-    auto consider = [&](const Int8Plan& g, double us) {
-        if (us < least) least = us, best = g;
-    };
+    const double mb = 128e-6 * double(M) * double(kb);
+    Best best;
     for (const TileCost& c : kCost) {
         const bool big = c.fa == 8;
         if (big && (!near || T <= 64)) continue;
@@ -536,17 +538,19 @@ Int8Plan choose(int64_t M, int64_t T, uint32_t kb, bool near) {
             const double tiles = double(across * down * n), strips = double(across * ((T + strip - 1) / strip) * n);
             const double steps = ceil(double(kb) / double(n)), rounds = ceil(tiles / double((big ? 1 : 2) * ncu)) - 1;
             double us = c.call + c.step * steps + rounds * (c.round_step * steps + c.round) +
-                        (c.tile_step * tiles + c.strip_step * strips) / double(ncu) * steps + c.strip * strips / double(ncu) + c.byte * bytes;
-            if (n > 1) us += c.parts + c.part_bytes * 1e-6 * double(n) * double(T) * double(M);
-            consider({big ? kInt8Big : kInt8Mid, c.fa, c.fb, uint32_t(n), 0, 0, 0}, us);
+                        (c.tile_step * tiles + c.strip_step * strips) / double(ncu) * steps + c.strip * strips / double(ncu) +
+                        c.mb * mb + c.out_mb * out_mb;
+            if (n > 1) us += c.parts + c.part_mb * 1e-6 * double(n) * double(T) * double(M);
+            best.consider({big ? kInt8Big : kInt8Mid, c.fa, c.fb, uint32_t(n), 0, 0, 0}, us);
         }
     }
-    if (T <= 32) {
+    if (T <= kFewRows) {
         const double w = double((M + 15) / 16 * ((T + 15) / 16)) / double(ncu), x = fmax(0, w - 1), k = kb / 32.0,
                      t = double(T < 16 ? T : 16) / 16;
-        consider({kInt8Rows1, 0, 0, 1, 0, 0, 0}, 2.94 + k * (2.40 + 1.34 * t) + x * (k * (2.74 + 0.56 * t) + 0.385) + (bytes > 60 ? 0.0114 * bytes : 0));
+        best.consider({kInt8Rows1, 0, 0, 1, 0, 0, 0},
+                      2.87 + k * (2.36 + 1.45 * t) + x * (k * (2.59 + 1.17 * t) + 0.333) + (mb > 60 ? 0.0077 * mb : 0));
     }
-    return best;
+    return best.plan;
 }
 
 template <int YD, bool GROUP>
@@ -576,8 +580,9 @@ sketch_status launch(const GemmArgs& a, const Int8Plan& g, hipStream_t st) {
 
 }  // namespace
 
-sketch_status int8_plan(int64_t M, int64_t T, uint32_t kb, int experts, bool group, bool near, Int8Plan* g) {
-    *g = group ? choose_group(M, T, kb, experts, near) : choose(M, T, kb, near);
+sketch_status int8_plan(int64_t M, int64_t T, uint32_t kb, int ydt, int experts, bool group, bool near, Int8Plan* g) {
+    const double out_mb = 1e-6 * double(T) * double(M) * double(elem_bytes(ydt));
+    *g = group ? choose_group(M, T, kb, experts, out_mb, near) : choose(M, T, kb, out_mb, near);
     if (g->kind == kInt8Rows1 || g->kind == kInt8Rows2) return SKETCH_OK;   // their launch counts its own workgroups
     const int64_t rows = 32 * g->fa, cols = 32 * g->fb;
     g->tiles_o = (M + rows - 1) / rows;
