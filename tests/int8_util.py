@@ -95,3 +95,10 @@ def group(qx, sx, rows, counts, qw, sw, out):
         rr = np.where(ok, r, 0)
         out[at:end] = product(qx[rr], np.where(ok, sx[rr], np.float32("nan")), qw[e], sw[e], dt)
     return out
+
+
+def ragged(E, terms, seed, empty=0.3):
+    """Counts of E experts that add up to `terms`, some of them zero."""
+    g = np.random.default_rng(seed)
+    p = g.gamma(0.7, size=E) * (g.random(E) >= empty) + 1e-9
+    return g.multinomial(terms, p / p.sum()).tolist()

@@ -137,7 +137,7 @@ def check_swiglu(g, up, t):
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
-@pytest.mark.parametrize("M,N", [(1, 1), (7, 1408), (33, 129), (5, 2048), (3, 2049), (64, 5000), (2, 11008), (1, 70000)])
+@pytest.mark.parametrize("M,N", [(1, 1), (7, 1408), (33, 129), (5, 2048), (3, 2049), (64, 5000), (2, 11008), (1, 70000), (1100, 131)])
 def test_swiglu(M, N, dt):
     x = randn((M, 2 * N), M + N, 2.0, dt).to(dev())
     g, up = x[:, :N], x[:, N:]

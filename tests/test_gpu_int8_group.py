@@ -5,7 +5,7 @@ import torch
 
 import int8_util as u
 from gpu_util import dev
-from int8_util import DT, randn
+from int8_util import DT, ragged, randn
 
 sk = pytest.importorskip("sub_bit_weight_sketch_amd")
 
@@ -30,13 +30,6 @@ def check(w, X, counts, rows=None, y="f32", wide=(False, False), encoded=False, 
     got = sk.int8_matmul_group(w, x, c, rows=r, out=out)
     assert got is out
     u.same(got, want)
-
-
-def ragged(E, terms, seed, empty=0.3):
-    """Counts of E experts that add up to `terms`, some of them zero."""
-    g = np.random.default_rng(seed)
-    p = g.gamma(0.7, size=E) * (g.random(E) >= empty) + 1e-9
-    return g.multinomial(terms, p / p.sum()).tolist()
 
 
 CASES = [(1, 33, 130, 1), (2, 16, 64, 2), (8, 300, 1000, 3), (8, 256, 512, 16), (8, 130, 257, 40), (64, 96, 200, 42),
