@@ -474,6 +474,9 @@ __global__ __launch_bounds__(256) void int8_add_kernel(GemmArgs a) {
 // 24000 terms).  What the model takes is 2.6% and 3.0% slower than the fastest kernel
 // on average, at worst 45% and 43%; on the third that the fit has not seen 2.8% (61%) and 2.9%
 // (37%).  Tiles of 128 x 128, unsplit or split as is best, in place of the set: 28% and 16%.
+// The tiles of 256 terms were fitted to 477 large products of one weight; those of 224 outputs fill
+// the last round where those of 256 leave it half empty (28672 x 8192 at 2048 rows: 1024
+// tiles are 4 rounds, 896 are 3.5; 355 and 375 us) and save 4% of these on average.
 struct TileCost {
     int fa, fb;   // outputs and terms of a tile in units of 32
     double call, step, round_step, round, tile_step, strip_step, strip, parts, part_mb, mb, out_mb;   // one weight
@@ -485,7 +488,8 @@ constexpr TileCost kCost[] = {
     {2, 4, 3.75, 0.151, 0.211, 0.0, 0.094, 0.036, 0.160, 2.42, 1.45, 0.0417, 0.153, 0, 0, 0, 0, 0, 0, 0},
     {4, 2, 3.80, 0.188, 0.235, 0.0, 0.122, 0.034, 0.215, 2.57, 1.38, 0.0796, 0.178, 4.84, 0.174, 0.180, 0.47, 0.136, 0.279, 0.0831},
     {4, 4, 4.57, 0.182, 0.222, 0.0, 0.181, 0.055, 0.235, 1.98, 1.27, 0.0630, 0.115, 5.69, 0.172, 0.102, 1.02, 0.123, 0.233, 0.0920},
-    {8, 8, 5.84, 0.806, 0.836, 0.0, 0.0, 0.109, 1.03, 0.0, 0.0, 0.0320, 0.126, 6.21, 0.436, 0.492, 2.03, 0.263, 0.328, 0.0666}};
+    {7, 8, 9.40, 0.735, 0.853, 3.06, 0.0, 0.097, 0.0, 0.0, 0.0, 0.0311, 0.124, 0, 0, 0, 0, 0, 0, 0},
+    {8, 8, 8.66, 0.886, 0.991, 3.39, 0.0, 0.098, 0.0, 0.0, 0.0, 0.0233, 0.127, 6.21, 0.436, 0.492, 2.03, 0.263, 0.328, 0.0666}};
 constexpr int64_t kMaxSplits = 16;
 constexpr int64_t kFewRows = 32;      // rows up to which int8_rows_kernel was timed on one weight
 constexpr double kFewPerExpert = 6;   // and terms per expert on groups
@@ -507,7 +511,7 @@ Int8Plan choose_group(int64_t M, int64_t T, double kb, int experts, double out_m
     const double mb = 128e-6 * double(M) * kb * experts * (1 - exp(-mean));   // of the experts that have terms
     Best best;
     for (const TileCost& c : kCost) {
-        const bool big = c.fa == 8;
+        const bool big = c.fb == 8;
         if (c.g_call == 0 || (big && !near)) continue;
         const double across = double((M + 32 * c.fa - 1) / (32 * c.fa)) * experts;
         const double tiles = across * tiles_per_expert(mean, 32 * c.fb), strips = across * tiles_per_expert(mean, big ? 64 : 32);
@@ -530,7 +534,7 @@ Int8Plan choose(int64_t M, int64_t T, uint32_t kb, double out_mb, bool near) {
     const double mb = 128e-6 * double(M) * double(kb);
     Best best;
     for (const TileCost& c : kCost) {
-        const bool big = c.fa == 8;
+        const bool big = c.fb == 8;
         if (big && (!near || T <= 64)) continue;
         const int64_t across = (M + 32 * c.fa - 1) / (32 * c.fa), bt = 32 * c.fb, down = (T + bt - 1) / bt, strip = big ? 64 : 32;
         for (int64_t n = 1; n <= kMaxSplits; ++n) {
@@ -557,7 +561,11 @@ template <int YD, bool GROUP>
 sketch_status launch(const GemmArgs& a, const Int8Plan& g, hipStream_t st) {
     const int64_t tiles = g.tiles_o * g.tiles_t;
     if (g.kind == kInt8Big) {
-        int8_gemm_big_kernel<YD, 8, GROUP><<<unsigned(tiles), 512, kBigLds, st>>>(a);
+        auto go = [&](auto kernel) { kernel<<<unsigned(tiles), 512, kBigLds, st>>>(a); };
+        if (g.fa == 8)
+            go(int8_gemm_big_kernel<YD, 8, GROUP>);
+        else if constexpr (!GROUP)
+            go(int8_gemm_big_kernel<YD, 7, false>);
         return launch_status();
     }
     const dim3 grid(unsigned(tiles), g.splits);
