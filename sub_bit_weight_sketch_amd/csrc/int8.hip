@@ -165,7 +165,7 @@ __device__ inline double swiglu64(float g, float u) { return double(g) / (1.0 + 
 // One row to L lanes (a workgroup of 256 has 256 / L rows), 8 elements to a
 // lane at a time; kKept such chunks of a lane stay in registers between the
 // maximum and the rounding, what a longer row has more is read again.
-// HBM-bound.
+// HBM-bound: 28672 x 8192 bfloat16 126 us, 5.6 TB/s.
 constexpr int kKept = 4;
 
 template <int DT, int L>
@@ -221,7 +221,9 @@ __global__ __launch_bounds__(256) void int8_encode_kernel(EncodeArgs a) {
 // read again; the largest magnitude is that of float64 among the elements within 2e-6
 // of the largest in float32.  Rows that float32 cannot hold (a gate below
 // kLeastGate, values past its range, or tiny ones throughout) are computed in float64.
-// HBM-bound beside the arithmetic, some 35 instructions an element.
+// 2048 x 11008 bfloat16: 34 us, 3.3 TB/s; bound by its arithmetic, some 35
+// instructions an element, as much as by memory.  (Gate and up read three times, with
+// nothing kept: 57 us.)
 template <int DT, int L, int K>
 __global__ __launch_bounds__(256) void int8_swiglu_kernel(EncodeArgs a) {
     __shared__ uint32_t red[4];
@@ -339,14 +341,16 @@ __global__ __launch_bounds__(256) void int8_swiglu_kernel(EncodeArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// Product of up to 16 TT terms at a time, bound by the codes of W coming from
+// Product of up to 16 terms at a time, bound by the codes of W coming from
 // memory: 16 RT outputs to a workgroup, whose waves share out the columns in runs
-// of RUN blocks of 128, all loads of a run in flight, both operands straight to
+// of 4 blocks of 128, all loads of a run in flight, both operands straight to
 // registers.  A fragment is 16 rows x 128 columns, one row to a lane: lane l
 // holds row l % 16 and the columns 16c..16c+15 and 64+16c..64+16c+15, c = l / 16,
 // the same ones of outputs (A) and terms (B), so that a pair of loads covers 128
 // contiguous bytes of a row.  D: term l % 16, outputs 4c..4c+3.  The waves' sums meet
-// in LDS, 16 terms at a time.
+// in LDS.  16 outputs to 8 waves for few rows of one weight (4096 x
+// 4096 at 5 rows 6.2 us), 32 to 4 waves where many experts have a few terms each (64 experts of
+// 2816 x 2048, 42 terms: 36 and 29 us).
 // ---------------------------------------------------------------------------
 struct Frag {
     i32x4 lo, hi;
@@ -362,78 +366,67 @@ __device__ inline i32x4 multiply(const Frag& a, const Frag& b, i32x4 acc) {
     return __builtin_amdgcn_mfma_i32_16x16x64_i8(a.hi, b.hi, acc, 0, 0, 0);
 }
 
-template <bool GROUP, int WAVES, int RT, int TT, int RUN>
+constexpr int kRun = 4;
+
+template <bool GROUP, int WAVES, int RT>
 __global__ __launch_bounds__(WAVES * 64) void int8_rows_kernel(Int8Product p) {
-    __shared__ __attribute__((aligned(16))) int part[TT > 1 ? 2 : 1][WAVES][16][RT * 16 + 4];
+    __shared__ __attribute__((aligned(16))) int part[WAVES][16][RT * 16 + 4];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r = lane & 15, c = lane >> 4;
     const int64_t tiles_o = (p.M + RT * 16 - 1) / (RT * 16);
     const int64_t id = int64_t(blockIdx.y) * gridDim.x + blockIdx.x, tile = id / tiles_o, m0 = (id - tile * tiles_o) * (RT * 16);
-    Terms t{0, int(tile * (16 * TT)), int(min(int64_t(16 * TT), p.T - tile * (16 * TT)))};
-    if (GROUP ? !find_terms<16 * TT>(p, [&](int) { return int(tile); }, t) : t.n <= 0) return;
+    Terms t{0, int(tile * 16), int(min(int64_t(16), p.T - tile * 16))};
+    if (GROUP ? !find_terms<16>(p, [&](int) { return int(tile); }, t) : t.n <= 0) return;
     const int8_t* w = p.w + size_t(t.expert) * p.w_bytes;
-    const int8_t *wrow[RT], *xrow[TT];
+    const int8_t* wrow[RT];
 #pragma unroll
     for (int i = 0; i < RT; ++i) wrow[i] = w + min(m0 + i * 16 + r, p.M - 1) * p.ld;
+    const int64_t mine = t.first + min(r, t.n - 1);
+    const int8_t* xrow = p.x + (GROUP ? max(term_row(p, mine), int64_t(0)) : mine) * p.ld;
+    i32x4 acc[RT];
 #pragma unroll
-    for (int j = 0; j < TT; ++j) {
-        const int64_t term = t.first + min(j * 16 + r, t.n - 1);
-        xrow[j] = p.x + (GROUP ? max(term_row(p, term), int64_t(0)) : term) * p.ld;
-    }
-    i32x4 acc[RT][TT];
+    for (int i = 0; i < RT; ++i) acc[i] = i32x4{0, 0, 0, 0};
+    for (uint32_t k = wave * kRun; k < p.kb; k += WAVES * kRun) {
+        Frag a[kRun][RT], b[kRun];
 #pragma unroll
-    for (int i = 0; i < RT; ++i)
-#pragma unroll
-        for (int j = 0; j < TT; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
-    for (uint32_t k = wave * RUN; k < p.kb; k += WAVES * RUN) {
-        Frag a[RUN][RT], b[RUN][TT];
-#pragma unroll
-        for (int u = 0; u < RUN; ++u) {   // blocks past the last are read as the last and not used
+        for (int u = 0; u < kRun; ++u) {   // blocks past the last are read as the last and not used
             const uint32_t block = min(k + u, p.kb - 1);
 #pragma unroll
             for (int i = 0; i < RT; ++i) a[u][i].load(wrow[i], block, c);
-#pragma unroll
-            for (int j = 0; j < TT; ++j) b[u][j].load(xrow[j], block, c);
+            b[u].load(xrow, block, c);
         }
         asm volatile("" ::: "memory");   // all loads of the run before its first use
 #pragma unroll
-        for (int u = 0; u < RUN; ++u) {
+        for (int u = 0; u < kRun; ++u) {
             if (k + u >= p.kb) break;
 #pragma unroll
-            for (int i = 0; i < RT; ++i)
-#pragma unroll
-                for (int j = 0; j < TT; ++j) acc[i][j] = multiply(a[u][i], b[u][j], acc[i][j]);
+            for (int i = 0; i < RT; ++i) acc[i] = multiply(a[u][i], b[u], acc[i]);
         }
     }
+#pragma unroll
+    for (int i = 0; i < RT; ++i) *reinterpret_cast<i32x4*>(&part[wave][r][i * 16 + 4 * c]) = acc[i];
+    __syncthreads();
     // 16 terms x 16 RT outputs, 4 outputs to a thread
     constexpr int kAcross = RT * 4;
+    static_assert(WAVES * 64 >= 16 * kAcross, "a thread for every 4 outputs");
     const int m = tid % kAcross * 4, n = tid / kAcross;
-    const bool stores = n < 16 && m0 + m < p.M;
-    f32x4 sw = {0, 0, 0, 0};
-    if (stores) sw = *reinterpret_cast<const f32x4*>(reinterpret_cast<const char*>(w) + p.w_scales + (m0 + m) * 4);
+    if (n >= t.n || m0 + m >= p.M) return;
+    const f32x4 sw = *reinterpret_cast<const f32x4*>(reinterpret_cast<const char*>(w) + p.w_scales + (m0 + m) * 4);
+    i32x4 sum = *reinterpret_cast<const i32x4*>(&part[0][n][m]);
 #pragma unroll
-    for (int j = 0; j < TT; ++j) {
-        int (&mine)[WAVES][16][RT * 16 + 4] = part[j & 1];
+    for (int i = 1; i < WAVES; ++i) sum += *reinterpret_cast<const i32x4*>(&part[i][n][m]);
+    const int64_t term = t.first + n, row = GROUP ? term_row(p, term) : term;
+    const float sx = row < 0 ? __builtin_nanf("") : p.xs[row];
+    f32x4 v;
 #pragma unroll
-        for (int i = 0; i < RT; ++i) *reinterpret_cast<i32x4*>(&mine[wave][r][i * 16 + 4 * c]) = acc[i][j];
-        __syncthreads();
-        if (!stores || j * 16 + n >= t.n) continue;
-        i32x4 sum = *reinterpret_cast<const i32x4*>(&mine[0][n][m]);
-#pragma unroll
-        for (int i = 1; i < WAVES; ++i) sum += *reinterpret_cast<const i32x4*>(&mine[i][n][m]);
-        const int64_t term = t.first + j * 16 + n, row = GROUP ? term_row(p, term) : term;
-        const float sx = row < 0 ? __builtin_nanf("") : p.xs[row];
-        f32x4 v;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = int8_value(sum[i], sx, sw[i]);
-        const int64_t at = term * p.M + m0 + m;
-        if (p.ydt == SKETCH_F32)
-            store4_any<SKETCH_F32>(p.Y, at, v, m0 + m, p.M);
-        else if (p.ydt == SKETCH_BF16)
-            store4_any<SKETCH_BF16>(p.Y, at, v, m0 + m, p.M);
-        else
-            store4_any<SKETCH_F16>(p.Y, at, v, m0 + m, p.M);
-    }
+    for (int i = 0; i < 4; ++i) v[i] = int8_value(sum[i], sx, sw[i]);
+    const int64_t at = term * p.M + m0 + m;
+    if (p.ydt == SKETCH_F32)
+        store4_any<SKETCH_F32>(p.Y, at, v, m0 + m, p.M);
+    else if (p.ydt == SKETCH_BF16)
+        store4_any<SKETCH_BF16>(p.Y, at, v, m0 + m, p.M);
+    else
+        store4_any<SKETCH_F16>(p.Y, at, v, m0 + m, p.M);
 }
 
 // ---------------------------------------------------------------------------
@@ -451,7 +444,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(ONE ? 6 : 4
     extern __shared__ __attribute__((aligned(16))) uint8_t codes[];   // [min(16, T)][ld + 64]
     __shared__ uint32_t red[16];
     __shared__ __attribute__((aligned(16))) int part[8][16][20];
-    constexpr int RUN = 4, es = XD == SKETCH_F32 ? 4 : 2;
+    constexpr int es = XD == SKETCH_F32 ? 4 : 2;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r = lane & 15, c = lane >> 4, pitch = int(p.ld) + 64, chunks = int(p.ld / 8);
     const int64_t tiles_o = (p.M + 15) / 16, tile = GROUP ? blockIdx.x / tiles_o : 0;
@@ -460,10 +453,10 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(ONE ? 6 : 4
     if (GROUP && !find_terms<16>(p, [&](int) { return int(tile); }, t)) return;
     const int8_t* w = p.w + size_t(t.expert) * p.w_bytes;
     const int8_t* wrow = w + min(m0 + r, p.M - 1) * p.ld;
-    const uint32_t k0 = wave * RUN;
-    Frag a[RUN];
+    const uint32_t k0 = wave * kRun;
+    Frag a[kRun];
 #pragma unroll
-    for (int u = 0; u < RUN; ++u) a[u].load(wrow, min(k0 + u, p.kb - 1), c);
+    for (int u = 0; u < kRun; ++u) a[u].load(wrow, min(k0 + u, p.kb - 1), c);
     const float sw = reinterpret_cast<const float*>(reinterpret_cast<const char*>(w) + p.w_scales)[min(m0 + (tid & 15), p.M - 1)];
     asm volatile("" ::: "memory");   // on their way before X is asked for
 
@@ -527,13 +520,13 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(ONE ? 6 : 4
 
     i32x4 acc = {0, 0, 0, 0};
     const int8_t* xrow = reinterpret_cast<const int8_t*>(codes) + min(r, t.n - 1) * pitch;   // terms past the last are not stored
-    for (uint32_t k = k0; k < p.kb; k += 8 * RUN) {
+    for (uint32_t k = k0; k < p.kb; k += 8 * kRun) {
         if (k != k0) {
 #pragma unroll
-            for (int u = 0; u < RUN; ++u) a[u].load(wrow, min(k + u, p.kb - 1), c);
+            for (int u = 0; u < kRun; ++u) a[u].load(wrow, min(k + u, p.kb - 1), c);
         }
 #pragma unroll
-        for (int u = 0; u < RUN; ++u) {
+        for (int u = 0; u < kRun; ++u) {
             if (k + u >= p.kb) break;
             Frag b;
             b.load(xrow, k + u, c);
@@ -658,15 +651,15 @@ sketch_status make_plan(const sketch_int8_params* p, int64_t terms, int64_t x_ro
     return rc;
 }
 
-template <int WAVES, int RT, int TT, int RUN>
+template <int WAVES, int RT>
 sketch_status launch_rows(const Int8Product& a, hipStream_t st) {
-    const int64_t tiles = (a.T + 16 * TT - 1) / (16 * TT) + (a.counts ? min(a.T, int64_t(a.experts)) : 0);
+    const int64_t tiles = (a.T + 15) / 16 + (a.counts ? min(a.T, int64_t(a.experts)) : 0);
     dim3 grid;
     if (!grid_of((a.M + RT * 16 - 1) / (RT * 16) * tiles, WAVES * 64, &grid)) return SKETCH_EINVAL;
     if (a.counts)
-        int8_rows_kernel<true, WAVES, RT, TT, RUN><<<grid, WAVES * 64, 0, st>>>(a);
+        int8_rows_kernel<true, WAVES, RT><<<grid, WAVES * 64, 0, st>>>(a);
     else
-        int8_rows_kernel<false, WAVES, RT, TT, RUN><<<grid, WAVES * 64, 0, st>>>(a);
+        int8_rows_kernel<false, WAVES, RT><<<grid, WAVES * 64, 0, st>>>(a);
     return launch_status();
 }
 
@@ -736,8 +729,8 @@ sketch_status product(const sketch_int8_params* p, const void* buf, const void* 
     if (g) a.counts = g->counts, a.rows = g->rows, a.counts64 = g->counts_bits == 64, a.rows64 = g->rows_bits == 64;
     if (!plan.encode && x_dtype != SKETCH_INT8_ROWS)
         return launch_tokens(a, x_dtype, p->N, st);
-    if (plan.gemm.kind == kInt8Rows1) return launch_rows<8, 1, 1, 4>(a, st);
-    if (plan.gemm.kind == kInt8Rows2) return launch_rows<4, 2, 1, 4>(a, st);
+    if (plan.gemm.kind == kInt8Rows1) return launch_rows<8, 1>(a, st);
+    if (plan.gemm.kind == kInt8Rows2) return launch_rows<4, 2>(a, st);
     return launch_int8_gemm(a, plan.gemm, workspace, st);
 }
 

@@ -51,7 +51,8 @@ __device__ inline bool my_tile(const GemmArgs& a, int64_t& o0, Terms& t) {
 }
 
 // The scales of a tile: thread i loads that of output i, or of term i - ROWS, well
-// before the sums are there; they meet in LDS behind the waves' parts.
+// before the sums are there; they meet in LDS behind the waves' parts.  (Asked for where they are
+// used they cost a wait of two loads a tile: 28672 x 8192 at 2048 rows 374 -> 364 us.)
 template <int ROWS, int BT, bool GROUP>
 __device__ inline float tile_scale(const Int8Product& p, const Terms& t, int64_t o0) {
     const int i = threadIdx.x;
@@ -133,18 +134,27 @@ __device__ inline void store_tile(const Int8Product& p, const Terms& t, const i3
 }
 
 // ---------------------------------------------------------------------------
-// 32 FA outputs x 256 terms.  8 waves, two to a SIMD, each 16 FA x 64: 4 FA
-// accumulators of 16x16.  The waves work in two groups, one on each SIMD, half
-// a step apart: while one group runs the MFMAs of its step from registers, the
-// other reads its fragments from LDS.  Group g has the outputs 16 FA g .. of the
-// tile.  In phase 2k group 0 reads step k, in phase 2k + 1 group 1 does; each
-// multiplies in the phase after.
+// 32 FA outputs x 256 terms (FA 8, or 7 where that fills the last round).  8 waves,
+// two to a SIMD, each 16 FA x 64 by 16x16x64 MFMAs: 4 FA accumulators.  The waves work in two
+// groups, one on each SIMD, half a step apart: while one group runs the MFMAs of its
+// step from registers, the other reads its fragments from LDS, so the matrix
+// cores always have one wave's work and LDS the other's.  Group g has the outputs
+// 16 FA g .. of the tile.  In phase 2k group 0 reads step k, in phase 2k + 1 group
+// 1 does; each multiplies in the phase after.
+//
+// A wave's terms are strips of 16, 64 apart, so that a tile of few terms leaves out whole
+// strips, with their MFMAs and loads, and takes that much less (8 experts of 22016 x
+// 4096, 600 terms: 198 -> 178 us).
 //
 // Loads go out between the MFMAs.  What a load overwrites has to have been
 // read: group 0 loads its rows of W of step k + 2 in phase 2k + 1; group 1 its
 // own and X, which both read, in phase 2k + 2.  The loads of steps past the
 // last repeat it, into buffers that are done with, so that every phase has the
 // same number of loads to count.
+//
+// 28672 x 8192 at 2048 rows: 355 us, 2.71 POPS (the library's int8 product: 530 us).  Bound by the
+// card's power: the matrix cores are busy 65% to 68% of the cycles, at 1.9 of 2.4 GHz.
+// 32x32x32 MFMAs, with half the instructions, took 3% to 24% longer.
 // ---------------------------------------------------------------------------
 constexpr uint32_t kBigStage = 512 * 128;   // 32 FA rows of W in the first half, 256 of X in the second
 constexpr uint32_t kBigLds = 2 * kBigStage;
@@ -292,11 +302,17 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 }
 
 // ---------------------------------------------------------------------------
-// 32 FA outputs x up to 128 terms, 4 waves of 16 FA x 64, two workgroups to a CU,
+// 32 FA outputs x up to 32 FB terms, 4 waves of 16 FA x 16 FB, WGS workgroups to a CU,
 // which share its LDS: for fewer terms than the big kernel needs, down to those
-// whose time is the way of W from memory.  A wave's terms are strips of 16, 32
-// apart, so that a tile of few terms leaves out whole strips, with their loads, and
-// has LDS for more steps in flight instead.
+// whose time is the way of W from memory.  LDS holds as many steps of both
+// operands as fit, all but one of them on their way: no registers are tied up by
+// loads in flight, which is what operands straight to registers ran into (16 rows of 28672 x
+// 8192: 59 us in int8_rows_kernel, here 45, 5.2 TB/s).  A wave's terms are strips of
+// 16, 32 apart, so that a tile of few terms leaves out whole strips, with their loads, and
+// has LDS for more steps instead.  Tiles of 32 or 64 outputs x 64 terms with 4 workgroups to a
+// CU hide each other's beginnings and ends (two, with more steps each, were slower
+// almost everywhere); three steps of 128 x 128, which leave a CU one workgroup, took
+// 25% longer than two.
 // K is split over blockIdx.y when the tiles alone leave compute units
 // idle; the parts are the 32-bit sums, rows padded to 4 outputs, and
 // int8_add_kernel adds them.

@@ -26,7 +26,8 @@ def product(qx, sx, qw, sw, dtype):
 # M, N, rows: the smallest products found for each kind of tile and number of parts, for float32 or for 16 bits
 DENSE = [(67, 74, 18), (71, 72, 39), (87, 3528, 17), (65, 2811, 37), (75, 2618, 44), (163, 64, 1814), (7493, 72, 33),
          (97, 5361, 302), (103, 4153, 275), (17435, 440, 68), (1617, 5680, 74), (1741, 4686, 80), (2273, 923, 907),
-         (4759, 673, 391), (5873, 65, 1270), (8387, 68, 1275), (9269, 412, 1463), (19957, 143, 1378), (2304, 4096, 2048),
+         (4759, 673, 391), (5873, 65, 1270), (8387, 68, 1275), (9269, 412, 1463), (19957, 143, 1378), (18993, 199, 1524), (13811, 129, 2035),
+         (15183, 129, 1024), (12957, 106, 1275), (2304, 4096, 2048),
          (4096, 1024, 1537), (5000, 300, 2111)]
 
 
