@@ -28,6 +28,10 @@ __device__ inline void dma16_at(const int8_t* at, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(at), "s"(lds) : "memory", "m0");
 }
 
+// Until at most N loads are on their way, the latest ones.
+template <int N>
+__device__ inline void wait_until() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory"); }
+
 // Tile of a workgroup: its first output and its terms; false where it has none.
 template <int ROWS, int BT, bool GROUP>
 __device__ inline bool my_tile(const GemmArgs& a, int64_t& o0, Terms& t) {
@@ -247,7 +251,10 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
                 for (int i = 0; i < 2 * NJ; ++i) load_x(min(k, last), k, i);
             }
         }
-        wait_loads();
+        if (group == 0)   // step 0 is here
+            wait_until<kTurns>();
+        else
+            wait_until<kLoads>();
         barrier();
         if (group == 0) {
             for (uint32_t k = 0; k < p.kb; ++k) {
@@ -257,7 +264,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
                 compute([&](int n) {
                     if (n % 2 == 0 && n / 2 < kTurns) load_w(min(k + 2, last), k & 1, n / 2);
                 });
-                asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kTurns) : "memory");   // step k + 1 is here
+                wait_until<kTurns>();   // step k + 1 is here
                 barrier();
             }
             barrier();
@@ -328,9 +335,6 @@ template <int FA, int NJ, int WGS> constexpr int mid_steps_w() {
     constexpr int x = mid_steps_x<FA, NJ, WGS>();
     return x < 4 && (x * NJ + (x + 1) * FA) * 4096 <= int(mid_lds(WGS)) ? x + 1 : x;
 }
-
-template <int N>
-__device__ inline void wait_until() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory"); }
 
 template <int YD, int FA, int FB, int WGS, bool GROUP>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(WGS, WGS))) void int8_gemm_kernel(GemmArgs a) {
