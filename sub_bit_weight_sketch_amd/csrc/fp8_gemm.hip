@@ -20,7 +20,7 @@ struct GemmArgs {
 
 // Tile of a workgroup.
 __device__ inline void tile_of(const GemmArgs& a, uint32_t& to, uint32_t& tt) {
-    spread_tile(blockIdx.x, a.tiles_o, a.tiles_t, gridDim.x, to, tt);
+    spread_tile<8>(blockIdx.x, a.tiles_o, a.tiles_t, gridDim.x, to, tt);
 }
 
 // ---------------------------------------------------------------------------

@@ -33,12 +33,12 @@ __device__ inline uint32_t lds_address(const void* p) {
 }
 
 // Tile `block` of n = tiles_o * tiles_t.  Workgroups go round the 8 XCDs, so
-// each XCD gets a contiguous run of tiles; a run goes through groups of 8 token
+// each XCD gets a contiguous run of tiles; a run goes through groups of G token
 // tiles, so that the tiles in flight on an XCD share both operands in its L2.
+template <uint32_t G>
 __device__ inline void spread_tile(uint32_t block, uint32_t tiles_o, uint32_t tiles_t, uint32_t n, uint32_t& to, uint32_t& tt) {
     const uint32_t q = n / 8, rem = n % 8, xcd = block % 8;
     const uint32_t id = xcd * q + (xcd < rem ? xcd : rem) + block / 8;
-    constexpr uint32_t G = 8;
     const uint32_t g = id / (G * tiles_o), gt = min(G, tiles_t - g * G), in = id - g * G * tiles_o;
     to = in / gt;
     tt = g * G + in % gt;
