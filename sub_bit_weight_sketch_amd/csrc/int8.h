@@ -131,7 +131,7 @@ struct Int8Plan {
     size_t workspace;  // the parts of a split
 };
 
-// near: the place of every row of X in bytes fits 32 bits.  SKETCH_EINVAL when
+// near: terms that take rows of X in any order find each within 32 bits of bytes.  SKETCH_EINVAL when
 // there are more tiles than a grid holds.
 sketch_status int8_plan(int64_t M, int64_t T, uint32_t kb, int ydt, int experts, bool group, bool near, Int8Plan* g);
 sketch_status launch_int8_gemm(const Int8Product& p, const Int8Plan& g, void* ws, hipStream_t st);

@@ -645,7 +645,7 @@ sketch_status make_plan(const sketch_int8_params* p, int64_t terms, int64_t x_ro
     plan->encode = !rows && !encodes_itself(p->M, terms, plan->x.ld, int(matrices(p)), group);
     if (plan->encode) plan->workspace += plan->x.bytes;
     if (!plan->encode && !rows) return SKETCH_OK;   // encoded by the product's own workgroups
-    const bool near = x_rows * plan->x.ld <= int64_t(0xFFFFFFFF);
+    const bool near = !group || x_rows * plan->x.ld <= int64_t(0xFFFFFFFF);
     rc = int8_plan(p->M, terms, uint32_t(plan->w.ld / 128), y_dtype, int(matrices(p)), group, near, &plan->gemm);
     plan->workspace += plan->gemm.workspace;
     return rc;

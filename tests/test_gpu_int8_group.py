@@ -222,6 +222,28 @@ def test_experts_beyond_4_gib():
         assert not Y.any()
 
 
+def test_rows_of_x_beyond_4_gib():
+    """Terms whose rows of X lie past 2^32 bytes, few and many."""
+    R, N, M = 40000, 131071, 40
+    x = sk.Int8Tables(R, N, None, dev())
+    x.buf.zero_()
+    g = torch.Generator(device=dev()).manual_seed(3)
+    at = [0, 5, 32766, 32767, 32768, 39000, R - 1]
+    x.codes()[at] = torch.randint(-127, 128, (len(at), N), generator=g, device=dev(), dtype=torch.int8)
+    x.scales()[at] = torch.rand(len(at), generator=g, device=dev())
+    w = sk.int8_tables(torch.randint(-127, 128, (2, M, N), generator=g, device=dev(), dtype=torch.int8),
+                       torch.rand(2, M, generator=g, device=dev()))
+    for terms in (9, 300, 3000):
+        rows = torch.tensor([at[i * i % len(at)] for i in range(terms)], device=dev())
+        counts = [terms // 3, terms - terms // 3]
+        Y = sk.int8_matmul_group(w, x, torch.tensor(counts, device=dev()), rows=rows)
+        for e, a, b in u.spans(counts, terms):
+            r = rows[a:b]
+            total = torch.matmul(x.codes()[at].double(), w.codes()[e].double().t().contiguous()).float()
+            i = torch.tensor([at.index(v) for v in r.tolist()], device=dev())
+            assert torch.equal(Y[a:b], total[i] * x.scales()[r][:, None] * w.scales()[e]), terms
+
+
 # --------------------------------------------------------------------------
 # the operators together: a prompt through the experts of a layer
 # --------------------------------------------------------------------------
