@@ -616,9 +616,9 @@ struct Plan {
 // 5179 x 3673 8.5 us, 11.1 with a launch of its own; 28672 x 8192 44 and 49; 28616 x 1385 19
 // and 12.  2 to 16 rows, up to 16384 codes, where a compute unit has one workgroup at most, are
 // 20% faster to 20% slower (1376 x 2048, 4 rows 5.7 and 7.1; 4096 x 4096, 2 rows 11.6 and
-// 9.5), with more workgroups much slower (14601 x 356, 4 rows 18 and 7.4).  But a launch takes the
-// host 4.5 us, and calls this small among others wait for it (16 rows of 256 x 512
-// 12.1 and 7.3 us), so the border lies where one launch takes what the host takes for two.
+// 9.5), with more workgroups much slower (14601 x 356, 4 rows 18 and 7.4).  Those are
+// replays of a graph; launched one by one a second kernel costs 4.5 us (16 rows of 256 x 512 12.1
+// and 7.3 us), so the border lies where one launch takes what two of them take.
 bool encodes_itself(int64_t M, int64_t terms, int64_t ld, int experts, bool group) {
     if (terms > 16 * (group ? experts : 1)) return false;   // more than a tile of each
     const int64_t rows = min(terms, int64_t(16)), tiles = group ? (terms + 15) / 16 + min(terms, int64_t(experts)) : 1;
