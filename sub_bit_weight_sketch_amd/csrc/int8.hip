@@ -143,10 +143,13 @@ struct EncodeArgs {
     size_t scales_offset, bytes;
 };
 
-// SwiGLU of 8 elements in float32, and the least gate.  exp(-g) is a product in two
-// parts, so that the error is that of a few roundings (h: under 6e-7 of its size) for
-// gates from kLeastGate on; infinities and NaN show in h.
+// SwiGLU of 8 elements in float32, times 2^24, and the least gate.  exp(-g) is a product in
+// two parts, so that the error is that of a few roundings (h: under 6e-7 of its size) for
+// gates from kLeastGate on.  The factor, which the sum 1 + exp(-g) takes on its way, keeps
+// g / (1 + exp(-g)) of a subnormal gate normal: without it that quotient has lost its bits before
+// a large `up` makes it count.  Infinities, NaN and h from 2^104 on show in the result.
 constexpr float kLeastGate = -80.0f;
+constexpr float kDown = 5.9604644775390625e-8f;   // 2^-24
 
 __device__ inline void swiglu8(const float (&g)[8], const float (&u)[8], float (&h)[8], float& least) {
 #pragma unroll
@@ -155,7 +158,7 @@ __device__ inline void swiglu8(const float (&g)[8], const float (&u)[8], float (
         const float t = -g[e] * kLog2e;
         const float low = __builtin_fmaf(-g[e], kLog2e, -t) - g[e] * kLog2eLow;   // what t lacks
         const float ex = __builtin_amdgcn_exp2f(t) * __builtin_fmaf(low, 0.693147182f, 1.0f);
-        h[e] = g[e] * __builtin_amdgcn_rcpf(1.0f + ex) * u[e];
+        h[e] = g[e] * __builtin_amdgcn_rcpf(__builtin_fmaf(ex, kDown, kDown)) * u[e];
         least = fminf(least, g[e]);
     }
 }
@@ -220,8 +223,8 @@ __global__ __launch_bounds__(256) void int8_encode_kernel(EncodeArgs a) {
 // error is under 7.6e-5), float64 the others, one in 4000, for which gate and up are
 // read again; the largest magnitude is that of float64 among the elements within 2e-6
 // of the largest in float32.  Rows that float32 cannot hold (a gate below
-// kLeastGate, values past its range or in its last binade, where float64 may count
-// them as past it, or tiny ones throughout) are computed in float64.
+// kLeastGate, values from 2^104 on, or tiny ones throughout) are computed in float64,
+// which alone tells those past float32's range.
 // 2048 x 11008 bfloat16: 34 us, 3.3 TB/s; bound by its arithmetic, some 35
 // instructions an element, as much as by memory.  (Gate and up read three times, with
 // nothing kept: 57 us.)
@@ -243,7 +246,7 @@ __global__ __launch_bounds__(256) void int8_swiglu_kernel(EncodeArgs a) {
     auto umax = [](uint32_t x, uint32_t y) { return max(x, y); };
     auto dmax = [](double x, double y) { return x > y || x != x ? x : y; };   // NaN wins
     uint8_t* codes = a.buf + row * a.ld;
-    float h[K][8], least = 0.0f;
+    float h[K][8], least = 0.0f;   // h and its bits: of 2^24 h
     uint32_t bits = 0;
     Chunks<DT, K, L> gates, ups;
     gates.load(G, a.N, at);
@@ -269,7 +272,7 @@ __global__ __launch_bounds__(256) void int8_swiglu_kernel(EncodeArgs a) {
     }
     if (least < kLeastGate) bits = 0x7FFFFFFFu;
     bits = row_max<L>(bits, red, umax);
-    const bool whole = bits >= 0x7F000000u || bits < __float_as_uint(kTiny);   // 2^127 on
+    const bool whole = bits >= 0x7F800000u || bits < __float_as_uint(kTiny);
     double big = 0.0;
     auto larger = [&](int c, const float (&x)[8]) {
         const float near = __uint_as_float(bits) * (1.0f - 2e-6f);
@@ -298,7 +301,7 @@ __global__ __launch_bounds__(256) void int8_swiglu_kernel(EncodeArgs a) {
     const bool bad = !(big <= 3.4028234663852886e38);   // NaN too
     const double per = bad || big == 0.0 ? 1.0 : big;
     auto code = [&](double x) { return bad ? 0 : int(__builtin_rint(x * 127.0 / per)); };
-    const float inv = float(127.0 / per);
+    const float inv = float(127.0 * double(kDown) / per);   // of 2^24 h
     auto put = [&](int c, const float (&x)[8]) {
         int q[8];
         uint32_t unsure = 0;

@@ -46,3 +46,37 @@ def test_values_at_the_end_of_float32(N):
     t = sk.int8_swiglu(g.to(dev()), up.to(dev()), status=flags)
     assert torch.isnan(t.scales()).tolist() == [True, False, False] and int(flags) == sk.FLAG_WEIGHT_RANGE
     both_ways(g, up)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("N", [7, 300, 1000, 2048, 3001])
+def test_subnormal_gates(N, dt):
+    """Gates of 2^-149 to 2^-120 beside an `up` of 1e9 to 1e38, alone, with
+    ordinary elements of the same size as their product, and with larger ones."""
+    g = np.random.default_rng(N)
+    rows = []
+    for lo, hi, big in ((-149, -120, 1e38), (-149, -145, 1e20), (-149, -149, 1e38), (-140, -126, 1e30), (-128, -124, 1e9),
+                        (-149, -120, 1e9), (-133, -126, 3e38)):
+        for mixed in (0, 1, 2):
+            sign = g.choice([-1.0, 1.0], N)
+            a = sign * np.exp2(g.uniform(lo, hi, N)) * g.uniform(1, 2, N)
+            b = big * g.uniform(0.05, 1, N)
+            if mixed:                                            # every third element an ordinary one
+                size = 2.0 ** hi * big * (1 if mixed == 1 else 50)
+                ordinary = np.arange(N) % 3 == 1
+                a[ordinary] = g.uniform(0.2, 2, ordinary.sum())
+                b[ordinary] = size * g.uniform(0.05, 2, ordinary.sum())
+            rows.append((a, b))
+    gate, up = (torch.from_numpy(np.stack([r[i] for r in rows]).astype(np.float32)) for i in (0, 1))
+    gate, up = (v.to(torch.bfloat16) for v in (gate, up)) if dt == "bf16" else (gate, up)
+    both_ways(gate, up)
+
+
+def test_subnormal_gates_by_hand():
+    """Gates that differ in their last bits alone: 127 times their ratios."""
+    tiny = 2.0 ** -149
+    gate = torch.tensor([[3 * tiny, 4 * tiny, 0.0], [7 * tiny, 9 * tiny, 5 * tiny], [-tiny, 2 * tiny, -3 * tiny]])
+    up = torch.tensor([[2.0 ** 127, 2.0 ** 127, 1.0], [1e20, 0.8e20, 1e20], [3e38, 3e38, 3e38]])
+    t = sk.int8_swiglu(gate.to(dev()), up.to(dev()))
+    assert t.codes().tolist() == [[95, 127, 0], [123, 127, 88], [-42, 85, -127]]
+    both_ways(gate, up)
