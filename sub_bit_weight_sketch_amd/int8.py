@@ -126,16 +126,18 @@ class Int8Tables:
     """A matrix [M, N] (or a stack [count, M, N]) as int8 codes and a float32
     scale for each row, in the buffer layout of the C ABI (a uint8 device
     tensor).  Its values may be changed, its shape and buffer not: `params` and
-    `layout` are copies."""
+    `layout` are copies.  The products read the padding behind a row's N codes,
+    which has to be zero: a table made here starts as zeros, the padding of a
+    `buf` that is given is the caller's."""
 
-    def __init__(self, M, N, count=None, device="cuda", buf=None):
+    def __init__(self, M, N, count=None, device="cuda", buf=None, *, _zero=True):
         if count is not None and count < 1:
             raise ValueError("an empty stack of matrices")
         self._M, self._N, self._count = int(M), int(N), None if count is None else int(count)
         self._params, self._ref, self._layout = _shape(self._M, self._N, self._count or 1)
         n = (self._count or 1) * self._layout.bytes
         if buf is None:
-            self._codes = torch.empty(n, dtype=torch.int8, device=device)
+            self._codes = (torch.zeros if _zero else torch.empty)(n, dtype=torch.int8, device=device)
         else:
             _need(buf.dtype == torch.uint8 and buf.is_contiguous() and buf.numel() >= n and buf.data_ptr() % 16 == 0,
                   "the buffer must be %d dense, 16-byte aligned bytes" % n)
@@ -204,7 +206,7 @@ def int8_encode(W, check=True, status=None):
     _flags(status, W.device)
     dtype = dtype_code(W)
     W, ld = _rows_of(W)
-    t = Int8Tables(W.shape[-2], W.shape[-1], W.shape[0] if W.dim() == 3 else None, W.device)
+    t = Int8Tables(W.shape[-2], W.shape[-1], W.shape[0] if W.dim() == 3 else None, W.device, _zero=False)
     with _On(W.device) as stream:
         if check and status is None:
             status = torch.zeros(1, dtype=torch.int32, device=W.device)
@@ -235,7 +237,7 @@ def int8_swiglu(gate, up, status=None):
     dtype = dtype_code(gate)
     gate, ld_gate = _rows_of(gate)
     up, ld_up = _rows_of(up)
-    t = Int8Tables(*shape, None, device)
+    t = Int8Tables(*shape, None, device, _zero=False)
     with _On(device) as stream:
         rc = _int8_lib().sketch_int8_swiglu(t._ref, gate.data_ptr(), ld_gate, up.data_ptr(), ld_up, dtype, t._at,
                                             status.data_ptr() if status is not None else None, stream)
@@ -252,7 +254,6 @@ def int8_tables(codes, scales):
           "codes and scales must be tensors on one GPU, codes 2-D (or 3-D)")
     _need(scales.shape == codes.shape[:-1], "scales must have shape %s" % (tuple(codes.shape[:-1]),))
     t = Int8Tables(codes.shape[-2], codes.shape[-1], codes.shape[0] if codes.dim() == 3 else None, codes.device)
-    t.buf.zero_()
     t.codes().copy_(codes)
     t.scales().copy_(scales)
     return t
