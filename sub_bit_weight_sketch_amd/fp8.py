@@ -161,9 +161,11 @@ class Fp8Tables:
     """A matrix [M, N] (or a stack [count, M, N]) as e4m3 codes and block
     scales, in the buffer layout of the C ABI (a uint8 device tensor).  Its
     values may be changed, its shape and buffer not: `params` and `layout` are
-    copies."""
+    copies.  The products read the padding behind a row's codes and scales, which
+    has to be zero: a table made here starts as zeros, the padding of a `buf` that
+    is given is the caller's."""
 
-    def __init__(self, M, N, block_rows=128, count=None, device="cuda", buf=None):
+    def __init__(self, M, N, block_rows=128, count=None, device="cuda", buf=None, *, _zero=True):
         if count is not None and count < 1:
             raise ValueError("an empty stack of matrices")
         stack = 1 if count is None else int(count)
@@ -171,7 +173,7 @@ class Fp8Tables:
         self._params, self._ref, self._layout = _shape(self._M, self._N, self._block_rows, stack)
         n = stack * self._layout.bytes
         if buf is None:
-            buf = torch.empty(n, dtype=torch.uint8, device=device)
+            buf = (torch.zeros if _zero else torch.empty)(n, dtype=torch.uint8, device=device)
         else:
             _need(buf.dtype == torch.uint8 and buf.is_contiguous() and buf.numel() >= n and buf.data_ptr() % 16 == 0,
                   "the buffer must be %d dense, 16-byte aligned bytes" % n)
@@ -222,7 +224,8 @@ def fp8_encode(W, block_rows=128, check=True, status=None):
               "status must be an int32 tensor on W's device")
     dtype_code(W)
     W = _aligned(W)
-    t = Fp8Tables(W.shape[-2], W.shape[-1], block_rows, W.shape[0] if W.dim() == 3 else None, W.device)
+    t = Fp8Tables(W.shape[-2], W.shape[-1], block_rows, W.shape[0] if W.dim() == 3 else None, W.device,
+                  _zero=False)
     with _On(W.device) as stream:
         if check and status is None:
             status = torch.zeros(1, dtype=torch.int32, device=W.device)
@@ -248,7 +251,6 @@ def fp8_tables(codes, scales, block_rows=128):
     t = Fp8Tables(codes.shape[-2], codes.shape[-1], block_rows, count, codes.device)
     want = (t._layout.row_blocks, t._layout.col_blocks)
     _need(tuple(scales.shape) == (want if count is None else (count,) + want), "scales must have shape %s" % (want,))
-    t.buf.zero_()
     t._view(t.M, t.N, t._layout.ld, 0).copy_(codes)
     t.scales().copy_(scales)
     return t
