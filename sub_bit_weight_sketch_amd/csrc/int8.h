@@ -118,7 +118,7 @@ __device__ inline float int8_value(int sum, float sx, float sw) {
 // Which kernel a product takes, and over how many workgroups K is split.
 enum Int8Kind {
     kInt8Rows1,   // int8_rows_kernel (int8.hip), 16 outputs to 8 waves
-    kInt8Rows2,   // the same, 32 outputs to 4 waves
+    kInt8Rows2,   // the same, 32 outputs to 4 waves (groups alone)
     kInt8Mid,     // int8_gemm_kernel (int8_gemm.hip)
     kInt8Big      // int8_gemm_big_kernel
 };

@@ -655,15 +655,12 @@ sketch_status make_plan(const sketch_int8_params* p, int64_t terms, int64_t x_ro
     return rc;
 }
 
-template <int WAVES, int RT>
+template <bool GROUP, int WAVES, int RT>
 sketch_status launch_rows(const Int8Product& a, hipStream_t st) {
-    const int64_t tiles = (a.T + 15) / 16 + (a.counts ? min(a.T, int64_t(a.experts)) : 0);
+    const int64_t tiles = (a.T + 15) / 16 + (GROUP ? min(a.T, int64_t(a.experts)) : 0);
     dim3 grid;
     if (!grid_of((a.M + RT * 16 - 1) / (RT * 16) * tiles, WAVES * 64, &grid)) return SKETCH_EINVAL;
-    if (a.counts)
-        int8_rows_kernel<true, WAVES, RT><<<grid, WAVES * 64, 0, st>>>(a);
-    else
-        int8_rows_kernel<false, WAVES, RT><<<grid, WAVES * 64, 0, st>>>(a);
+    int8_rows_kernel<GROUP, WAVES, RT><<<grid, WAVES * 64, 0, st>>>(a);
     return launch_status();
 }
 
@@ -733,8 +730,8 @@ sketch_status product(const sketch_int8_params* p, const void* buf, const void* 
     if (g) a.counts = g->counts, a.rows = g->rows, a.counts64 = g->counts_bits == 64, a.rows64 = g->rows_bits == 64;
     if (!plan.encode && x_dtype != SKETCH_INT8_ROWS)
         return launch_tokens(a, x_dtype, p->N, st);
-    if (plan.gemm.kind == kInt8Rows1) return launch_rows<8, 1>(a, st);
-    if (plan.gemm.kind == kInt8Rows2) return launch_rows<4, 2>(a, st);
+    if (plan.gemm.kind == kInt8Rows1) return g ? launch_rows<true, 8, 1>(a, st) : launch_rows<false, 8, 1>(a, st);
+    if (plan.gemm.kind == kInt8Rows2) return launch_rows<true, 4, 2>(a, st);   // groups alone
     return launch_int8_gemm(a, plan.gemm, workspace, st);
 }
 

@@ -552,13 +552,13 @@ Int8Plan choose_group(int64_t M, int64_t T, double kb, int experts, double out_m
     return best.plan;
 }
 
-Int8Plan choose(int64_t M, int64_t T, uint32_t kb, double out_mb, bool near) {
+Int8Plan choose(int64_t M, int64_t T, uint32_t kb, double out_mb) {
     const int64_t ncu = compute_units();
     const double mb = 128e-6 * double(M) * double(kb);
     Best best;
     for (const TileCost& c : kCost) {
         const bool big = c.fb == 8;
-        if (big && (!near || T <= 64)) continue;
+        if (big && T <= 64) continue;
         const int64_t across = (M + 32 * c.fa - 1) / (32 * c.fa), bt = 32 * c.fb, down = (T + bt - 1) / bt, strip = big ? 64 : 32;
         for (int64_t n = 1; n <= kMaxSplits; ++n) {
             if (n > 1 && (big || 2 * n > int64_t(kb) || across * down * n > 4 * ncu || T > 65535)) break;   // T: a grid's second dimension
@@ -613,7 +613,7 @@ sketch_status launch(const GemmArgs& a, const Int8Plan& g, hipStream_t st) {
 
 sketch_status int8_plan(int64_t M, int64_t T, uint32_t kb, int ydt, int experts, bool group, bool near, Int8Plan* g) {
     const double out_mb = 1e-6 * double(T) * double(M) * double(elem_bytes(ydt));
-    *g = group ? choose_group(M, T, kb, experts, out_mb, near) : choose(M, T, kb, out_mb, near);
+    *g = group ? choose_group(M, T, kb, experts, out_mb, near) : choose(M, T, kb, out_mb);
     if (g->kind == kInt8Rows1 || g->kind == kInt8Rows2) return SKETCH_OK;   // their launch counts its own workgroups
     const int64_t rows = 32 * g->fa, cols = 32 * g->fb;
     g->tiles_o = (M + rows - 1) / rows;
