@@ -631,9 +631,10 @@ bool encodes_itself(int64_t M, int64_t terms, int64_t ld, int experts, bool grou
     return rows * ld <= int64_t(kTokenCodes / 2) && groups <= ncu;
 }
 
-// Checks the parameters and fills the plan.
+// Checks the parameters and fills the plan.  any_order: terms may take any rows of X.  The
+// workspace does not depend on it (groups have no parts).
 sketch_status make_plan(const sketch_int8_params* p, int64_t terms, int64_t x_rows, int x_dtype, int y_dtype,
-                        bool group, Plan* plan) {
+                        bool group, bool any_order, Plan* plan) {
     sketch_status rc = int8_shape(p, &plan->w);
     if (rc != SKETCH_OK) return rc;
     const bool rows = x_dtype == SKETCH_INT8_ROWS;
@@ -649,7 +650,7 @@ sketch_status make_plan(const sketch_int8_params* p, int64_t terms, int64_t x_ro
     plan->encode = !rows && !encodes_itself(p->M, terms, plan->x.ld, int(matrices(p)), group);
     if (plan->encode) plan->workspace += plan->x.bytes;
     if (!plan->encode && !rows) return SKETCH_OK;   // encoded by the product's own workgroups
-    const bool near = !group || x_rows * plan->x.ld <= int64_t(0xFFFFFFFF);
+    const bool near = !any_order || x_rows * plan->x.ld <= int64_t(0xFFFFFFFF);
     rc = int8_plan(p->M, terms, uint32_t(plan->w.ld / 128), y_dtype, int(matrices(p)), group, near, &plan->gemm);
     plan->workspace += plan->gemm.workspace;
     return rc;
@@ -688,9 +689,9 @@ sketch_status product(const sketch_int8_params* p, const void* buf, const void* 
                       int64_t terms, const sketch_int8_groups* g, void* Y, int y_dtype, void* workspace,
                       size_t workspace_bytes, void* stream) {
     Plan plan;
-    sketch_status rc = make_plan(p, terms, x_rows, x_dtype, y_dtype, g != nullptr, &plan);
-    if (rc != SKETCH_OK) return rc;
     const bool index = g && g->rows;
+    sketch_status rc = make_plan(p, terms, x_rows, x_dtype, y_dtype, g != nullptr, index, &plan);
+    if (rc != SKETCH_OK) return rc;
     if (g && ((g->counts_bits != 32 && g->counts_bits != 64) || (index && g->rows_bits != 32 && g->rows_bits != 64)))
         return SKETCH_EINVAL;
     if (terms == 0 || p->M == 0) return SKETCH_OK;
@@ -793,7 +794,7 @@ sketch_status sketch_int8_swiglu(const sketch_int8_params* p, const void* gate, 
 sketch_status sketch_int8_workspace_bytes(const sketch_int8_params* p, int64_t batch, int x_dtype, int y_dtype,
                                           size_t* bytes) {
     Plan plan;
-    const sketch_status rc = make_plan(p, batch, batch, x_dtype, y_dtype, false, &plan);
+    const sketch_status rc = make_plan(p, batch, batch, x_dtype, y_dtype, false, false, &plan);
     if (rc != SKETCH_OK) return rc;
     if (!bytes) return SKETCH_EINVAL;
     *bytes = plan.workspace;
@@ -809,7 +810,7 @@ sketch_status sketch_int8_matmul(const sketch_int8_params* p, const void* buf, c
 sketch_status sketch_int8_group_workspace_bytes(const sketch_int8_params* p, int64_t terms, int64_t x_rows,
                                                 int x_dtype, int y_dtype, size_t* bytes) {
     Plan plan;
-    const sketch_status rc = make_plan(p, terms, x_rows, x_dtype, y_dtype, true, &plan);
+    const sketch_status rc = make_plan(p, terms, x_rows, x_dtype, y_dtype, true, true, &plan);
     if (rc != SKETCH_OK) return rc;
     if (!bytes) return SKETCH_EINVAL;
     *bytes = plan.workspace;
