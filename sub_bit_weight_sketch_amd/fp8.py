@@ -256,11 +256,23 @@ def fp8_tables(codes, scales, block_rows=128):
     return t
 
 
+_SIZES = 1024               # workspace sizes that a table remembers
+
+
+def _remember(sizes, key, n):
+    """n, kept in `sizes`, which starts anew once it is full: a program meets any
+    number of batch sizes as it runs."""
+    if len(sizes) >= _SIZES:
+        sizes.clear()
+    sizes[key] = n
+    return n
+
+
 def _workspace_bytes(t, batch, x_dtype, y_dtype):
     key = (batch, x_dtype, y_dtype)
     n = t._ws.get(key)
     if n is None:
-        n = t._ws[key] = sketch_fp8_workspace_bytes(t._params, batch, x_dtype, y_dtype)
+        n = _remember(t._ws, key, sketch_fp8_workspace_bytes(t._params, batch, x_dtype, y_dtype))
     return n
 
 

@@ -13,7 +13,7 @@ import functools
 import torch
 
 from . import OK, SketchError, _check, _ptr, _stream_handle, dtype_code, lib, sketch_encode_status
-from .fp8 import _aligned, _given, _need, _On, _out, _shared
+from .fp8 import _aligned, _given, _need, _On, _out, _remember, _shared
 
 INT8_ROWS = 4               # x_dtype of rows that an encoder wrote
 INT8_TOKENS = 16            # rows that a product may encode as it reads them
@@ -263,7 +263,7 @@ def _workspace_bytes(t, batch, x_dtype, y_dtype):
     key = (batch, x_dtype, y_dtype)
     n = t._ws.get(key)
     if n is None:
-        n = t._ws[key] = sketch_int8_workspace_bytes(t._params, batch, x_dtype, y_dtype)
+        n = _remember(t._ws, key, sketch_int8_workspace_bytes(t._params, batch, x_dtype, y_dtype))
     return n
 
 
@@ -271,7 +271,7 @@ def _group_workspace_bytes(t, terms, x_rows, x_dtype, y_dtype):
     key = (terms, x_rows, x_dtype, y_dtype)
     n = t._ws.get(key)
     if n is None:
-        n = t._ws[key] = sketch_int8_group_workspace_bytes(t._params, terms, x_rows, x_dtype, y_dtype)
+        n = _remember(t._ws, key, sketch_int8_group_workspace_bytes(t._params, terms, x_rows, x_dtype, y_dtype))
     return n
 
 
