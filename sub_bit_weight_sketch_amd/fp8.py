@@ -322,10 +322,10 @@ def fp8_matmul(t, X, out=None, workspace=None, dtype=None, float32_sums=False):
     shape, device = X.shape, t._device
     if X.device != device:
         raise ValueError("X and the weight are on different devices")
+    if len(shape) not in (1, 2) or shape[-1] != t._N:
+        raise ValueError("X must have %d columns, got shape %s" % (t._N, tuple(shape)))
     squeeze = len(shape) == 1
     batch = 1 if squeeze else shape[0]
-    if len(shape) > 2 or shape[-1] != t._N:
-        raise ValueError("X must have %d columns, got shape %s" % (t._N, tuple(shape)))
     if rows:
         xdt, at = FP8_ROWS, X._at
     else:

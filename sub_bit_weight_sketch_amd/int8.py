@@ -312,10 +312,10 @@ def int8_matmul(t, X, out=None, workspace=None, dtype=None):
     if t._count is not None:
         raise ValueError("t must be one weight")
     shape = X.shape
+    if len(shape) not in (1, 2) or shape[-1] != t._N:
+        raise ValueError("X must have %d columns, got shape %s" % (t._N, tuple(shape)))
     squeeze = len(shape) == 1
     batch = 1 if squeeze else shape[0]
-    if len(shape) > 2 or shape[-1] != t._N:
-        raise ValueError("X must have %d columns, got shape %s" % (t._N, tuple(shape)))
     xdt, x = _operand(t, X)
     device = t._device
     if xdt == INT8_ROWS:
