@@ -6,7 +6,9 @@
  * 8-bit integers with a scale for each output channel ("Resumen Técnico",
  * Metodología §2 and §5: layers differ in how much compression they tolerate),
  * and for mixture-of-experts prompts, whose tokens stand in groups of any size,
- * one for each expert.  The conventions of sketch.h hold (device pointers,
+ * one for each expert.  Serving only: no gradients.  Sketched linears and the
+ * e4m3 experts of sketch_fp8.h are not taken; the order of the terms and the
+ * weighted sum by token are the caller's.  The conventions of sketch.h hold (device pointers,
  * caller-owned memory, 16-byte alignment unless said otherwise, asynchronous on
  * the caller's stream, nothing allocated, host-side checks before anything is
  * enqueued, safe under HIP graph capture).
@@ -138,8 +140,9 @@ sketch_status sketch_int8_group_workspace_bytes(const sketch_int8_params* p, int
  * sketch_int8_matmul.
  *   buf      the experts' encoded weights (count of them, up to
  *            SKETCH_INT8_MAX_EXPERTS).
- *   X        [x_rows][N] of x_dtype, or SKETCH_INT8_ROWS, as above.  Each row is
- *            encoded once.  Without g->rows, x_rows >= terms.
+ *   X        [x_rows][N] of x_dtype, or SKETCH_INT8_ROWS, as above.  A row has
+ *            one set of codes, whichever terms take it.  Without g->rows,
+ *            x_rows >= terms.
  *   Y        [terms][M] of y_dtype.  Rows behind the last term of the last
  *            expert are left as they were.
  * The counts are read on the device, so routing needs no wait of the host.  A

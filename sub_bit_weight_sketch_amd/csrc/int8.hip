@@ -168,7 +168,7 @@ __device__ inline double swiglu64(float g, float u) { return double(g) / (1.0 + 
 // One row to L lanes (a workgroup of 256 has 256 / L rows), 8 elements to a
 // lane at a time; kKept such chunks of a lane stay in registers between the
 // maximum and the rounding, what a longer row has more is read again.
-// HBM-bound: 28672 x 8192 bfloat16 126 us, 5.6 TB/s.
+// HBM-bound: 28672 x 8192 bfloat16 126 us, 5.6 TB/s (vector units busy 84% of the cycles).
 constexpr int kKept = 4;
 
 template <int DT, int L>
@@ -225,9 +225,9 @@ __global__ __launch_bounds__(256) void int8_encode_kernel(EncodeArgs a) {
 // of the largest in float32.  Rows that float32 cannot hold (a gate below
 // kLeastGate, values from 2^104 on, or tiny ones throughout) are computed in float64,
 // which alone tells those past float32's range.
-// 2048 x 11008 bfloat16: 34 us, 3.3 TB/s; bound by its arithmetic, some 35
-// instructions an element, as much as by memory.  (Gate and up read three times, with
-// nothing kept: 57 us.)
+// 2048 x 11008 bfloat16: 34 us, 3.4 TB/s.  Bound by neither alone: 36 instructions an
+// element keep the vector units busy 68% of the cycles, and a workgroup's loads and arithmetic
+// follow one another.  (Gate and up read three times, with nothing kept: 57 us.)
 template <int DT, int L, int K>
 __global__ __launch_bounds__(256) void int8_swiglu_kernel(EncodeArgs a) {
     __shared__ uint32_t red[4];

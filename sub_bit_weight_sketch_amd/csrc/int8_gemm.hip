@@ -159,8 +159,9 @@ __device__ inline void store_tile(const Int8Product& p, const Terms& t, const i3
 // last repeat it, into buffers that are done with, so that every phase has the
 // same number of loads to count.
 //
-// 28672 x 8192 at 2048 rows: 355 us, 2.71 POPS (the library's int8 product: 530 us).  Bound by the
-// card's power: the matrix cores are busy 65% to 68% of the cycles, at 1.9 of 2.4 GHz.
+// 28672 x 8192 at 2048 rows: 370 us (350 to 395 from run to run), 2.6 POPS (the library's int8
+// product: 530 us).  Bound by the card's power: the matrix cores are busy 72% of the cycles, at
+// 1.8 of 2.4 GHz.
 // 32x32x32 MFMAs, with half the instructions, took 3% to 24% longer.
 // ---------------------------------------------------------------------------
 constexpr uint32_t kBigStage = 512 * 128;   // 32 FA rows of W in the first half, 256 of X in the second

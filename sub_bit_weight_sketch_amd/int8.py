@@ -355,8 +355,8 @@ def int8_matmul_group(t, X, counts, rows=None, out=None, workspace=None, dtype=N
     the order of their experts, counts[e] of them for expert e (int32 or int64
     [E] on the device: nothing waits for the host).  Term i takes row rows[i] of
     X [x_rows, N] (int32 or int64 [terms]; a row outside X gives NaN), or row i
-    without `rows`.  X is encoded row by row on the way in, each row once, or is
-    the Int8Tables of encoded rows.  dtype: of Y, float32 (the default, or that
+    without `rows`.  X is encoded row by row on the way in, or is the Int8Tables
+    of encoded rows.  dtype: of Y, float32 (the default, or that
     of `out`), bfloat16 or float16.  Rows of Y behind the last term are left as
     they were (an `out` that is not given holds anything there).  `out` may share
     memory with X (a copy is made), not with the weights or with encoded rows."""
