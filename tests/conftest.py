@@ -8,3 +8,17 @@ if ROOT not in sys.path:
 
 def pytest_configure(config):
     config.addinivalue_line("markers", "gpu: needs an MI355X (gfx950) GPU and the built HIP library")
+
+
+def pytest_collection_modifyitems(config, items):
+    """The tests of buffers that share memory let calls that are not refused go on to
+    their launch, on addresses that hold nothing.  Without a GPU that launch fails;
+    on one it would fault."""
+    import pytest
+    import torch
+
+    if torch.cuda.device_count() == 0:
+        return
+    for item in items:
+        if os.path.basename(str(item.fspath)).endswith("_host_overlap.py"):
+            item.add_marker(pytest.mark.skip(reason="launches on made-up addresses: only where there is no GPU"))
