@@ -500,7 +500,7 @@ __global__ __launch_bounds__(256) void int8_add_kernel(GemmArgs a) {
 // (37%).  Tiles of 128 x 128, unsplit or split as is best, in place of the set: 28% and 16%.
 // The tiles of 256 terms were fitted to 477 large products of one weight; those of 224 outputs fill
 // the last round where those of 256 leave it half empty (28672 x 8192 at 2048 rows: 1024
-// tiles are 4 rounds, 896 are 3.5; 355 and 375 us) and save 4% of these on average.
+// tiles are 4 rounds, 896 are 3.5; 355 and 375 us in one run) and save 4% of these on average.
 struct TileCost {
     int fa, fb;   // outputs and terms of a tile in units of 32
     double call, step, round_step, round, tile_step, strip_step, strip, parts, part_mb, mb, out_mb;   // one weight
